@@ -16,6 +16,8 @@
  * pa_reshape_and_cache_int8 / pa_decode_int8 / pa_decode_write_int8 are the
  * write, the decode and the step over INT8 pools, the _fp8 calls the same
  * over FP8 (E4M3) pools; pa_copy_blocks copies whole blocks (copy-on-write).
+ * pa_build_tables forms a step's block tables, slots and cumulative lengths
+ * from request lengths.
  *
  * Sources (web pages on paged KV caches, cited by page and section):
  *   [SKILL] cannbot-skills "model-infer-kvcache" skill page: §3.1 physical
@@ -98,6 +100,7 @@ typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1 } pa_dtype;
 #define PA_DEVERR_CONTEXT 8    /* context_len < 0, > capacity or > host hint  */
 #define PA_DEVERR_TIMEOUT 16   /* a bounded pipeline wait gave up             */
 #define PA_DEVERR_SCALE 32     /* an 8-bit pool's scale not positive finite   */
+#define PA_DEVERR_NO_BLOCKS 64 /* the free list is too short for the step     */
 
 /* ABI version the library was built with (PA_ABI_VERSION). */
 int32_t pa_abi_version(void);
@@ -508,6 +511,63 @@ pa_status pa_decode_write_fp8(void *out, int64_t out_row_stride, const void *que
 pa_status pa_copy_blocks(void *key_cache, void *value_cache, int64_t block_bytes,
                          int64_t num_blocks, const int64_t *block_mapping,
                          int32_t num_pairs, int32_t *d_error, void *stream);
+
+/*
+ * pa_build_tables -- a serving step's metadata from request lengths.
+ *
+ * Defines ([SKILL] §3.1-3.3 logical mapping and slot_mapping; [LQNN] §3.1
+ * cu_seqlens): request b of num_seqs holds c = context_lens[b] cached tokens
+ * and gets n = query_lens[b] new ones.  With bs = block_size,
+ *     have = ceil(c / bs), need = ceil((c + n) / bs), take = need - have,
+ * the request keeps its block table entries 0 .. have - 1 and takes `take`
+ * blocks off the END of the free list, requests in order, so
+ *     block_table[b][have + i] = free_blocks[F - 1 - taken_before_b - i],
+ *     cu_seqlens_q[b + 1]      = cu_seqlens_q[b] + n,   cu_seqlens_q[0] = 0,
+ * and its new token i, at t = cu_seqlens_q[b] + i, has
+ *     positions[t]    = c + i,
+ *     slot_mapping[t] = block_table[b][(c + i) / bs] * bs + (c + i) % bs.
+ * context_lens_out[b] = c + n (the length the attention calls take) and
+ * *num_free_out = F - (blocks taken).  Tokens t >= cu_seqlens_q[num_seqs] (a
+ * step padded to a fixed token count) get slot -1 and position 0.
+ *
+ *   block_table       int32 [num_seqs, block_table_stride], in and out: only
+ *                     the entries of newly taken blocks are written.
+ *   context_lens,
+ *   query_lens        int32 [num_seqs].
+ *   free_blocks       int32 [free_capacity]; the first F = *num_free entries
+ *                     are free block ids.  Only read: the step's blocks are
+ *                     off the list once the caller takes *num_free_out for
+ *                     the list's length.
+ *   context_lens_out  int32 [num_seqs];  cu_seqlens_q  int32 [num_seqs + 1].
+ *   slot_mapping      int64 [max_tokens];
+ *   positions         int32 [max_tokens], nullable.
+ *   num_free_out      int32 [1].
+ * No output may overlap an input (PA_ERR_SHAPE where context_lens_out or
+ * num_free_out does); the same inputs give the same outputs again.
+ *
+ * A request that cannot be served takes no blocks, its tokens get slot -1 and
+ * its context_lens_out is 0 (its cached tokens stay where they are; the
+ * caller still has their number in context_lens):
+ *     c < 0, n < 0 or c + n > max_blocks_per_seq * bs: PA_DEVERR_CONTEXT, and
+ *         it counts as n = 0 in cu_seqlens_q;
+ *     its tokens end past max_tokens: PA_DEVERR_CU_SEQLENS;
+ *     the list does not hold the blocks that it and the requests before it
+ *         take: PA_DEVERR_NO_BLOCKS (later requests that need no block are
+ *         still served).  F < 0 or > free_capacity sets it too, and F is
+ *         clamped.
+ * A block id outside [0, num_blocks) among a served request's blocks sets
+ * PA_DEVERR_BLOCK_ID; the tokens of that block get slot -1, and a taken
+ * block's entry is written as -1.
+ * Requirements: block_size 8, 16, 32, 64 or 128.
+ */
+pa_status pa_build_tables(int32_t *block_table, int64_t block_table_stride,
+                          int32_t max_blocks_per_seq, const int32_t *context_lens,
+                          const int32_t *query_lens, const int32_t *free_blocks,
+                          const int32_t *num_free, int32_t free_capacity,
+                          int32_t *context_lens_out, int32_t *cu_seqlens_q,
+                          int64_t *slot_mapping, int32_t *positions, int32_t *num_free_out,
+                          int32_t num_seqs, int32_t max_tokens, int32_t block_size,
+                          int64_t num_blocks, int32_t *d_error, void *stream);
 
 #ifdef __cplusplus
 }

@@ -13,6 +13,8 @@ first call raises.
     pa_reshape_and_cache_int8, pa_decode_int8, pa_decode_write_int8 (and _fp8)
                           the write, decode and step over INT8 (FP8 E4M3) pools
     pa_copy_blocks        copy whole blocks of both pools (copy-on-write)
+    pa_build_tables       a step's block tables, slots, positions and cumulative
+                          lengths from request lengths
 
 Build the library with ``python -m paged_kv_cache_34_gb300.build``.
 """
@@ -27,15 +29,17 @@ import torch
 __all__ = ["pa_reshape_and_cache", "pa_decode", "pa_decode_plan", "pa_decode_write",
            "pa_prefill_varlen", "pa_reshape_and_cache_int8", "pa_decode_int8",
            "pa_decode_write_int8", "pa_reshape_and_cache_fp8", "pa_decode_fp8",
-           "pa_decode_write_fp8", "pa_copy_blocks", "PaError",
+           "pa_decode_write_fp8", "pa_copy_blocks", "pa_build_tables", "PaError",
            "library", "DEVERR_SLOT", "DEVERR_BLOCK_ID", "DEVERR_CU_SEQLENS",
-           "DEVERR_CONTEXT", "DEVERR_TIMEOUT", "DEVERR_SCALE", "LIB_PATH"]
+           "DEVERR_CONTEXT", "DEVERR_TIMEOUT", "DEVERR_SCALE", "DEVERR_NO_BLOCKS",
+           "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpa.so")
 
 # Device error bits (include/pa.h PA_DEVERR_*).
 DEVERR_SLOT, DEVERR_BLOCK_ID, DEVERR_CU_SEQLENS, DEVERR_CONTEXT, DEVERR_TIMEOUT = 1, 2, 4, 8, 16
 DEVERR_SCALE = 32
+DEVERR_NO_BLOCKS = 64
 
 _STATUS = {0: "PA_OK", 1: "PA_ERR_NULL", 2: "PA_ERR_SHAPE", 3: "PA_ERR_UNSUPPORTED",
            4: "PA_ERR_ALIGN", 5: "PA_ERR_WORKSPACE", 6: "PA_ERR_CUDA"}
@@ -93,6 +97,9 @@ def library(path: str | None = None):
         lib.pa_reshape_and_cache_int8.restype = c.c_int
         lib.pa_copy_blocks.argtypes = [V, V, I64, I64, V, I32, V, V]
         lib.pa_copy_blocks.restype = c.c_int
+        lib.pa_build_tables.argtypes = [V, I64, I32, V, V, V, V, I32, V, V, V, V, V, I32, I32,
+                                        I32, I64, V, V]
+        lib.pa_build_tables.restype = c.c_int
         lib.pa_decode_int8.argtypes = [V, I64, V, I64, V, V, V, I64, I32, V, I32, I32, I32,
                                        I32, I32, I64, V, V, F, I32, I32, V, SZ, c.c_int, V, V]
         lib.pa_decode_int8.restype = c.c_int
@@ -230,6 +237,63 @@ def pa_copy_blocks(key_cache, value_cache, block_mapping, *, d_error=None, strea
                             _ptr(block_mapping), block_mapping.numel() // 2, _ptr(d_error),
                             _stream(stream))
     _check(lib, st, "pa_copy_blocks")
+
+
+def _on_device(where, **tensors):
+    """Every tensor given is on the current CUDA device (where the kernel is
+    launched) -- a pointer of another device, or of the host, would fault."""
+    cur = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != cur:
+            raise ValueError(f"{where}: {name} is not on the current CUDA device ({cur})")
+
+
+def _vector(t, n, dtype, name):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values".replace(
+            "torch.", ""))
+
+
+def pa_build_tables(block_table, context_lens, query_lens, free_blocks, num_free,
+                    context_lens_out, cu_seqlens_q, slot_mapping, num_free_out, *, block_size,
+                    num_blocks, positions=None, d_error=None, stream=None, lib=None):
+    """A serving step's metadata from request lengths: request b holds
+    context_lens[b] cached tokens and gets query_lens[b] new ones (int32 [S]).
+    Writes context_lens_out int32 [S], cu_seqlens_q int32 [S+1], slot_mapping
+    int64 [T] and positions int32 [T] (entries past the step's tokens get -1
+    and 0), the block_table (int32 [S, max_blocks]) entries of the blocks
+    taken off the end of free_blocks[:num_free], and num_free_out int32 [1].
+    No output may overlap an input."""
+    lib = lib or library()
+    s, t = context_lens.shape[0], slot_mapping.shape[0]
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != s \
+            or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [num_seqs, max_blocks] with contiguous rows")
+    _vector(context_lens, s, torch.int32, "context_lens")
+    _vector(query_lens, s, torch.int32, "query_lens")
+    _vector(free_blocks, free_blocks.shape[0], torch.int32, "free_blocks")
+    _vector(num_free, 1, torch.int32, "num_free")
+    _vector(context_lens_out, s, torch.int32, "context_lens_out")
+    _vector(cu_seqlens_q, s + 1, torch.int32, "cu_seqlens_q")
+    _vector(slot_mapping, t, torch.int64, "slot_mapping")
+    _vector(num_free_out, 1, torch.int32, "num_free_out")
+    if positions is not None:
+        _vector(positions, t, torch.int32, "positions")
+    _on_device("pa_build_tables", block_table=block_table, context_lens=context_lens,
+               query_lens=query_lens, free_blocks=free_blocks, num_free=num_free,
+               context_lens_out=context_lens_out, cu_seqlens_q=cu_seqlens_q,
+               slot_mapping=slot_mapping, positions=positions, num_free_out=num_free_out,
+               d_error=d_error)
+    stride = block_table.stride(0) if s > 1 else block_table.shape[1]
+    st = lib.pa_build_tables(block_table.data_ptr(), stride, block_table.shape[1],
+                             context_lens.data_ptr(), query_lens.data_ptr(),
+                             free_blocks.data_ptr(), num_free.data_ptr(), free_blocks.shape[0],
+                             context_lens_out.data_ptr(), cu_seqlens_q.data_ptr(),
+                             slot_mapping.data_ptr(),
+                             None if positions is None else positions.data_ptr(),
+                             num_free_out.data_ptr(), s, t, block_size, num_blocks,
+                             None if d_error is None else d_error.data_ptr(), _stream(stream))
+    _check(lib, st, "pa_build_tables")
 
 
 def pa_debug_set_wait_limit_ns(ns: int, *, lib=None):

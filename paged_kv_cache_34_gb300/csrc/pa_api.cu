@@ -282,6 +282,64 @@ pa_status pa_copy_blocks(void *key_cache, void *value_cache, int64_t block_bytes
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
+pa_status pa_build_tables(int32_t *block_table, int64_t block_table_stride,
+                          int32_t max_blocks_per_seq, const int32_t *context_lens,
+                          const int32_t *query_lens, const int32_t *free_blocks,
+                          const int32_t *num_free, int32_t free_capacity,
+                          int32_t *context_lens_out, int32_t *cu_seqlens_q,
+                          int64_t *slot_mapping, int32_t *positions, int32_t *num_free_out,
+                          int32_t num_seqs, int32_t max_tokens, int32_t block_size,
+                          int64_t num_blocks, int32_t *d_error, void *stream) {
+  if (num_seqs < 0 || max_tokens < 0 || max_blocks_per_seq < 0 || free_capacity < 0 ||
+      num_blocks < 0 || block_size <= 0)
+    return PA_ERR_SHAPE;
+  if (block_table_stride < max_blocks_per_seq) return PA_ERR_SHAPE;
+  if (!valid_block_size(block_size)) return PA_ERR_UNSUPPORTED;
+  if (!cu_seqlens_q || !num_free || !num_free_out) return PA_ERR_NULL;
+  if (num_seqs > 0 && (!context_lens || !query_lens || !context_lens_out)) return PA_ERR_NULL;
+  if (num_seqs > 0 && max_blocks_per_seq > 0 && !block_table) return PA_ERR_NULL;
+  if (free_capacity > 0 && !free_blocks) return PA_ERR_NULL;
+  if (max_tokens > 0 && !slot_mapping) return PA_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(context_lens) |
+       reinterpret_cast<uintptr_t>(query_lens) | reinterpret_cast<uintptr_t>(free_blocks) |
+       reinterpret_cast<uintptr_t>(num_free) | reinterpret_cast<uintptr_t>(context_lens_out) |
+       reinterpret_cast<uintptr_t>(cu_seqlens_q) | reinterpret_cast<uintptr_t>(positions) |
+       reinterpret_cast<uintptr_t>(num_free_out)) & 3u)
+    return PA_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) return PA_ERR_ALIGN;
+  // every CTA reads the lengths and the list's length while others write
+  auto overlaps = [](const int32_t *x, int64_t nx, const int32_t *y, int64_t ny) {
+    return nx > 0 && ny > 0 && x < y + ny && y < x + nx;
+  };
+  if (overlaps(context_lens_out, num_seqs, context_lens, num_seqs) ||
+      overlaps(context_lens_out, num_seqs, query_lens, num_seqs) ||
+      overlaps(num_free_out, 1, num_free, 1))
+    return PA_ERR_SHAPE;
+  pa::BuildTablesArgs a;
+  a.block_table = block_table;
+  a.block_table_stride = block_table_stride;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.context_lens = context_lens;
+  a.query_lens = query_lens;
+  a.free_blocks = free_blocks;
+  a.num_free = num_free;
+  a.free_capacity = free_capacity;
+  a.context_lens_out = context_lens_out;
+  a.cu_seqlens_q = cu_seqlens_q;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.num_free_out = num_free_out;
+  a.num_seqs = num_seqs;
+  a.max_tokens = max_tokens;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.d_error = d_error;
+  cudaError_t e = current_num_sms(&a.num_sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  e = pa::launch_build_tables(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
 pa_status pa_reshape_and_cache_int8(const void *key, const void *value, int64_t kv_row_stride,
                                     void *key_cache, void *value_cache,
                                     const int64_t *slot_mapping, int32_t num_tokens,

@@ -45,6 +45,23 @@ struct CopyBlocksArgs {
 };
 cudaError_t launch_copy_blocks(const CopyBlocksArgs &a, cudaStream_t stream);
 
+struct BuildTablesArgs {
+  int32_t *block_table;
+  int64_t block_table_stride;
+  int32_t max_blocks_per_seq;
+  const int32_t *context_lens, *query_lens, *free_blocks, *num_free;
+  int32_t free_capacity;
+  int32_t *context_lens_out, *cu_seqlens_q;
+  int64_t *slot_mapping;
+  int32_t *positions;  // nullable
+  int32_t *num_free_out;
+  int32_t num_seqs, max_tokens, block_size;
+  int64_t num_blocks;
+  int32_t *d_error;
+  int num_sms;
+};
+cudaError_t launch_build_tables(const BuildTablesArgs &a, cudaStream_t stream);
+
 // Decode tiling shared by the planner and the kernels.
 constexpr int kDecodeWarps = 4;     // consumer warps (independent workers) per CTA
 constexpr int kDecodeCtasPerSm = 2;  // resident decode CTAs per SM
