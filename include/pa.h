@@ -17,7 +17,8 @@
  * write, the decode and the step over INT8 pools, the _fp8 calls the same
  * over FP8 (E4M3) pools; pa_copy_blocks copies whole blocks (copy-on-write).
  * pa_build_tables forms a step's block tables, slots and cumulative lengths
- * from request lengths.
+ * from request lengths; pa_attention_varlen is the attention of packed
+ * prompts straight from their K/V rows, without a cache.
  *
  * Sources (web pages on paged KV caches, cited by page and section):
  *   [SKILL] cannbot-skills "model-infer-kvcache" skill page: §3.1 physical
@@ -568,6 +569,42 @@ pa_status pa_build_tables(int32_t *block_table, int64_t block_table_stride,
                           int64_t *slot_mapping, int32_t *positions, int32_t *num_free_out,
                           int32_t num_seqs, int32_t max_tokens, int32_t block_size,
                           int64_t num_blocks, int32_t *d_error, void *stream);
+
+/*
+ * pa_attention_varlen -- attention of packed prompts over their own K/V rows.
+ *
+ * Defines ([LQNN] §3.1 cu_seqlens, §4.4 packed attention; [SKILL] App. C
+ * sparse_mode 3): sequence b owns rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of
+ * query, key, value and out; query head h of its row i gets
+ *     out_i = sum_j softmax_j(scale * q_i . k_j) v_j,
+ * over its own rows j <= i (causal != 0) or all its rows (causal == 0), of KV
+ * head h / (num_q_heads / num_kv_heads).  It is what pa_prefill_varlen
+ * computes for whole prompts, without a cache: it need not wait for the
+ * cache write, and serves prompts whose cache holds one-byte codes.
+ *
+ *   query, out   [total_tokens, num_q_heads, head_dim] at their row strides.
+ *   key, value   [total_tokens, num_kv_heads, head_dim], both at
+ *                kv_row_stride (so K and V may be views into one buffer).
+ *   cu_seqlens   int32 [num_seqs + 1]: starts at 0, never decreases, ends at
+ *                or before total_tokens; sequences may be empty.  Rows from
+ *                cu_seqlens[num_seqs] on (padding) are not read as keys and
+ *                their out rows are left as they were; they may hold
+ *                anything.
+ *   max_seqlen   host upper bound of the sequences' lengths.
+ * A cu_seqlens that is none, or a sequence longer than max_seqlen, sets
+ * PA_DEVERR_CU_SEQLENS; a sequence whose own two entries are bad is skipped.
+ * No row of out may overlap query, key or value.  K and V of a sequence must
+ * be finite for its rows to be.
+ * Supported: fp16 / bf16, head_dim 64 or 128, any num_q_heads % num_kv_heads
+ * == 0.
+ */
+pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *query,
+                              int64_t q_row_stride, const void *key, const void *value,
+                              int64_t kv_row_stride, const int32_t *cu_seqlens,
+                              int32_t num_seqs, int32_t total_tokens, int32_t max_seqlen,
+                              int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                              float scale, int32_t causal, pa_dtype dtype, int32_t *d_error,
+                              void *stream);
 
 #ifdef __cplusplus
 }

@@ -15,6 +15,7 @@ first call raises.
     pa_copy_blocks        copy whole blocks of both pools (copy-on-write)
     pa_build_tables       a step's block tables, slots, positions and cumulative
                           lengths from request lengths
+    pa_attention_varlen   causal attention of packed prompts from their K/V rows
 
 Build the library with ``python -m paged_kv_cache_34_gb300.build``.
 """
@@ -29,7 +30,8 @@ import torch
 __all__ = ["pa_reshape_and_cache", "pa_decode", "pa_decode_plan", "pa_decode_write",
            "pa_prefill_varlen", "pa_reshape_and_cache_int8", "pa_decode_int8",
            "pa_decode_write_int8", "pa_reshape_and_cache_fp8", "pa_decode_fp8",
-           "pa_decode_write_fp8", "pa_copy_blocks", "pa_build_tables", "PaError",
+           "pa_decode_write_fp8", "pa_copy_blocks", "pa_build_tables",
+           "pa_attention_varlen", "PaError",
            "library", "DEVERR_SLOT", "DEVERR_BLOCK_ID", "DEVERR_CU_SEQLENS",
            "DEVERR_CONTEXT", "DEVERR_TIMEOUT", "DEVERR_SCALE", "DEVERR_NO_BLOCKS",
            "LIB_PATH"]
@@ -100,6 +102,9 @@ def library(path: str | None = None):
         lib.pa_build_tables.argtypes = [V, I64, I32, V, V, V, V, I32, V, V, V, V, V, I32, I32,
                                         I32, I64, V, V]
         lib.pa_build_tables.restype = c.c_int
+        lib.pa_attention_varlen.argtypes = [V, I64, V, I64, V, V, I64, V, I32, I32, I32, I32,
+                                            I32, I32, F, I32, c.c_int, V, V]
+        lib.pa_attention_varlen.restype = c.c_int
         lib.pa_decode_int8.argtypes = [V, I64, V, I64, V, V, V, I64, I32, V, I32, I32, I32,
                                        I32, I32, I64, V, V, F, I32, I32, V, SZ, c.c_int, V, V]
         lib.pa_decode_int8.restype = c.c_int
@@ -488,4 +493,35 @@ def pa_prefill_varlen(out, query, key_cache, value_cache, block_table, cu_seqlen
                                1 if causal else 0, _DTYPE[query.dtype], _ptr(d_error),
                                _stream(stream))
     _check(lib, st, "pa_prefill_varlen")
+    return out
+
+
+def pa_attention_varlen(out, query, key, value, cu_seqlens, *, scale, max_seqlen, causal=True,
+                        d_error=None, stream=None, lib=None):
+    """Attention of prompts packed one behind the other, over their own rows:
+    out/query [T, Hq, D], key/value [T, Hkv, D] (equal row strides, e.g. views
+    into one QKV buffer), cu_seqlens int32 [S+1].  ``max_seqlen`` is the host
+    upper bound of the lengths; rows past cu_seqlens[S] are left alone."""
+    lib = lib or library()
+    t, hq, d = query.shape
+    if out.shape != query.shape or key.shape != value.shape or key.shape[0] != t \
+            or key.shape[2] != d:
+        raise ValueError("out/query must be [T, Hq, D] and key/value [T, Hkv, D]")
+    if not (out.dtype == query.dtype == key.dtype == value.dtype) or query.dtype not in _DTYPE:
+        raise ValueError("out, query, key and value must share a dtype, float16 or bfloat16")
+    os, qs, ks = _rows(out, "out"), _rows(query, "query"), _rows(key, "key")
+    if _rows(value, "value") != ks:
+        raise ValueError("key and value must share a row stride")
+    _vector(cu_seqlens, cu_seqlens.numel(), torch.int32, "cu_seqlens")
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold num_seqs + 1 values")
+    _on_device("pa_attention_varlen", out=out, query=query, key=key, value=value,
+               cu_seqlens=cu_seqlens, d_error=d_error)
+    st = lib.pa_attention_varlen(out.data_ptr(), os, query.data_ptr(), qs, key.data_ptr(),
+                                 value.data_ptr(), ks, cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, t,
+                                 int(max_seqlen), hq, key.shape[1], d, float(scale),
+                                 1 if causal else 0, _DTYPE[query.dtype],
+                                 None if d_error is None else d_error.data_ptr(),
+                                 _stream(stream))
+    _check(lib, st, "pa_attention_varlen")
     return out

@@ -102,6 +102,15 @@ bool encode_rows_map(CUtensorMap *map, const void *base, pa_dtype dtype, int hea
 
 bool valid_block_size(int bs) { return bs == 8 || bs == 16 || bs == 32 || bs == 64 || bs == 128; }
 
+// The factor of the flash engine's scores: |scale| log2 e, kept away from 0 so
+// that a masked score (-inf) times it stays -inf (1e-37 leaves every finite
+// score's weight at 1), and whether Q enters the product negated.
+void flash_scale(float scale, float *scale_log2, bool *negate) {
+  const double f = fabs(static_cast<double>(scale)) * 1.4426950408889634;
+  *scale_log2 = f > 1e-37 ? static_cast<float>(f) : 1e-37f;
+  *negate = scale < 0.0f;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // The automatic plan is the balanced split, as long as its positions fit in
@@ -773,6 +782,59 @@ pa_status pa_prefill_varlen(void *out, int64_t out_row_stride, const void *query
                        box))
     return cuda_fail(cudaErrorInvalidValue);
   e = pa::launch_prefill(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *query,
+                              int64_t q_row_stride, const void *key, const void *value,
+                              int64_t kv_row_stride, const int32_t *cu_seqlens,
+                              int32_t num_seqs, int32_t total_tokens, int32_t max_seqlen,
+                              int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                              float scale, int32_t causal, pa_dtype dtype, int32_t *d_error,
+                              void *stream) {
+  if (num_seqs < 0 || total_tokens < 0 || max_seqlen < 0 || num_q_heads <= 0 ||
+      num_kv_heads <= 0 || head_dim <= 0)
+    return PA_ERR_SHAPE;
+  if (num_q_heads % num_kv_heads != 0) return PA_ERR_SHAPE;
+  if (!isfinite(scale)) return PA_ERR_SHAPE;
+  if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || total_tokens == 0 || max_seqlen == 0) return PA_OK;
+  if (!out || !query || !key || !value || !cu_seqlens) return PA_ERR_NULL;
+  const int64_t qrow = static_cast<int64_t>(num_q_heads) * head_dim;
+  const int64_t kvrow = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (q_row_stride < qrow || out_row_stride < qrow || kv_row_stride < kvrow) return PA_ERR_SHAPE;
+  if (q_row_stride % 8 || out_row_stride % 8 || kv_row_stride % 8) return PA_ERR_ALIGN;
+  if (!aligned16(out) || !aligned16(query) || !aligned16(key) || !aligned16(value))
+    return PA_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) return PA_ERR_ALIGN;
+
+  pa::AttentionVarlenArgs a;
+  a.out = out;
+  a.out_row_stride = out_row_stride;
+  a.cu_seqlens = cu_seqlens;
+  a.num_seqs = num_seqs;
+  a.total = total_tokens;
+  a.max_seqlen = max_seqlen;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.packed_heads = pa::flash_packed_heads(num_q_heads / num_kv_heads);
+  flash_scale(scale, &a.scale_log2, &a.negate);
+  a.causal = causal ? 1 : 0;
+  a.d_error = d_error;
+  a.dtype = dtype;
+  a.wait_ns = pa::pipeline_wait_ns();
+  cudaError_t e = current_num_sms(&a.num_sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (!encode_rows_map(&a.tm_q, query, dtype, head_dim, num_q_heads, total_tokens, q_row_stride,
+                       128 / a.packed_heads, false, a.packed_heads) ||
+      !encode_rows_map(&a.tm_k, key, dtype, head_dim, num_kv_heads, total_tokens, kv_row_stride,
+                       128) ||
+      !encode_rows_map(&a.tm_v, value, dtype, head_dim, num_kv_heads, total_tokens,
+                       kv_row_stride, 128))
+    return cuda_fail(cudaErrorInvalidValue);
+  e = pa::launch_attention_varlen(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 

@@ -196,4 +196,31 @@ inline int prefill_packed_heads(int group, int max_seqlen_q) {
 }
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);
 
+// The query heads a tile of the flash engine packs into its rows: the largest
+// divisor of the GQA group whose multiples fill at least 7/8 of 128 rows.
+inline int flash_packed_heads(int group) {
+  for (int d = group < 128 ? group : 128; d > 1; --d)
+    if (group % d == 0 && (128 / d) * d >= 112) return d;
+  return 1;
+}
+
+struct AttentionVarlenArgs {
+  void *out;
+  int64_t out_row_stride;
+  const int32_t *cu_seqlens;
+  int32_t num_seqs, total, max_seqlen;
+  int32_t num_q_heads, num_kv_heads, head_dim;
+  int packed_heads;
+  float scale_log2;  // |scale| * log2(e), not 0
+  bool negate;       // the scale is negative
+  int32_t causal;
+  int32_t *d_error;
+  pa_dtype dtype;
+  // boxes: q 64 x packed_heads x 128 / packed_heads, k and v 64 x 1 x 128
+  CUtensorMap tm_q, tm_k, tm_v;
+  int num_sms;
+  uint64_t wait_ns = 0;
+};
+cudaError_t launch_attention_varlen(const AttentionVarlenArgs &a, cudaStream_t stream);
+
 }  // namespace pa
