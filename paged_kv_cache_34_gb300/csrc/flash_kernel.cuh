@@ -744,93 +744,90 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The whole warp runs this loop; MMAs and commits are issued by one
       // elected lane.  The tensor core runs one thread's MMAs in order, so
       // Q K^T may overwrite the S columns that the P V before it reads.
+      // Issuing runs at the tensor core's own pace, so every cycle this warp
+      // spends between two issues is one the tensor core idles: a step's
+      // bookkeeping and its waits for K and V are done before the wait for P,
+      // and P V and the stream's next Q K^T go out in one block after it
+      // (separate waits and blocks measured 2700 cycles per tile step
+      // instead of 1024: 930 TFLOP/s on two prompts of 16384).
       const uint32_t id_qk = idesc_f16(E::kBF16, 128, 128, false) | (p.negate << 13);
       const uint32_t id_pv = idesc_f16(E::kBF16, 128, D, true);
-      const uint32_t smem0 = smem_u32(smem);
+      const uint64_t q_desc0 = sdesc_sw128(smem_u32(smem) + L::kQOff, 16, 1024);
+      const uint64_t k_desc0 = sdesc_sw128(smem_u32(smem) + L::kKOff, 16, 1024);
+      const uint64_t v_desc0 = sdesc_sw128(smem_u32(smem) + L::kVOff, kHalf, 1024);
       bool ok = true;
-      auto commit = [&](int b) {
-        if (elect_one()) umma_commit(bar(b));
-        __syncwarp();
+      // Every lane asks once; only a wait that is not over yet goes the long way.
+      auto ready = [&](int b, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_try_wait(bar(b), parity)) != 0;
       };
-      // Per stream: its place in the list (item cj with cursor fields), and
-      // the Q K^T issued whose P V is still to come.
+      auto wait = [&](int b, uint32_t parity) {
+        return ready(b, parity) || warp_wait(b, parity);
+      };
+      constexpr int kNone = 0x7fffffff;
+      // Per stream: the step whose Q K^T is issued and whose P V is to come
+      // (ring position pn, or kNone), the ring position np of the Q K^T after
+      // it where that is known (kNone: the item is exhausted), and the place
+      // in the item list.
       struct Stream {
-        int j;                    // item of the fields below (-1: none yet)
-        int first, step, cnt, used, end, q;
-        bool ended;
-        bool pend, plast, pfirst;
-        int pn;                   // ring position of the pending step
-        int items, psteps;        // items begun and P tiles taken
+        int pn, np;
+        bool pfirst, plast;       // the pending step is its item's first / last
+        int j, end;               // item the fields belong to, its end
+        int step, left, q;        // ring step, Q K^T still to issue, Q buffer
+        bool first, ended;        // the next Q K^T is the item's first
+        int items, psteps;        // items begun (P V), P tiles taken
       } st[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
+        st[t].pn = st[t].np = kNone;
+        st[t].pfirst = st[t].plast = st[t].first = st[t].ended = false;
         st[t].j = -1;
-        st[t].cnt = st[t].used = st[t].end = st[t].first = st[t].q = 0;
+        st[t].end = st[t].left = st[t].q = st[t].items = st[t].psteps = 0;
         st[t].step = 1;
-        st[t].ended = st[t].pend = st[t].plast = st[t].pfirst = false;
-        st[t].pn = 0;
-        st[t].items = st[t].psteps = 0;
       }
-      // Ring position of stream s's next Q K^T, if it is at most `limit`;
-      // else a larger number.  Walks on to items that begin within it.
-      auto next_use = [&](Stream &s, int t, int limit) {
-        while (!s.ended && s.used >= s.cnt && s.end <= limit) {
+      // An exhausted stream walks on to the items that begin by `limit`.
+      auto advance = [&](Stream &s, int t, int limit) {
+        while (!s.ended && s.left == 0 && s.end <= limit) {
           Item it;
           if (!peek_item(s.j + 1, &it)) ok = false;
           if (!ok || !it.live) {
             s.ended = true;
-            break;
+            return;
           }
           ++s.j;
-          s.first = use_first(it, t);
-          s.step = use_step(it);
-          s.cnt = it.cnt[t];
-          s.used = 0;
           s.end = it.base + it.nkv;
+          s.left = it.cnt[t];
+          s.np = s.left > 0 ? use_first(it, t) : kNone;
+          s.step = use_step(it);
+          s.first = true;
           s.q = it.qbase + (t == 1 && it.cnt[0] > 0 ? 1 : 0);
         }
-        return s.used < s.cnt ? s.first + s.used * s.step : 0x7fffffff;
       };
-      auto qk = [&](Stream &s, int t, int n) {  // S_t = Q_t K_n^T
+      // The elected lane's part of S_t = Q_t K_n^T.
+      auto issue_qk = [&](const Stream &s, int t, int n) {
         const int qs = s.q % L::NQ;
-        if (s.used == 0) ok = warp_wait(L::kQFull + qs, (s.q / L::NQ) & 1);
-        if (ok) ok = warp_wait(L::kKFull + n % L::NK, (n / L::NK) & 1);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t qd = sdesc_sw128(smem0 + L::kQOff + qs * L::kTile, 16, 1024);
-        const uint64_t kd = sdesc_sw128(smem0 + L::kKOff + (n % L::NK) * L::kTile, 16, 1024);
-        const bool last = s.used + 1 == s.cnt;
-        if (elect_one()) {
-          // K step k: 16 columns = 32 bytes into a 128-byte swizzled row,
-          // the second 64 columns in the tile's second half
+        const uint64_t qd = q_desc0 + static_cast<uint64_t>(qs) * (L::kTile >> 4);
+        const uint64_t kd = k_desc0 + static_cast<uint64_t>(n % L::NK) * (L::kTile >> 4);
+        // K step k: 16 columns = 32 bytes into a 128-byte swizzled row, the
+        // second 64 columns in the tile's second half
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-            umma_f16_ss(tbase + t * 128, qd + off, kd + off, id_qk, k > 0 ? 1u : 0u);
-          }
-          umma_commit(bar(L::kSFull + t));
-          if (last) umma_commit(bar(L::kQEmpty + qs));
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+          umma_f16_ss(tbase + t * 128, qd + off, kd + off, id_qk, k > 0 ? 1u : 0u);
         }
-        __syncwarp();
-        s.pend = true;
-        s.pn = n;
-        s.pfirst = s.used == 0;
-        s.plast = last;
-        ++s.used;
+        umma_commit(bar(L::kSFull + t));
+        if (s.left == 1) umma_commit(bar(L::kQEmpty + qs));
       };
-      auto pv = [&](Stream &s, int t) {  // O_t += P_t V_n, P_t from TMEM
-        const uint64_t vd =
-            sdesc_sw128(smem0 + L::kVOff + (s.pn % L::NV) * L::kTile, kHalf, 1024);
-        const uint32_t acc0 = s.pfirst ? 0u : 1u;
-        if (elect_one()) {
-          // K step k: 16 keys = 16 rows of 128 bytes of the MN-major V tile
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_f16_ts(tbase + 256 + t * 128, tbase + t * 128 + 8 * k, vd + ((k * 2048) >> 4),
-                        id_pv, k > 0 ? 1u : acc0);
-          if (s.plast) umma_commit(bar(L::kOFull + t));
-        }
-        __syncwarp();
+      // ... and the bookkeeping after it.
+      auto qk_issued = [&](Stream &s, int n) {
+        s.pn = n;
+        s.pfirst = s.first;
+        s.first = false;
+        s.plast = --s.left == 0;
+        s.np = s.plast ? kNone : n + s.step;
+      };
+      auto wait_qk = [&](const Stream &s, int n) {  // the operands of Q K_n^T
+        if (s.first && !wait(L::kQFull + s.q % L::NQ, (s.q / L::NQ) & 1)) return false;
+        return wait(L::kKFull + n % L::NK, (n / L::NK) & 1);
       };
       int r = -1, r_end = 0;         // the item that holds ring position n
       bool r_tail = false;
@@ -847,53 +844,83 @@ __global__ void __launch_bounds__(kThreads, 1)
           r_end = it.base + it.nkv;
           r_tail = (it.flags & kTail) != 0;
         }
-        bool have_v = false;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          Stream &s = st[t];
-          if (s.pend && s.pn == n) {
-            if (s.pfirst) {
-              if (s.items > 0) ok = warp_wait(L::kOFree + t, (s.items - 1) & 1);
-              ++s.items;
-              if (!ok) break;
-            }
-            if (!have_v) {
-              ok = warp_wait(L::kVFull + n % L::NV, (n / L::NV) & 1);
-              if (ok && r_tail && n + 1 == r_end) {
-                ok = warp_wait(L::kVFixed + n % L::NV, (fix_par >> (n % L::NV)) & 1);
-                fix_par ^= 1u << (n % L::NV);
-              }
-              have_v = true;
-              if (!ok) break;
-            }
-            ok = warp_wait(L::kPFull + t, s.psteps & 1);
-            ++s.psteps;
-            if (!ok) break;
-            tc_fence_after();
-            pv(s, t);
-            s.pend = false;
-            if (next_use(s, t, n + 1) == n + 1) qk(s, t, n + 1);
-            if (!ok) break;
+        if (n >= 0) {
+          ok = wait(L::kVFull + n % L::NV, (n / L::NV) & 1);
+          if (ok && r_tail && n + 1 == r_end) {
+            ok = wait(L::kVFixed + n % L::NV, (fix_par >> (n % L::NV)) & 1);
+            fix_par ^= 1u << (n % L::NV);
           }
         }
         if (!ok) break;
-        if (n >= 0) commit(L::kVEmpty + n % L::NV);
-        // streams that do not use tile n: their next one in the window
 #pragma unroll
-        for (int m = 1; m <= 2; ++m)
+        for (int t = 0; t < 2; ++t) {
+          Stream &s = st[t];
+          if (!ok || s.pn != n || n < 0) continue;
+          if (s.pfirst) {  // O of the stream's previous item has been read
+            if (s.items > 0) ok = wait(L::kOFree + t, (s.items - 1) & 1);
+            ++s.items;
+          }
+          // the stream's next Q K^T goes along if its K is there already
+          const bool along = s.np == n + 1 &&
+                             ready(L::kKFull + (n + 1) % L::NK, ((n + 1) / L::NK) & 1);
+          const uint64_t vd = v_desc0 + static_cast<uint64_t>(n % L::NV) * (L::kTile >> 4);
+          const uint32_t acc0 = s.pfirst ? 0u : 1u;
+          const bool last = s.plast;
+          if (!ok) continue;
+          ok = wait(L::kPFull + t, s.psteps & 1);
+          if (!ok) continue;
+          tc_fence_after();
+          if (elect_one()) {
+            // O_t += P_t V_n, P_t from TMEM; K step k: 16 keys = 16 rows of
+            // 128 bytes of the MN-major V tile
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              umma_f16_ts(tbase + 256 + t * 128, tbase + t * 128 + 8 * k, vd + ((k * 2048) >> 4),
+                          id_pv, k > 0 ? 1u : acc0);
+            if (last) umma_commit(bar(L::kOFull + t));
+            if (along) issue_qk(s, t, n + 1);
+          }
+          __syncwarp();
+          ++s.psteps;
+          s.pn = kNone;
+          if (along) qk_issued(s, n + 1);
+        }
+        if (!ok) break;
+        // Streams without a Q K^T out: tile n + 1 (its K was late, or the
+        // stream does not use tile n), then n + 2.
+        if (st[0].pn == kNone || st[1].pn == kNone) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
-            if (ok && !st[t].pend && next_use(st[t], t, n + m) == n + m) qk(st[t], t, n + m);
-        if (!ok) break;
-        // every use of tile n + 1 by Q K^T has been issued (a stream still
-        // behind it has no use of it)
-        if (n + 1 < r_end || st[0].end > n + 1 || st[1].end > n + 1)
-          commit(L::kKEmpty + (n + 1) % L::NK);
+            if (st[t].pn == kNone) advance(st[t], t, n + 2);
+#pragma unroll
+          for (int m = 1; m <= 2; ++m)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              Stream &s = st[t];
+              if (!ok || s.pn != kNone || s.np != n + m) continue;
+              ok = wait_qk(s, n + m);
+              if (!ok) continue;
+              tc_fence_after();
+              if (elect_one()) issue_qk(s, t, n + m);
+              __syncwarp();
+              qk_issued(s, n + m);
+            }
+          if (!ok) break;
+        }
+        // Tile n's V has been used, and every Q K^T of tile n + 1, if there is
+        // one, has been issued (a stream still behind it has no use of it).
+        const bool next_tile = n + 1 < r_end || st[0].end > n + 1 || st[1].end > n + 1;
+        if (elect_one()) {
+          if (n >= 0) umma_commit(bar(L::kVEmpty + n % L::NV));
+          if (next_tile) umma_commit(bar(L::kKEmpty + (n + 1) % L::NK));
+        }
+        __syncwarp();
       }
       if (!ok && lane == 0) give_up();
       // Every MMA issued above has completed once this barrier fires (the
       // full bound: TMEM is freed after it).
-      commit(L::kFin);
+      if (elect_one()) umma_commit(bar(L::kFin));
+      __syncwarp();
       if (lane == 0) mbar_wait_bounded(bar(L::kFin), 0);
       __syncwarp();
     }
