@@ -28,9 +28,15 @@ cudaError_t launch_attention_varlen(const AttentionVarlenArgs &a, cudaStream_t s
   p.max_seqlen = a.max_seqlen;
   p.err = a.d_error;
   p.wait_ns = a.wait_ns;
-  // pairs of query tiles: at most one partly filled per sequence
-  int64_t items = (a.total / (2 * p.tpt) + static_cast<int64_t>(a.num_seqs)) * p.hu;
-  const int grid = static_cast<int>(items < a.num_sms ? items : a.num_sms);
+  p.kv_bytes = 4 * a.head_dim;
+  // One CTA per item, pairs of query tiles x head units: at most one pair of
+  // a sequence is partly filled.
+  const int64_t longest = a.max_seqlen < a.total ? a.max_seqlen : a.total;
+  int64_t pairs = a.total / (2 * p.tpt) + static_cast<int64_t>(a.num_seqs);
+  const int64_t most = a.num_seqs * ((longest + 2 * p.tpt - 1) / (2 * p.tpt));
+  if (pairs > most) pairs = most;
+  if (pairs * p.hu > 0x7fffffff) return cudaErrorInvalidValue;
+  const int grid = static_cast<int>(pairs * p.hu);
   const bool bf = a.dtype == PA_BF16;
   if (a.head_dim == 64)
     return bf ? flash::launch<BF16, 64, false>(p, a.tm_q, a.tm_k, a.tm_v, grid, stream)

@@ -28,17 +28,14 @@
 //    stream idles.  A tile's rows are (token, head) pairs of the query heads
 //    of one KV head.
 //  * The streams run through the items without a stop: K/V tiles are
-//    numbered through all of a CTA's items ("ring positions"), and in the
-//    round of position n the MMA warp issues P V of tile n for the streams
-//    that use it, then Q K^T of tile n + 1, and for a stream that skips it
-//    of tile n + 2 -- the next item's first.  A causal pair's A has one tile
-//    less than its B, so A starts the next item while B finishes.  (A kernel
-//    whose items start and end together measured 650 TFLOP/s on 16 prompts of
-//    1000 tokens, 3 us lost per item.)  Three Q buffers let the next item's
-//    A query load during the current item.
-//  * Items are dealt out statically, heaviest first and in alternating
-//    direction (packed prompts), or as equal runs of K/V tiles (prefix), so no
-//    counter in global memory is shared between launches.
+//    numbered through all of a CTA's items ("ring positions") and each stream,
+//    with an MMA warp of its own, goes on to the next tile it uses whatever
+//    item that is in.  A causal pair's A has one tile less than its B, so A
+//    starts the next item while B finishes; three Q buffers let the next
+//    item's first query tile load during the current item.
+//  * Items are handed out by the hardware's launch queue (packed prompts) or
+//    as equal runs of K/V tiles (prefix), so no counter in global memory is
+//    shared between launches.
 #pragma once
 
 #include <math.h>
@@ -52,7 +49,7 @@ namespace flash {
 
 // Warpgroups: 0 / 1 softmax of stream A / B, 2 epilogue, 3 producers.
 constexpr int kThreads = 512;
-constexpr int kEpiWarp0 = 8, kTmaWarp = 12, kMmaWarp = 13, kFixWarp = 14, kSchedWarp = 15;
+constexpr int kEpiWarp0 = 8, kTmaWarp = 12, kMmaWarp0 = 13, kSchedWarp = 15;  // MMA: 13 A, 14 B
 // Registers per thread after the split (setmaxnreg, per warpgroup); they must
 // fit in what the CTA is launched with (checked on the host).
 constexpr int kSoftmaxRegs = 152, kEpilogueRegs = 104, kProducerRegs = 104;
@@ -62,7 +59,7 @@ constexpr uint32_t kTmemCols = 512;        // S_A | S_B | O_A | O_B (P_t overlay
 constexpr float kRescaleThreshold = 8.0f;  // log2 of the largest weight allowed
 constexpr int kKeys = 128;                 // keys per K/V tile
 constexpr int kItemRing = 4;
-constexpr int kItemTakers = 15;  // 8 softmax warps, 4 epilogue warps, TMA, MMA, fixer
+constexpr int kItemTakers = 15;  // 8 softmax warps, 4 epilogue warps, TMA, 2 MMA
 
 template <int D>
 struct Layout {
@@ -91,10 +88,13 @@ struct Layout {
     kMLFull = kOFree + 2,        // ... the softmax has left (m, l)
     kItemFull = kMLFull + 2,
     kItemEmpty = kItemFull + kItemRing,
-    kFin = kItemEmpty + kItemRing,
-    kNumBars = kFin + 1
+    kBegun = kItemEmpty + kItemRing,  // the TMA warp has begun an item
+    kNext = kBegun + 1,               // the launch's next item has come
+    kFin = kNext + 1,                 // per stream: every MMA issued is done
+    kNumBars = kFin + 2
   };
-  static constexpr int kItemOff = kBarOff + kNumBars * 8;
+  static constexpr int kNextOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // the answer, 16 B
+  static constexpr int kItemOff = kNextOff + 16;
   static constexpr int kItemWords = 20;
   static constexpr int kMiscOff = kItemOff + kItemRing * kItemWords * 4;  // TMEM base, abort
   static constexpr int kBytes = kMiscOff + 16;
@@ -109,7 +109,7 @@ struct Item {
   int tok0;      // first of them in the item's first tile
   int head0;     // first query head of the tile's rows
   int kvh;       // KV head
-  int flags;     // kSingle | kTurns | kTail
+  int flags;     // kSingle | kTurns | kTail | kTailOdd (parity of the tail in its V buffer)
   int nkv;       // K/V tiles
   int cnt[2];    // ... used by stream A, B
   int key0;      // first key
@@ -122,7 +122,7 @@ struct Item {
 };
 constexpr int kItemFields = 17;
 static_assert(sizeof(Item) == kItemFields * 4, "item words");
-enum { kSingle = 1, kTurns = 2, kTail = 4 };
+enum { kSingle = 1, kTurns = 2, kTail = 4, kTailOdd = 8 };
 
 struct Params {
   // queries and output rows
@@ -136,6 +136,7 @@ struct Params {
   // packed prompts
   const int32_t *cu;
   int32_t num_seqs, total, max_seqlen;
+  int32_t kv_bytes;         // of one token's K and V, one KV head
   // prefix pass
   const int32_t *block_table;
   int64_t bt_stride;
@@ -157,86 +158,122 @@ __device__ __forceinline__ int tiles_of(const Params &p, int n) {
 }
 
 // ------------------------------------------------------ work distribution --
-// Packed prompts.  Item x of the launch: pairs of query tiles, the heaviest
-// first over the whole batch (a causal pair's cost is its index, whatever the
-// sequence), then by sequence and head unit; batches of more than 64
-// sequences go sequence by sequence, heaviest pair first, which needs no
-// counting over all sequences per step.  Item k of CTA c is x = k * grid + c,
-// or counted from the far end in odd rounds, so that no CTA always gets a
-// round's heaviest.  Warp-collective.
-struct PackedSched {
-  int pairs0, pairs1;  // pairs of sequences lane, lane + 32 (up to 64 sequences)
-  int level;           // ... the current pair index
-  int64_t base;        // items before the level (or before chunk c0)
-  int c0;              // first sequence of the current 32 (more than 64 sequences)
-  int k;
+// Packed prompts.  The launch has (at least) one CTA per item; the ones that
+// run take over the items of those still waiting (cluster launch control), so
+// items are handed out in order as CTAs become free, without a counter in
+// memory.  The order keeps K and V in L2 and the last items light: sequences
+// by falling length (up to 64 of them, else as they come), within one the
+// head units in blocks whose K and V stay in L2, within a block the tile pairs
+// from the last, heaviest one down, then the block's head units.  (All
+// sequences' heaviest pairs first read K and V again for each pair: 190 us
+// instead of 146 on 16 prompts of 1000 tokens, 32/32 heads.)
+constexpr int64_t kBlockBytes = 40 << 20;  // K and V of a head block: a third of L2
 
-  __device__ int pairs(const Params &p, int s) const {
+// Warp-collective; each call goes on from the one before while x grows.
+struct PackedSched {
+  unsigned key0, key1;  // sequences lane, lane + 32: pairs << 6 | (63 - index), 0 once passed
+  int seq, n;           // the current sequence and its pairs
+  int64_t base;         // items before it
+
+  // Query tile pairs of sequence s; none where its two entries are bad.
+  static __device__ int pairs_of(const Params &p, int s) {
     if (s >= p.num_seqs) return 0;
-    const int a = __ldg(p.cu + s), e = __ldg(p.cu + s + 1);  // a bad pair of entries: no items
+    const int a = __ldg(p.cu + s), e = __ldg(p.cu + s + 1);
     if (a < 0 || e <= a || e > p.total || e - a > p.max_seqlen) return 0;
     return (tiles_of(p, e - a) + 1) / 2;
   }
+  // The next sequence by length (up to 64).
+  __device__ void longest(int lane) {
+    const unsigned top = __reduce_max_sync(0xffffffffu, max(key0, key1));
+    n = static_cast<int>(top >> 6);
+    seq = 63 - static_cast<int>(top & 63u);
+    if (key0 == top) key0 = 0;
+    if (key1 == top) key1 = 0;
+  }
   __device__ void init(const Params &p, int lane) {
-    k = 0;
     base = 0;
-    c0 = 0;
-    level = 0;
-    pairs0 = pairs1 = 0;
+    seq = 0;  // more than 64 sequences: first of the current 32
     if (p.num_seqs <= 64) {
-      pairs0 = pairs(p, lane);
-      pairs1 = pairs(p, lane + 32);
-      level = __reduce_max_sync(0xffffffffu, max(pairs0, pairs1)) - 1;
+      const int n0 = pairs_of(p, lane), n1 = pairs_of(p, lane + 32);
+      key0 = n0 ? static_cast<unsigned>(n0) << 6 | (63 - lane) : 0u;
+      key1 = n1 ? static_cast<unsigned>(n1) << 6 | (31 - lane) : 0u;
+      longest(lane);
     }
   }
-  // (sequence, pair, head unit) of this CTA's next item; false at the end.
-  __device__ bool next(const Params &p, int lane, int *seq, int *pair, int *head) {
-    const int64_t c = (k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-    const int64_t x = static_cast<int64_t>(k) * gridDim.x + c;
-    ++k;
+  // (sequence, pair, head unit) of item x; false beyond the last.
+  __device__ bool find(const Params &p, int64_t x, int lane, int *seq_out, int *pair, int *head) {
+    int pairs, rem;
     if (p.num_seqs <= 64) {
-      for (; level >= 0; --level) {
-        const unsigned b0 = __ballot_sync(0xffffffffu, pairs0 > level);
-        const unsigned b1 = __ballot_sync(0xffffffffu, pairs1 > level);
-        const int n0 = __popc(b0), n = n0 + __popc(b1);
-        if (x < base + static_cast<int64_t>(n) * p.hu) {
-          const int rem = static_cast<int>(x - base);
-          const int i = rem / p.hu;
-          *head = rem - i * p.hu;
-          *seq = i < n0 ? __fns(b0, 0, i + 1) : 32 + __fns(b1, 0, i - n0 + 1);
-          *pair = level;
-          return true;
-        }
+      while (n > 0 && x >= base + static_cast<int64_t>(n) * p.hu) {
         base += static_cast<int64_t>(n) * p.hu;
+        longest(lane);
       }
-      return false;
-    }
-    for (; c0 < p.num_seqs; c0 += 32) {
-      const int n = pairs(p, c0 + lane);
-      int incl = n;
+      if (n == 0) return false;
+      *seq_out = seq;
+      pairs = n;
+      rem = static_cast<int>(x - base);
+    } else {
+      for (;; seq += 32) {
+        if (seq >= p.num_seqs) return false;
+        const int m = pairs_of(p, seq + lane);
+        int incl = m;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        const int64_t lo = base + static_cast<int64_t>(incl - m) * p.hu;
+        const int64_t hi = base + static_cast<int64_t>(incl) * p.hu;
+        const unsigned hit = __ballot_sync(0xffffffffu, x >= lo && x < hi);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          *seq_out = seq + src;
+          pairs = __shfl_sync(0xffffffffu, m, src);
+          rem = static_cast<int>(x - __shfl_sync(0xffffffffu, lo, src));
+          break;
+        }
+        base = __shfl_sync(0xffffffffu, hi, 31);
       }
-      const int64_t lo = base + static_cast<int64_t>(incl - n) * p.hu;
-      const int64_t hi = base + static_cast<int64_t>(incl) * p.hu;
-      const unsigned hit = __ballot_sync(0xffffffffu, x >= lo && x < hi);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        const int64_t first = __shfl_sync(0xffffffffu, lo, src);
-        const int ns = __shfl_sync(0xffffffffu, n, src);
-        const int rem = static_cast<int>(x - first);
-        *seq = c0 + src;
-        *pair = ns - 1 - rem / p.hu;
-        *head = rem % p.hu;
-        return true;
-      }
-      base = __shfl_sync(0xffffffffu, hi, 31);
     }
-    return false;
+    // head units per block: pairs * 2 * tpt tokens of K and V per KV head
+    const int64_t kv = static_cast<int64_t>(pairs) * 2 * p.tpt * p.kv_bytes;
+    const int per_kv = p.group / p.pg;
+    const int hb = static_cast<int>(
+        min(static_cast<int64_t>(p.hu), max(kBlockBytes / kv, static_cast<int64_t>(1)) * per_kv));
+    const int blk = rem / (pairs * hb);
+    rem -= blk * pairs * hb;
+    const int hn = min(hb, p.hu - blk * hb);
+    const int q = rem / hn;
+    *pair = pairs - 1 - q;
+    *head = blk * hb + rem - q * hn;
+    return true;
   }
 };
+
+// The launch's next item for this CTA: a request that the hardware answers
+// with the index of a waiting CTA, which it then does not start, or with none.
+__device__ __forceinline__ void clc_request(uint32_t dst, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+      "[%0], [%1];" ::"r"(dst),
+      "r"(bar)
+      : "memory");
+}
+// The answer's CTA index, or -1.
+__device__ __forceinline__ int clc_answer(uint32_t src) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(src)
+      : "memory");
+  return got ? static_cast<int>(x) : -1;
+}
 
 // cu_seqlens must start at 0, never decrease, end within the packed rows,
 // and no sequence may exceed max_seqlen.
@@ -313,6 +350,39 @@ __host__ __device__ __forceinline__ int64_t run_cost(int64_t total, int runs) {
 // from word 8 on 8 words per sequence: prefix length (0: none), the group's
 // first sequence, its size, 0, and its first cost position (int64).
 constexpr int kInfoWords = 8;
+
+// Warp-collective.
+__device__ inline void write_info(const Params &p, int lane, bool good, int64_t total) {
+  if (lane == 0) *reinterpret_cast<int64_t *>(p.ws_info) = run_cost(total, gridDim.x);
+  if (!good) {
+    for (int b = lane; b < p.num_seqs; b += 32)
+      p.ws_info[static_cast<int64_t>(b + 1) * kInfoWords] = 0;
+    return;
+  }
+  int64_t gbase = 0;
+  for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
+    const GroupGeom r = group_geom(p, g0 + lane);
+    int64_t incl = r.cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int64_t lo = gbase + incl - r.cost;
+    gbase = __shfl_sync(0xffffffffu, gbase + incl, 31);
+    for (int i = 0; i < 32 && g0 + i < p.num_groups; ++i) {
+      const int first = __shfl_sync(0xffffffffu, r.first, i);
+      const int n = __shfl_sync(0xffffffffu, r.n, i);
+      const int pre = __shfl_sync(0xffffffffu, r.prefix, i);
+      const int64_t at = __shfl_sync(0xffffffffu, lo, i);
+      for (int b = lane; b < n; b += 32) {
+        int32_t *w = p.ws_info + static_cast<int64_t>(first + b + 1) * kInfoWords;
+        *reinterpret_cast<int4 *>(w) = make_int4(pre, first, n, 0);
+        *reinterpret_cast<int64_t *>(w + 4) = at;
+      }
+    }
+  }
+}
 
 struct PrefixSched {
   int64_t x, xend, gbase;
@@ -444,12 +514,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n = 1;
       if ((i >= L::kPFull && i < L::kPFull + 2) || (i >= L::kOFree && i < L::kOFree + 2)) n = 4;
       if (i >= L::kMLFull && i < L::kMLFull + 2) n = 128;
+      if (i >= L::kKEmpty && i < L::kKEmpty + L::NK) n = 2;    // either stream
+      if (i >= L::kVEmpty && i < L::kVEmpty + L::NV) n = 2;
+      if (i >= L::kVFixed && i < L::kVFixed + L::NV) n = 4;    // the epilogue's warps
       if (i >= L::kItemEmpty && i < L::kItemEmpty + kItemRing) n = kItemTakers;
       mbar_init(bar(i), n);
     }
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kMmaWarp0) {
     tmem_alloc(smem_u32(const_cast<int *>(misc)), kTmemCols);
     tmem_relinquish();
   }
@@ -464,17 +537,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------- scheduler --
       bool ok = true;
       int base = 0, qbase = 0;
+      uint32_t tails = 0;  // parity of each V buffer's tails so far
       PackedSched ps;
       PrefixSched xs;
       if constexpr (PAGED) {
         int64_t total;
-        check_groups(p, lane, blockIdx.x == 0, &total);
+        const bool good = check_groups(p, lane, blockIdx.x == 0, &total);
         xs.init(p, total);
+        if (blockIdx.x == 0) write_info(p, lane, good, total);
       } else {
         if (blockIdx.x == 0 && !check_cu(p, lane) && lane == 0)
           raise_error(p.err, PA_DEVERR_CU_SEQLENS);
         ps.init(p, lane);
       }
+      int x = blockIdx.x;  // packed prompts: the item in hand
+      int asked = 0;       // ... and requests made for the next
       for (int j = 0;; ++j) {
         Item it;
         it.live = 0;
@@ -503,7 +580,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           int seq, pair, head;
-          if (ps.next(p, lane, &seq, &pair, &head)) {
+          bool found = false;
+          // Item j is taken when item j - 1 begins to load: early enough, and
+          // no CTA holds items that an idle one could run.
+          if (j > 0) ok = warp_wait(L::kBegun, (j - 1) & 1);
+          while (!found && x >= 0 && ok) {  // (a CTA beyond the last item has none)
+            if (j > 0) {
+              if (lane == 0) {
+                fence_proxy_async_smem();
+                mbar_arrive_expect_tx(bar(L::kNext), 16);
+                clc_request(smem_u32(smem + L::kNextOff), bar(L::kNext));
+              }
+              ok = __all_sync(0xffffffffu,
+                              mbar_wait_bounded(bar(L::kNext), asked & 1, p.wait_ns));
+              ++asked;
+              if (!ok) break;
+              x = clc_answer(smem_u32(smem + L::kNextOff));
+              __syncwarp();  // read by every lane before it is asked again
+              if (x < 0) break;
+            }
+            if (x < ps.base) ps.init(p, lane);
+            found = ps.find(p, x, lane, &seq, &pair, &head);
+            if (!found && j == 0) break;
+          }
+          if (found && ok) {
             it.live = 1;
             it.q0 = __ldg(p.cu + seq);
             it.ntok = __ldg(p.cu + seq + 1) - it.q0;
@@ -526,7 +626,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (it.live) {
           it.kvh = it.head0 / p.group;
-          if (it.key0 + it.nkv * kKeys > it.kend) it.flags |= kTail;
+          if (it.key0 + it.nkv * kKeys > it.kend) {
+            const int slot = (base + it.nkv - 1) % L::NV;
+            it.flags |= kTail | ((tails >> slot) & 1u ? kTailOdd : 0);
+            tails ^= 1u << slot;
+          }
           if (it.flags & kSingle) {
             // one query tile: its keys by turns on both streams; a single
             // K/V tile goes to either stream, by turns of the items
@@ -553,77 +657,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (!it.live) break;
       }
-      if (!ok && lane == 0) give_up();
-    } else if (warp == kFixWarp) {
-      // --------------------------------------------------------- fixer --
-      // K/V rows past an item's last key may hold anything (another
-      // sequence's rows, never-written pool rows, even NaN); their weights
-      // are 0, but 0 * NaN is NaN: V's are cleared once the tile has landed,
-      // before the P V that reads it (K's scores are masked).
-      if constexpr (PAGED) {
-        if (blockIdx.x == 0) {  // what the joining kernel needs
-          int64_t total;
-          const bool good = check_groups(p, lane, false, &total);
-          if (lane == 0) *reinterpret_cast<int64_t *>(p.ws_info) = run_cost(total, gridDim.x);
-          if (!good) {
-            for (int b = lane; b < p.num_seqs; b += 32)
-              p.ws_info[(b + 1) * kInfoWords] = 0;
-          } else {
-            int64_t gbase = 0;
-            for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
-              const GroupGeom r = group_geom(p, g0 + lane);
-              int64_t incl = r.cost;
-#pragma unroll
-              for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-              }
-              const int64_t lo = gbase + incl - r.cost;
-              gbase = __shfl_sync(0xffffffffu, gbase + incl, 31);
-              for (int i = 0; i < 32; ++i) {
-                const int first = __shfl_sync(0xffffffffu, r.first, i);
-                const int n = __shfl_sync(0xffffffffu, r.n, i);
-                const int pre = __shfl_sync(0xffffffffu, r.prefix, i);
-                const int64_t at = __shfl_sync(0xffffffffu, lo, i);
-                if (g0 + i >= p.num_groups) break;
-                for (int b = lane; b < n; b += 32) {
-                  int32_t *w = p.ws_info + static_cast<int64_t>(first + b + 1) * kInfoWords;
-                  *reinterpret_cast<int4 *>(w) = make_int4(pre, first, n, 0);
-                  *reinterpret_cast<int64_t *>(w + 4) = at;
-                }
-              }
-            }
-          }
-        }
-      }
-      // The load is waited for only once it is out (an earlier phase of the
-      // buffer would pass for it otherwise), one phase of kTailIn per tail
-      // in the buffer: the next one there needs this one cleared and used.
-      bool ok = true;
-      uint32_t par = 0;
-      for (int j = 0;; ++j) {
-        Item it;
-        ok = peek_item(j, &it);
-        drop_item(j);
-        if (!ok || !it.live) break;
-        if (!(it.flags & kTail)) continue;
-        const int n = it.base + it.nkv - 1, slot = n % L::NV;
-        ok = warp_wait(L::kTailIn + slot, (par >> slot) & 1);
-        par ^= 1u << slot;
-        ok = ok && mbar_wait_bounded(bar(L::kVFull + slot), (n / L::NV) & 1, p.wait_ns);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        uint8_t *vt = smem + L::kVOff + slot * L::kTile;
-        const int first = it.kend - it.key0 - (it.nkv - 1) * kKeys;  // 1..127
-        for (int i = lane; i < (kKeys - first) * (D / 8); i += 32) {
-          const int row = first + i / (D / 8), c16 = i % (D / 8);
-          *reinterpret_cast<uint4 *>(vt + (c16 >> 3) * kHalf + row * 128 + (c16 & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();  // generic writes before the tensor core reads
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kVFixed + slot));
-      }
+      // a request that was given up on still lands before the CTA leaves
+      if (asked > 0 && lane == 0) mbar_wait_bounded(bar(L::kNext), (asked - 1) & 1);
       if (!ok && lane == 0) give_up();
     } else if (warp == kTmaWarp) {
       // ----------------------------------------------------------- TMA --
@@ -686,6 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item it;
         ok = peek_item(j, &it);
         if (!ok || !it.live || misc[1]) break;
+        if (lane == 0) mbar_arrive(bar(L::kBegun));
         const int t_first = it.cnt[0] > 0 ? 0 : 1;
         const bool two = it.cnt[0] > 0 && it.cnt[1] > 0;
         // PAGED: this lane's block ids, the next tile's in flight
@@ -741,20 +777,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else {
       // ----------------------------------------------------------- MMA --
-      // The whole warp runs this loop; MMAs and commits are issued by one
-      // elected lane.  The tensor core runs one thread's MMAs in order, so
-      // Q K^T may overwrite the S columns that the P V before it reads.
-      // Issuing runs at the tensor core's own pace, so every cycle this warp
-      // spends between two issues is one the tensor core idles: a step's
-      // bookkeeping and its waits for K and V are done before the wait for P,
-      // and P V and the stream's next Q K^T go out in one block after it
-      // (separate waits and blocks measured 2700 cycles per tile step
-      // instead of 1024: 930 TFLOP/s on two prompts of 16384).
+      // One warp per stream.  The whole warp runs the loop; MMAs and commits
+      // are issued by one elected lane.  The tensor core runs one thread's
+      // MMAs in order, so Q K^T may overwrite the S columns that the P V
+      // before it reads.  Issuing runs at the tensor core's own pace, so a
+      // step's waits and bookkeeping stand between its issues; with a warp per
+      // stream the other stream's MMAs run meanwhile (one warp for both
+      // measured 1740 cycles per tile step on long prompts, 1064 of them
+      // issuing), and P V and the stream's next Q K^T go out in one block.
+      //
+      // Each stream accounts for every K and V buffer use, in ring order: by
+      // a commit after the MMAs that read it, or, for a tile it does not use,
+      // by an arrival once the tile has landed (an earlier one would count
+      // towards the buffer's use before).
+      const int t = warp - kMmaWarp0;
       const uint32_t id_qk = idesc_f16(E::kBF16, 128, 128, false) | (p.negate << 13);
       const uint32_t id_pv = idesc_f16(E::kBF16, 128, D, true);
       const uint64_t q_desc0 = sdesc_sw128(smem_u32(smem) + L::kQOff, 16, 1024);
       const uint64_t k_desc0 = sdesc_sw128(smem_u32(smem) + L::kKOff, 16, 1024);
       const uint64_t v_desc0 = sdesc_sw128(smem_u32(smem) + L::kVOff, kHalf, 1024);
+      const uint32_t s_tm = tbase + t * 128, o_tm = tbase + 256 + t * 128;
       bool ok = true;
       // Every lane asks once; only a wait that is not over yet goes the long way.
       auto ready = [&](int b, uint32_t parity) {
@@ -764,47 +806,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         return ready(b, parity) || warp_wait(b, parity);
       };
       constexpr int kNone = 0x7fffffff;
-      // Per stream: the step whose Q K^T is issued and whose P V is to come
-      // (ring position pn, or kNone), the ring position np of the Q K^T after
-      // it where that is known (kNone: the item is exhausted), and the place
-      // in the item list.
-      struct Stream {
-        int pn, np;
-        bool pfirst, plast;       // the pending step is its item's first / last
-        int j, end;               // item the fields belong to, its end
-        int step, left, q;        // ring step, Q K^T still to issue, Q buffer
-        bool first, ended;        // the next Q K^T is the item's first
-        int items, psteps;        // items begun (P V), P tiles taken
-      } st[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        st[t].pn = st[t].np = kNone;
-        st[t].pfirst = st[t].plast = st[t].first = st[t].ended = false;
-        st[t].j = -1;
-        st[t].end = st[t].left = st[t].q = st[t].items = st[t].psteps = 0;
-        st[t].step = 1;
-      }
-      // An exhausted stream walks on to the items that begin by `limit`.
-      auto advance = [&](Stream &s, int t, int limit) {
-        while (!s.ended && s.left == 0 && s.end <= limit) {
-          Item it;
-          if (!peek_item(s.j + 1, &it)) ok = false;
-          if (!ok || !it.live) {
-            s.ended = true;
-            return;
-          }
-          ++s.j;
-          s.end = it.base + it.nkv;
-          s.left = it.cnt[t];
-          s.np = s.left > 0 ? use_first(it, t) : kNone;
-          s.step = use_step(it);
-          s.first = true;
-          s.q = it.qbase + (t == 1 && it.cnt[0] > 0 ? 1 : 0);
+      int j = -1;              // the item whose tiles are being issued ...
+      int end = 0, left = 0;   // ... its end, its Q K^T still to issue
+      int np = kNone;          // ring position of the next Q K^T, where it is known
+      int step = 1, q = 0;     // ring step and Q buffer of the item
+      bool first = false, tail = false, odd = false, ended = false;
+      int kdone = 0, vdone = 0;  // K and V uses accounted for
+      int items = 0, psteps = 0; // items begun (P V), P tiles taken
+      // the step whose Q K^T is out and whose P V is to come
+      int pn = kNone;
+      bool pfirst = false, plast = false, ptail = false, podd = false;
+
+      // Moves on to item j + 1 (exhausted stream).
+      auto next_item = [&]() {
+        Item it;
+        ok = peek_item(j + 1, &it);
+        if (j >= 0) drop_item(j);
+        ++j;
+        if (!ok || !it.live) {
+          ended = true;
+          if (ok) drop_item(j);
+          np = kNone;
+          return;
+        }
+        end = it.base + it.nkv;
+        left = it.cnt[t];
+        np = left > 0 ? use_first(it, t) : kNone;
+        step = use_step(it);
+        first = true;
+        tail = (it.flags & kTail) != 0;
+        odd = (it.flags & kTailOdd) != 0;
+        q = it.qbase + (t == 1 && it.cnt[0] > 0 ? 1 : 0);
+      };
+      // Accounts for the tiles before ring position m that this stream does
+      // not use.
+      auto skip_to = [&](int m) {
+        while (ok && kdone < m) {
+          ok = wait(L::kKFull + kdone % L::NK, (kdone / L::NK) & 1);
+          if (lane == 0) mbar_arrive(bar(L::kKEmpty + kdone % L::NK));
+          ++kdone;
+        }
+        while (ok && vdone < m) {
+          ok = wait(L::kVFull + vdone % L::NV, (vdone / L::NV) & 1);
+          if (lane == 0) mbar_arrive(bar(L::kVEmpty + vdone % L::NV));
+          ++vdone;
         }
       };
-      // The elected lane's part of S_t = Q_t K_n^T.
-      auto issue_qk = [&](const Stream &s, int t, int n) {
-        const int qs = s.q % L::NQ;
+      // The elected lane's part of S = Q K_n^T.
+      auto issue_qk = [&](int n) {
+        const int qs = q % L::NQ;
         const uint64_t qd = q_desc0 + static_cast<uint64_t>(qs) * (L::kTile >> 4);
         const uint64_t kd = k_desc0 + static_cast<uint64_t>(n % L::NK) * (L::kTile >> 4);
         // K step k: 16 columns = 32 bytes into a 128-byte swizzled row, the
@@ -812,116 +862,97 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-          umma_f16_ss(tbase + t * 128, qd + off, kd + off, id_qk, k > 0 ? 1u : 0u);
+          umma_f16_ss(s_tm, qd + off, kd + off, id_qk, k > 0 ? 1u : 0u);
         }
         umma_commit(bar(L::kSFull + t));
-        if (s.left == 1) umma_commit(bar(L::kQEmpty + qs));
+        umma_commit(bar(L::kKEmpty + n % L::NK));
+        if (left == 1) umma_commit(bar(L::kQEmpty + qs));
       };
       // ... and the bookkeeping after it.
-      auto qk_issued = [&](Stream &s, int n) {
-        s.pn = n;
-        s.pfirst = s.first;
-        s.first = false;
-        s.plast = --s.left == 0;
-        s.np = s.plast ? kNone : n + s.step;
+      auto qk_issued = [&](int n) {
+        pn = n;
+        pfirst = first;
+        first = false;
+        plast = --left == 0;
+        ptail = tail && n + 1 == end;
+        podd = odd;
+        np = plast ? kNone : n + step;
       };
-      auto wait_qk = [&](const Stream &s, int n) {  // the operands of Q K_n^T
-        if (s.first && !wait(L::kQFull + s.q % L::NQ, (s.q / L::NQ) & 1)) return false;
-        return wait(L::kKFull + n % L::NK, (n / L::NK) & 1);
-      };
-      int r = -1, r_end = 0;         // the item that holds ring position n
-      bool r_tail = false;
-      uint32_t fix_par = 0;          // parity of each V buffer's next clearing
-      for (int n = -1; ok; ++n) {
-        if (n == r_end) {            // the next item (or the end of the list)
-          if (r >= 0) drop_item(r);
-          Item it;
-          ok = peek_item(++r, &it);
-          if (!ok || !it.live) {
-            if (ok) drop_item(r);
-            break;
+
+      while (ok) {
+        // P V of the pending step, and the next Q K^T with it where its
+        // operands are there already.
+        if (pn != kNone) {
+          const int n = pn;
+          if (left == 0) next_item();  // where the stream goes on, if at once
+          bool along = false;
+          if (ok && np <= n + 2) {
+            along = ready(L::kKFull + np % L::NK, (np / L::NK) & 1);
+            if (along && first) along = ready(L::kQFull + q % L::NQ, (q / L::NQ) & 1);
           }
-          r_end = it.base + it.nkv;
-          r_tail = (it.flags & kTail) != 0;
-        }
-        if (n >= 0) {
-          ok = wait(L::kVFull + n % L::NV, (n / L::NV) & 1);
-          if (ok && r_tail && n + 1 == r_end) {
-            ok = wait(L::kVFixed + n % L::NV, (fix_par >> (n % L::NV)) & 1);
-            fix_par ^= 1u << (n % L::NV);
+          if (ok && pfirst) {  // O of the stream's previous item has been read
+            if (items > 0) ok = wait(L::kOFree + t, (items - 1) & 1);
+            ++items;
           }
-        }
-        if (!ok) break;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          Stream &s = st[t];
-          if (!ok || s.pn != n || n < 0) continue;
-          if (s.pfirst) {  // O of the stream's previous item has been read
-            if (s.items > 0) ok = wait(L::kOFree + t, (s.items - 1) & 1);
-            ++s.items;
+          if (ok) ok = wait(L::kVFull + n % L::NV, (n / L::NV) & 1);
+          if (ok && ptail) {
+            // (the buffer's tails before it have been cleared and used)
+            ok = wait(L::kVFixed + n % L::NV, podd ? 1 : 0);
           }
-          // the stream's next Q K^T goes along if its K is there already
-          const bool along = s.np == n + 1 &&
-                             ready(L::kKFull + (n + 1) % L::NK, ((n + 1) / L::NK) & 1);
-          const uint64_t vd = v_desc0 + static_cast<uint64_t>(n % L::NV) * (L::kTile >> 4);
-          const uint32_t acc0 = s.pfirst ? 0u : 1u;
-          const bool last = s.plast;
-          if (!ok) continue;
-          ok = wait(L::kPFull + t, s.psteps & 1);
-          if (!ok) continue;
+          if (ok) ok = wait(L::kPFull + t, psteps & 1);
+          if (!ok) break;
+          ++psteps;
           tc_fence_after();
+          const uint64_t vd = v_desc0 + static_cast<uint64_t>(n % L::NV) * (L::kTile >> 4);
+          const uint32_t acc0 = pfirst ? 0u : 1u;
           if (elect_one()) {
-            // O_t += P_t V_n, P_t from TMEM; K step k: 16 keys = 16 rows of
-            // 128 bytes of the MN-major V tile
+            // O += P V_n, P from TMEM; K step k: 16 keys = 16 rows of 128
+            // bytes of the MN-major V tile
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              umma_f16_ts(tbase + 256 + t * 128, tbase + t * 128 + 8 * k, vd + ((k * 2048) >> 4),
-                          id_pv, k > 0 ? 1u : acc0);
-            if (last) umma_commit(bar(L::kOFull + t));
-            if (along) issue_qk(s, t, n + 1);
+              umma_f16_ts(o_tm, s_tm + 8 * k, vd + ((k * 2048) >> 4), id_pv, k > 0 ? 1u : acc0);
+            if (plast) umma_commit(bar(L::kOFull + t));
+            umma_commit(bar(L::kVEmpty + n % L::NV));
+            if (along) issue_qk(np);
           }
           __syncwarp();
-          ++s.psteps;
-          s.pn = kNone;
-          if (along) qk_issued(s, n + 1);
+          vdone = n + 1;
+          pn = kNone;
+          if (along) {
+            const int m = np;
+            qk_issued(m);
+            skip_to(m);       // the tiles in between
+            kdone = m + 1;
+            continue;
+          }
+        }
+        // Otherwise walk to the next tile the stream uses.
+        while (ok && !ended && left == 0) {
+          skip_to(end);
+          if (ok) next_item();
+        }
+        if (ended) {
+          skip_to(end);       // of the last item, which is over
+          break;
         }
         if (!ok) break;
-        // Streams without a Q K^T out: tile n + 1 (its K was late, or the
-        // stream does not use tile n), then n + 2.
-        if (st[0].pn == kNone || st[1].pn == kNone) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (st[t].pn == kNone) advance(st[t], t, n + 2);
-#pragma unroll
-          for (int m = 1; m <= 2; ++m)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              Stream &s = st[t];
-              if (!ok || s.pn != kNone || s.np != n + m) continue;
-              ok = wait_qk(s, n + m);
-              if (!ok) continue;
-              tc_fence_after();
-              if (elect_one()) issue_qk(s, t, n + m);
-              __syncwarp();
-              qk_issued(s, n + m);
-            }
-          if (!ok) break;
-        }
-        // Tile n's V has been used, and every Q K^T of tile n + 1, if there is
-        // one, has been issued (a stream still behind it has no use of it).
-        const bool next_tile = n + 1 < r_end || st[0].end > n + 1 || st[1].end > n + 1;
-        if (elect_one()) {
-          if (n >= 0) umma_commit(bar(L::kVEmpty + n % L::NV));
-          if (next_tile) umma_commit(bar(L::kKEmpty + (n + 1) % L::NK));
-        }
+        const int m = np;
+        skip_to(m);
+        if (ok && first) ok = wait(L::kQFull + q % L::NQ, (q / L::NQ) & 1);
+        if (ok) ok = wait(L::kKFull + m % L::NK, (m / L::NK) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) issue_qk(m);
         __syncwarp();
+        qk_issued(m);
+        kdone = m + 1;
       }
       if (!ok && lane == 0) give_up();
       // Every MMA issued above has completed once this barrier fires (the
       // full bound: TMEM is freed after it).
-      if (elect_one()) umma_commit(bar(L::kFin));
+      if (elect_one()) umma_commit(bar(L::kFin + t));
       __syncwarp();
-      if (lane == 0) mbar_wait_bounded(bar(L::kFin), 0);
+      if (lane == 0) mbar_wait_bounded(bar(L::kFin + t), 0);
       __syncwarp();
     }
   } else if (warp >= kEpiWarp0) {
@@ -939,6 +970,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok || !it.live) {
         drop_item(j);
         break;
+      }
+      if (it.flags & kTail) {
+        // V rows past the item's last key may hold anything (another
+        // sequence's rows, never-written pool rows, even NaN); their weights
+        // are 0, but 0 * NaN is NaN: they are cleared once the tile has
+        // landed, before the P V that reads it (K's scores are masked).  The
+        // load is waited for only once it is out (an earlier phase of the
+        // buffer would pass for it otherwise), one phase of kTailIn per tail
+        // in the buffer: the next one there needs this one cleared and used.
+        const int n = it.base + it.nkv - 1, slot = n % L::NV;
+        ok = mbar_wait_bounded(bar(L::kTailIn + slot), (it.flags & kTailOdd) ? 1 : 0, p.wait_ns);
+        ok = ok && mbar_wait_bounded(bar(L::kVFull + slot), (n / L::NV) & 1, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          drop_item(j);
+          break;
+        }
+        uint8_t *vt = smem + L::kVOff + slot * L::kTile;
+        const int first = it.kend - it.key0 - (it.nkv - 1) * kKeys;  // 1..127
+        for (int i = r; i < (kKeys - first) * (D / 8); i += 128) {
+          const int row = first + i / (D / 8), c16 = i % (D / 8);
+          *reinterpret_cast<uint4 *>(vt + (c16 >> 3) * kHalf + row * 128 + (c16 & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();  // generic writes before the tensor core reads
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kVFixed + slot));
       }
       const bool single = (it.flags & kSingle) != 0;
       // one pass per query tile: both streams' halves of a single tile, or
@@ -1139,7 +1197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kMmaWarp0) {
     tc_fence_after();
     tmem_dealloc(tbase, kTmemCols);
   }
