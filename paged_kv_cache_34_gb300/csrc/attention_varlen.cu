@@ -27,7 +27,7 @@ cudaError_t launch_attention_varlen(const AttentionVarlenArgs &a, cudaStream_t s
   p.total = a.total;
   p.max_seqlen = a.max_seqlen;
   p.err = a.d_error;
-  p.wait_ns = a.wait_ns;
+  p.wait_ns = flash::wait_limit(a.wait_ns);
   p.kv_bytes = 4 * a.head_dim;
   // One CTA per item, pairs of query tiles x head units: at most one pair of
   // a sequence is partly filled.

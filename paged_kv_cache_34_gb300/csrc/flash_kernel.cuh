@@ -149,14 +149,44 @@ struct Params {
   float *ws_o, *ws_ml;
   int32_t *ws_info;
   int32_t *err;
-  uint64_t wait_ns;
+  uint32_t wait_ns;
 };
+
+// The waits' bound for a launch (at most the 2 s of the library).
+inline uint32_t wait_limit(uint64_t ns) {
+  return static_cast<uint32_t>(ns < kWaitLimitNs ? ns : kWaitLimitNs);
+}
 
 // Query tiles of a sequence or group of n rows (tokens).
 __device__ __forceinline__ int tiles_of(const Params &p, int n) {
   return n > 0 ? (n - 1) / p.tpt + 1 : 0;
 }
 
+// A pipeline wait, bounded in time.  In few instructions (a 32-bit timer; the
+// bound is at most 2 s): this kernel has some 25 waits, its roles run their
+// parts of it side by side, and what does not fit in the SM's instruction
+// cache is paid for at every item.
+__device__ __forceinline__ uint32_t timer_lo_ns() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, uint32_t limit_ns) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint32_t start = timer_lo_ns();
+    do {
+      ok = mbar_try_wait(bar, parity);
+    } while (!ok && timer_lo_ns() - start <= limit_ns);
+  }
+  return ok;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // ------------------------------------------------------ work distribution --
 // Packed prompts.  The launch has (at least) one CTA per item; the ones that
 // run take over the items of those still waiting (cluster launch control), so
@@ -165,8 +195,8 @@ __device__ __forceinline__ int tiles_of(const Params &p, int n) {
 // by falling length (up to 64 of them, else as they come), within one the
 // head units in blocks whose K and V stay in L2, within a block the tile pairs
 // from the last, heaviest one down, then the block's head units.  (All
-// sequences' heaviest pairs first read K and V again for each pair: 190 us
-// instead of 146 on 16 prompts of 1000 tokens, 32/32 heads.)
+// sequences' heaviest pairs first would read K and V from memory again for
+// each pair.)
 constexpr int64_t kBlockBytes = 40 << 20;  // K and V of a head block: a third of L2
 
 // Warp-collective; each call goes on from the one before while x grows.
@@ -460,6 +490,10 @@ __device__ __forceinline__ Item load_item(const volatile int *w) {
 __device__ __forceinline__ int use_first(const Item &it, int t) {
   return it.base + ((it.flags & kTurns) ? t : 0);
 }
+// (without a runtime index, which would put the item into local memory)
+__device__ __forceinline__ int use_count(const Item &it, int t) {
+  return t ? it.cnt[1] : it.cnt[0];
+}
 __device__ __forceinline__ int use_step(const Item &it) { return (it.flags & kTurns) ? 2 : 1; }
 
 // -------------------------------------------------------------- the kernel --
@@ -486,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Lane 0 waits, the warp learns the outcome.
   auto warp_wait = [&](int b, uint32_t parity) {
     bool ok = true;
-    if (lane == 0) ok = mbar_wait_bounded(bar(b), parity, p.wait_ns);
+    if (lane == 0) ok = wait_for(bar(b), parity, p.wait_ns);
     return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
   };
   auto slot_words = [&](int j) { return items + (j % kItemRing) * L::kItemWords; };
@@ -592,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 clc_request(smem_u32(smem + L::kNextOff), bar(L::kNext));
               }
               ok = __all_sync(0xffffffffu,
-                              mbar_wait_bounded(bar(L::kNext), asked & 1, p.wait_ns));
+                              wait_for(bar(L::kNext), asked & 1, p.wait_ns));
               ++asked;
               if (!ok) break;
               x = clc_answer(smem_u32(smem + L::kNextOff));
@@ -658,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!it.live) break;
       }
       // a request that was given up on still lands before the CTA leaves
-      if (asked > 0 && lane == 0) mbar_wait_bounded(bar(L::kNext), (asked - 1) & 1);
+      if (asked > 0 && lane == 0) wait_for(bar(L::kNext), (asked - 1) & 1, static_cast<uint32_t>(kWaitLimitNs));
       if (!ok && lane == 0) give_up();
     } else if (warp == kTmaWarp) {
       // ----------------------------------------------------------- TMA --
@@ -731,7 +765,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           return (lane < nbox && i < it.nkv && key < it.kend) ? __ldg(bt + key / bs) : -1;
         };
         int id = PAGED ? load_id(0) : 0;
-        ok = load_q(it, t_first, it.qbase);
+        // (the last item's V tail first: nothing of this item holds it back)
+        if (v_pos >= 0) {
+          ok = load_v();
+          v_pos = -1;
+        }
+        if (ok) ok = load_q(it, t_first, it.qbase);
         for (int i = 0; ok && i < it.nkv; ++i) {
           const int id_next = PAGED ? load_id(i + 1) : 0;
           int row;
@@ -768,11 +807,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Do not leave while copies this CTA issued may still land.
       if (lane == 0) {
         for (int n = nq - 1; n >= 0 && n >= nq - L::NQ; --n)
-          mbar_wait_bounded(bar(L::kQFull + n % L::NQ), (n / L::NQ) & 1);
+          wait_for(bar(L::kQFull + n % L::NQ), (n / L::NQ) & 1, static_cast<uint32_t>(kWaitLimitNs));
         for (int n = nk - 1; n >= 0 && n >= nk - L::NK; --n)
-          mbar_wait_bounded(bar(L::kKFull + n % L::NK), (n / L::NK) & 1);
+          wait_for(bar(L::kKFull + n % L::NK), (n / L::NK) & 1, static_cast<uint32_t>(kWaitLimitNs));
         for (int n = nv - 1; n >= 0 && n >= nv - L::NV; --n)
-          mbar_wait_bounded(bar(L::kVFull + n % L::NV), (n / L::NV) & 1);
+          wait_for(bar(L::kVFull + n % L::NV), (n / L::NV) & 1, static_cast<uint32_t>(kWaitLimitNs));
       }
       __syncwarp();
     } else {
@@ -830,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return;
         }
         end = it.base + it.nkv;
-        left = it.cnt[t];
+        left = use_count(it, t);
         np = left > 0 ? use_first(it, t) : kNone;
         step = use_step(it);
         first = true;
@@ -952,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // full bound: TMEM is freed after it).
       if (elect_one()) umma_commit(bar(L::kFin + t));
       __syncwarp();
-      if (lane == 0) mbar_wait_bounded(bar(L::kFin + t), 0);
+      if (lane == 0) wait_for(bar(L::kFin + t), 0, static_cast<uint32_t>(kWaitLimitNs));
       __syncwarp();
     }
   } else if (warp >= kEpiWarp0) {
@@ -980,8 +1019,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // buffer would pass for it otherwise), one phase of kTailIn per tail
         // in the buffer: the next one there needs this one cleared and used.
         const int n = it.base + it.nkv - 1, slot = n % L::NV;
-        ok = mbar_wait_bounded(bar(L::kTailIn + slot), (it.flags & kTailOdd) ? 1 : 0, p.wait_ns);
-        ok = ok && mbar_wait_bounded(bar(L::kVFull + slot), (n / L::NV) & 1, p.wait_ns);
+        ok = wait_for(bar(L::kTailIn + slot), (it.flags & kTailOdd) ? 1 : 0, p.wait_ns);
+        ok = ok && wait_for(bar(L::kVFull + slot), (n / L::NV) & 1, p.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
           drop_item(j);
@@ -1009,8 +1048,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!use[t]) continue;
-          ok = ok && mbar_wait_bounded(bar(L::kOFull + t), done[t] & 1, p.wait_ns);
-          ok = ok && mbar_wait_bounded(bar(L::kMLFull + t), done[t] & 1, p.wait_ns);
+          ok = ok && wait_for(bar(L::kOFull + t), done[t] & 1, p.wait_ns);
+          ok = ok && wait_for(bar(L::kMLFull + t), done[t] & 1, p.wait_ns);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           m[t] = s_m[t * 128 + r];
@@ -1104,7 +1143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = peek_item(j, &it);
       drop_item(j);
       if (!ok || !it.live) break;
-      const int cnt = it.cnt[t];
+      const int cnt = use_count(it, t);
       if (cnt == 0) continue;
       const int tok = it.tok0 + ((it.flags & kSingle) ? 0 : t * p.tpt) + tl;
       // the row's last visible key (rows outside the batch see what there is)
@@ -1120,27 +1159,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int bstep = use_step(it) * kKeys;
       float m_ref = -INFINITY, l = 0.f;
       for (int i = 0; i < cnt; ++i, ++n, bound -= bstep) {
-        ok = mbar_wait_bounded(bar(L::kSFull + t), n & 1, p.wait_ns);
+        ok = wait_for(bar(L::kSFull + t), n & 1, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
+        // Columns past `bound` are hidden: where a tile has any, its S goes
+        // through a loop (not unrolled, for the instruction cache's sake).
+        if (__any_sync(0xffffffffu, bound < kKeys - 1)) {
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += 32) {
+            if (!__any_sync(0xffffffffu, bound < c + 31)) continue;
+            uint32_t h[32];
+            tmem_ld32(s_tm + c, h);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (k > bound - c) h[k] = __float_as_uint(-INFINITY);
+            tmem_st32(s_tm + c, h);
+          }
+          tmem_wait_st();
+        }
         // The whole S row in one TMEM round trip.
         uint32_t v[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           tmem_ld32(s_tm + c * 32, *reinterpret_cast<uint32_t(*)[32]>(v + c * 32));
         tmem_wait_ld();
-        if (bound < kKeys - 1) {  // columns 0..bound are visible
+        float mx[4];  // raw scores (the factor is positive), as a tree
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c > bound) v[c] = __float_as_uint(-INFINITY);
-        }
-        float mx[8];  // raw scores (the factor is positive), as a tree
+        for (int c = 0; c < 4; ++c)
+          mx[c] = max3(__uint_as_float(v[c]), __uint_as_float(v[4 + c]), __uint_as_float(v[8 + c]));
 #pragma unroll
-        for (int c = 0; c < 8; ++c) mx[c] = __uint_as_float(v[c]);
+        for (int c = 12; c + 7 < 128; c += 8)
 #pragma unroll
-        for (int c = 8; c < 128; ++c) mx[c & 7] = fmaxf(mx[c & 7], __uint_as_float(v[c]));
-        const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                               fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sl;
+          for (int k = 0; k < 4; ++k)
+            mx[k] = max3(mx[k], __uint_as_float(v[c + k]), __uint_as_float(v[c + 4 + k]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(v[124 + k]));
+        const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl;
         const bool raise = mt > m_ref + kRescaleThreshold;  // false for a fully masked row
         const float m_new = raise ? mt : m_ref;
         const float corr = raise ? fast_exp2(m_ref - m_new) : 1.f;
@@ -1166,7 +1221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i > 0 && __any_sync(0xffffffffu, raise)) {
           // O holds exactly the sum so far: S(n) being complete means Q K^T
           // of this tile ran, which was issued after the P V before it.
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(o_tm + c * 32, o);
