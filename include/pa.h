@@ -18,7 +18,8 @@
  * over FP8 (E4M3) pools; pa_copy_blocks copies whole blocks (copy-on-write).
  * pa_build_tables forms a step's block tables, slots and cumulative lengths
  * from request lengths; pa_attention_varlen is the attention of packed
- * prompts straight from their K/V rows, without a cache.
+ * prompts straight from their K/V rows, without a cache; pa_decode_shared is
+ * pa_decode for a batch whose groups share a prefix, read once per group.
  *
  * Sources (web pages on paged KV caches, cited by page and section):
  *   [SKILL] cannbot-skills "model-infer-kvcache" skill page: §3.1 physical
@@ -605,6 +606,55 @@ pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *que
                               int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                               float scale, int32_t causal, pa_dtype dtype, int32_t *d_error,
                               void *stream);
+
+/*
+ * pa_decode_shared -- pa_decode for a batch whose groups of sequences share a
+ * prefix (requests forked from one prompt hold the same blocks, [ATB]): the
+ * prefix's K and V are read once for its whole group.
+ *
+ * Group g is sequences group_starts[g] .. group_starts[g+1]-1; the first
+ * P = prefix_lens[g] keys and values of each of them are those of the group's
+ * FIRST sequence's block_table row.  Sequence b of context_lens[b] = L tokens
+ * reads its own row from position P on (the whole block that holds position
+ * P must be its own or shared; what it holds before P is not used), and only
+ * the first L positions altogether: with L <= P all of them are the prefix's.
+ * The output is that of pa_decode where the rows name the same tokens, up to
+ * the order of fp32 sums.
+ *
+ *   group_starts   int32 [num_groups + 1]: starts at 0, never decreases, ends
+ *                  at num_seqs (groups of one sequence, and empty ones, are
+ *                  fine).
+ *   prefix_lens    int32 [num_groups], tokens; any length, 0 for none.  The
+ *                  first sequence's row must hold ceil(P / block_size) valid
+ *                  entries, whatever that sequence's own length.
+ *   max_context_len, max_prefix_len   host upper bounds.
+ * All other arguments as for pa_decode, without its partition size.
+ * group_starts that is none sets PA_DEVERR_CU_SEQLENS, a prefix length that
+ * is negative, beyond max_prefix_len or beyond the table sets
+ * PA_DEVERR_CONTEXT; sequences concerned are attended over their own rows
+ * alone, like pa_decode.  A bad block id sets PA_DEVERR_BLOCK_ID and its
+ * piece of the context adds nothing.
+ * The workspace (256-byte aligned) is of pa_decode_shared_plan's size for the
+ * same shape.  Without groups, or where num_seqs * num_kv_heads *
+ * max_context_len reaches 2^30 (and a GQA group of more than 16 heads counts
+ * once per 16), the call is pa_decode.
+ * Supported: 16-bit pools; head_dim 64 or 128; block_size 8, 16, 32, 64 or
+ * 128; any num_q_heads % num_kv_heads == 0.
+ */
+pa_status pa_decode_shared_plan(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
+                                int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
+                                int32_t max_prefix_len, size_t *workspace_bytes_out);
+
+pa_status pa_decode_shared(void *out, int64_t out_row_stride, const void *query,
+                           int64_t q_row_stride, const void *key_cache, const void *value_cache,
+                           const int32_t *block_table, int64_t block_table_stride,
+                           int32_t max_blocks_per_seq, const int32_t *context_lens,
+                           const int32_t *group_starts, const int32_t *prefix_lens,
+                           int32_t num_groups, int32_t num_seqs, int32_t num_q_heads,
+                           int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                           int64_t num_blocks, float scale, int32_t max_context_len,
+                           int32_t max_prefix_len, void *workspace, size_t workspace_bytes,
+                           pa_dtype dtype, int32_t *d_error, void *stream);
 
 #ifdef __cplusplus
 }

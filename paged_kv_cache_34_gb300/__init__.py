@@ -16,6 +16,7 @@ first call raises.
     pa_build_tables       a step's block tables, slots, positions and cumulative
                           lengths from request lengths
     pa_attention_varlen   causal attention of packed prompts from their K/V rows
+    pa_decode_shared      decode of a batch whose groups share a prefix
 
 Build the library with ``python -m paged_kv_cache_34_gb300.build``.
 """
@@ -31,7 +32,7 @@ __all__ = ["pa_reshape_and_cache", "pa_decode", "pa_decode_plan", "pa_decode_wri
            "pa_prefill_varlen", "pa_reshape_and_cache_int8", "pa_decode_int8",
            "pa_decode_write_int8", "pa_reshape_and_cache_fp8", "pa_decode_fp8",
            "pa_decode_write_fp8", "pa_copy_blocks", "pa_build_tables",
-           "pa_attention_varlen", "PaError",
+           "pa_attention_varlen", "pa_decode_shared", "pa_decode_shared_plan", "PaError",
            "library", "DEVERR_SLOT", "DEVERR_BLOCK_ID", "DEVERR_CU_SEQLENS",
            "DEVERR_CONTEXT", "DEVERR_TIMEOUT", "DEVERR_SCALE", "DEVERR_NO_BLOCKS",
            "LIB_PATH"]
@@ -105,6 +106,12 @@ def library(path: str | None = None):
         lib.pa_attention_varlen.argtypes = [V, I64, V, I64, V, V, I64, V, I32, I32, I32, I32,
                                             I32, I32, F, I32, c.c_int, V, V]
         lib.pa_attention_varlen.restype = c.c_int
+        lib.pa_decode_shared_plan.argtypes = [I32] * 7 + [c.POINTER(SZ)]
+        lib.pa_decode_shared_plan.restype = c.c_int
+        lib.pa_decode_shared.argtypes = [V, I64, V, I64, V, V, V, I64, I32, V, V, V, I32, I32,
+                                         I32, I32, I32, I32, I64, F, I32, I32, V, SZ, c.c_int,
+                                         V, V]
+        lib.pa_decode_shared.restype = c.c_int
         lib.pa_decode_int8.argtypes = [V, I64, V, I64, V, V, V, I64, I32, V, I32, I32, I32,
                                        I32, I32, I64, V, V, F, I32, I32, V, SZ, c.c_int, V, V]
         lib.pa_decode_int8.restype = c.c_int
@@ -524,4 +531,61 @@ def pa_attention_varlen(out, query, key, value, cu_seqlens, *, scale, max_seqlen
                                  None if d_error is None else d_error.data_ptr(),
                                  _stream(stream))
     _check(lib, st, "pa_attention_varlen")
+    return out
+
+
+def pa_decode_shared_plan(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim,
+                          max_context_len, max_prefix_len, lib=None):
+    """The workspace bytes pa_decode_shared needs for this shape."""
+    lib = lib or library()
+    ws = ctypes.c_size_t(0)
+    st = lib.pa_decode_shared_plan(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim,
+                                   int(max_context_len), int(max_prefix_len), ctypes.byref(ws))
+    _check(lib, st, "pa_decode_shared_plan")
+    return ws.value
+
+
+def pa_decode_shared(out, query, key_cache, value_cache, block_table, context_lens, group_starts,
+                     prefix_lens, *, scale, max_context_len, max_prefix_len, workspace=None,
+                     d_error=None, stream=None, lib=None):
+    """pa_decode for a batch whose groups share a prefix: group g is sequences
+    group_starts[g] .. group_starts[g+1]-1 (int32 [G+1]); the first
+    prefix_lens[g] (int32 [G]) tokens of each are those of its first sequence's
+    block_table row and are read once for the group.  ``max_context_len`` and
+    ``max_prefix_len`` are host upper bounds.  A workspace is allocated with
+    torch when none is given."""
+    lib = lib or library()
+    s, hq, d = query.shape
+    nb, bs, hkv, dk = key_cache.shape
+    g = prefix_lens.shape[0]
+    if out.shape != query.shape or dk != d or value_cache.shape != key_cache.shape:
+        raise ValueError("out/query must be [S, Hq, D], the caches [NB, bs, Hkv, D]")
+    if not (out.dtype == query.dtype == key_cache.dtype == value_cache.dtype) \
+            or query.dtype not in _DTYPE:
+        raise ValueError("out, query and caches must share a dtype, float16 or bfloat16")
+    if not key_cache.is_contiguous() or not value_cache.is_contiguous():
+        raise ValueError("caches must be contiguous [num_blocks, block_size, Hkv, D]")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != s \
+            or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [num_seqs, max_blocks] with contiguous rows")
+    _vector(context_lens, s, torch.int32, "context_lens")
+    _vector(group_starts, g + 1, torch.int32, "group_starts")
+    _vector(prefix_lens, g, torch.int32, "prefix_lens")
+    os, qs = _rows(out, "out"), _rows(query, "query")
+    _on_device("pa_decode_shared", out=out, query=query, key_cache=key_cache,
+               value_cache=value_cache, block_table=block_table, context_lens=context_lens,
+               group_starts=group_starts, prefix_lens=prefix_lens, workspace=workspace,
+               d_error=d_error)
+    if workspace is None:
+        need = pa_decode_shared_plan(s, g, hq, hkv, d, max_context_len, max_prefix_len, lib=lib)
+        workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+    stride = block_table.stride(0) if s > 1 else block_table.shape[1]
+    st = lib.pa_decode_shared(
+        out.data_ptr(), os, query.data_ptr(), qs, key_cache.data_ptr(), value_cache.data_ptr(),
+        block_table.data_ptr(), stride, block_table.shape[1], context_lens.data_ptr(),
+        group_starts.data_ptr(), prefix_lens.data_ptr(), g, s, hq, hkv, d, bs, nb, float(scale),
+        int(max_context_len), int(max_prefix_len), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _DTYPE[query.dtype],
+        None if d_error is None else d_error.data_ptr(), _stream(stream))
+    _check(lib, st, "pa_decode_shared")
     return out

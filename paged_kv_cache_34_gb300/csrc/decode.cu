@@ -17,8 +17,8 @@ size_t decode_smem_bytes(int head_dim, int num_seqs, int partition_size, int blo
                          : dec::DecodeSmem<64>::bytes(num_seqs, max_ids);
 }
 
-cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream) {
-  dec::DecodeParams p;
+dec::DecodeParams decode_params(const DecodeArgs &a) {
+  dec::DecodeParams p = {};
   p.out = a.out;
   p.out_row_stride = a.out_row_stride;
   p.q = a.query;
@@ -61,6 +61,11 @@ cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream) {
   p.v_scale = a.v_scale;
   p.err = a.d_error;
   p.wait_ns = a.wait_ns;
+  return p;
+}
+
+cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream) {
+  const dec::DecodeParams p = decode_params(a);
   if (a.head_dim != 64 && a.head_dim != 128) return cudaErrorInvalidValue;
   const bool bf = a.dtype == PA_BF16;
   if (a.kv_int8 && a.kv_fp8)

@@ -138,7 +138,43 @@ struct DecodeParams {
   int64_t num_slots;
   int32_t *err;
   uint64_t wait_ns;  // bound of a pipeline wait
+  // A batch whose groups share a prefix (SH variant): the launch before this
+  // one attends to the prefixes, this one to each sequence's own tokens, and
+  // every piece leaves its state for the join.
+  const int32_t *group_starts, *prefix_lens;
+  int32_t num_groups, max_prefix;
 };
+
+// The groups of a batch that shares prefixes (warp-collective): usable when
+// group_starts starts at 0, never decreases and ends at num_seqs.
+__device__ inline bool groups_usable(const int32_t *starts, int num_groups, int num_seqs,
+                                     int lane) {
+  bool bad = false;
+  if (lane == 0) bad = __ldg(starts) != 0 || __ldg(starts + num_groups) != num_seqs;
+  for (int g = lane; g < num_groups; g += 32) {
+    const int a = __ldg(starts + g), e = __ldg(starts + g + 1);
+    bad |= a < 0 || e < a || e > num_seqs;
+  }
+  return !__any_sync(0xffffffffu, bad);
+}
+// The prefix length of sequence b's group (usable groups); one that does not
+// fit counts as none.
+__device__ inline int group_prefix(const int32_t *starts, const int32_t *lens, int num_groups,
+                                   int b, int max_prefix, int capacity) {
+  int lo = 0, hi = num_groups;  // starts[lo] <= b < starts[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(starts + mid) <= b) lo = mid;
+    else hi = mid;
+  }
+  const int len = __ldg(lens + lo);
+  return len < 0 || len > max_prefix || len > capacity ? 0 : len;
+}
+// First position that a sequence's own part reads: its own first token, down
+// to a whole TMA box (the rows between are masked).
+__host__ __device__ __forceinline__ int own_start(int prefix, int box_rows) {
+  return prefix - prefix % box_rows;
+}
 
 // One piece of work: tokens [start, end) of unit (sequence b, slice g) whose
 // context is L tokens.  `direct`: the piece is the unit's whole context and
@@ -173,6 +209,8 @@ struct Sched {
   const int *len;   // checked context lengths
   int S, vh, hq, G, nc, hs, P, NP, NW;
   bool balanced;
+  const int *lo;  // SH: first own token of each sequence (else null)
+  int box;        // SH: rows per TMA box
   int total;      // fixed: items; balanced: token-units
   int C, chunks;  // balanced: chunk size and count
 };
@@ -222,6 +260,7 @@ __device__ __forceinline__ Cursor first_cursor(const Sched &sc, int gw) {
 
 // The next piece of a worker's list; false at the end.  The fixed schedule
 // also returns the (empty) items of empty sequences, end == start.
+template <bool SH = false>
 __device__ inline bool next_piece(const Sched &sc, Cursor &cu, Item &m) {
   if (!sc.balanced) {
     if (cu.i >= sc.total) return false;
@@ -263,6 +302,13 @@ __device__ inline bool next_piece(const Sched &sc, Cursor &cu, Item &m) {
     m.start = t0;
     m.end = min(t1, L);
     m.direct = t0 == 0 && t1 >= L;
+    if constexpr (SH) {  // positions count from the sequence's own start
+      const int own = own_start(sc.lo[lo], sc.box);
+      m.start += own;
+      m.end += own;
+      m.L += own;
+      m.direct = false;
+    }
     m.prow = (static_cast<int64_t>(lo) * sc.vh + g + cu.i) * sc.hs;
     m.pstride = 1;
     return true;
@@ -391,7 +437,8 @@ __device__ __forceinline__ uint32_t chunk_off(int r, int c) {
 // codes.  NG: 8-head column groups per slice (1 or 2).  WR: the one-call
 // step (the launch also writes the step's new rows); the plain decode is
 // built without that code, which would otherwise cost it registers.
-template <class E, int D, bool BAL, int KVF, int NG, bool WR>
+// SH: the own parts of sequences that share prefixes (see DecodeParams).
+template <class E, int D, bool BAL, int KVF, int NG, bool WR, bool SH = false>
 __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
     decode_persistent_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmk,
                              const __grid_constant__ CUtensorMap tmv) {
@@ -401,6 +448,7 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
   constexpr bool BF = M::kBF16;
   constexpr bool QS = KV8 && E::kBF16;  // bf16 queries rescaled per head into fp16
   static_assert(!(WR && KV8), "the one-call step is built for 16-bit pools");
+  static_assert(!SH || (BAL && !KV8 && !WR), "shared prefixes: 16-bit pools, balanced split");
   using S = DecodeSmem<D, KV8>;
   constexpr int NH = S::kHalves;
   constexpr int NR = S::kRegions;
@@ -423,13 +471,18 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
   int *s_pref = reinterpret_cast<int *>(smem + S::kVarOffset);
   int *s_len = s_pref + p.num_seqs + 1;
   int *s_ids = s_len + p.num_seqs;  // [kWorkers][2][max_ids]
+  int *s_lo = s_ids + kWorkers * 2 * p.max_ids;  // SH: [num_seqs] first own token
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int P = p.partition_size;
   const int nseq = p.num_seqs;
   // Inputs come from earlier kernels (after a separate cache write, only its
   // K/V rows do: see after_write).
-  if (!p.after_write) griddep_wait();
+  // The SH variant reads nothing of the launch before it (whose blocks all
+  // waited for the launches before them); it ends after it.
+  if constexpr (!SH) {
+    if (!p.after_write) griddep_wait();
+  }
   griddep_launch_dependents();
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -442,12 +495,21 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
   if (warp == 0) {
     // Items per sequence (checked context lengths) and their prefix sums.
     int carry = 0;
+    bool grouped = false;
+    if constexpr (SH) grouped = groups_usable(p.group_starts, p.num_groups, nseq, lane);
     for (int base = 0; base < nseq; base += 32) {
       const int b = base + lane;
       int items = 0;
       if (b < nseq) {
-        const int L = checked_context_len(__ldg(p.context_lens + b), p.capacity, p.max_ctx,
-                                          p.err, blockIdx.x == 0);
+        int L = checked_context_len(__ldg(p.context_lens + b), p.capacity, p.max_ctx,
+                                    p.err, blockIdx.x == 0);
+        if constexpr (SH) {
+          const int pre = grouped ? group_prefix(p.group_starts, p.prefix_lens, p.num_groups, b,
+                                                 p.max_prefix, p.capacity)
+                                  : 0;
+          s_lo[b] = pre;
+          L = L > pre ? L - own_start(pre, p.box_rows) : 0;
+        }
         s_len[b] = L;
         items = (BAL ? ceil16(L) : (L > 0 ? (L + P - 1) / P : 1)) * p.vh;
       }
@@ -481,6 +543,10 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
   sc.NP = p.num_partitions;
   sc.NW = gridDim.x * kWorkers;
   sc.balanced = BAL;  // compile-time: each kernel carries one schedule's code
+  if constexpr (SH) {
+    sc.lo = s_lo;
+    sc.box = p.box_rows;
+  }
   sc.total = s_pref[nseq];
   sc.C = sc.balanced ? balanced_chunk(sc.total, sc.NW, p.chunk_cap) : 0;
   sc.chunks = sc.balanced ? (sc.total + sc.C - 1) / sc.C : 0;
@@ -548,7 +614,7 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
     auto prefetch = [&](int buf, int k0, int kstep) {
       Item m;
       have_next = false;
-      while (next_piece(sc, pc, m)) {
+      while (next_piece<SH>(sc, pc, m)) {
         if (m.end <= m.start) continue;
         const int l0 = m.start / bs;
         const int nblk = (m.end - 1) / bs - l0 + 1;
@@ -639,6 +705,7 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
             mbar_wait_bounded(smem_u32(full + (k % NS)), (k / NS) & 1);
         }
         cp_async_wait_all();
+        if constexpr (SH) griddep_wait();
         return;
       }
       if (live == 0) {
@@ -653,6 +720,7 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
             mbar_wait_bounded(smem_u32(full + (k % NS)), (k / NS) & 1);
         }
         cp_async_wait_all();
+        if constexpr (SH) griddep_wait();  // the join waits for both launches by this one
         return;
       }
       const uint32_t bar = smem_u32(full + s);
@@ -704,7 +772,8 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
   bool nw_on = false;
   uint8_t *s_new = smem + S::kNewOffset + warp * S::kNewBytes;
   int64_t *s_nw = reinterpret_cast<int64_t *>(s_new + S::kNewMeta);  // [block id, token b's slot]
-  if (sc.balanced) {
+  int cur_lo = 0;  // SH: the piece's first own token
+  if (sc.balanced && !SH) {
     // Empty sequences have no pieces: their (zero) outputs are written here.
     for (int b = blockIdx.x * kWorkers + warp; b < nseq; b += sc.NW) {
       if (s_len[b] != 0) continue;
@@ -840,7 +909,7 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
   // (fixed schedule) are finished on the spot (zero output).
   auto begin = [&]() -> bool {
     Item m;
-    while (next_piece(sc, wc, m)) {
+    while (next_piece<SH>(sc, wc, m)) {
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
 #pragma unroll
@@ -867,6 +936,7 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
         if (!have_q) load_q<E, D, KV8, NG>(qf, p, m.b, h0, nh, lane);
         cur_item = m;
         cur = m.start;
+        if constexpr (SH) cur_lo = s_lo[m.b];
         const int kvh = p.nc == 1 ? m.g : m.g / p.nc;
         if constexpr (KV8) {
           // The piece's KV head's scales: K's scales the scores, V's the
@@ -917,7 +987,7 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
           Cursor peek = wc;
           Item nm;
           qn_b = qn_g = -1;
-          while (next_piece(sc, peek, nm)) {
+          while (next_piece<SH>(sc, peek, nm)) {
             if (nm.end <= nm.start) continue;
             int nnh;
             const int nh0 = slice_head0(sc, nm.g, nnh);
@@ -932,7 +1002,7 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
           // piece's query rows into L2 instead.
           Cursor peek = wc;
           Item nm;
-          while (next_piece(sc, peek, nm)) {
+          while (next_piece<SH>(sc, peek, nm)) {
             if (nm.end <= nm.start) continue;
             int nnh;
             const int nh0 = slice_head0(sc, nm.g, nnh);
@@ -1017,13 +1087,13 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
       // end - 1 - j0
       if (WR && nw_on && end - 1 < j0 + ROWS) touched = put_newest(kst, end - 1 - j0);
       if constexpr (!KV8) {
-        if (j0 + ROWS > end) {
+        if (j0 + ROWS > end || (SH && j0 < cur_lo)) {
           // Rows past the context may hold anything (even NaN); their weight
           // is zero, so make their V rows exact zeros before the P.V product.
           uint8_t *vrows = kst + NH * RB;
           for (int i = lane; i < ROWS * NH * 8; i += 32) {
             const int rr = i / (NH * 8), h = (i / 8) % NH, cc = i % 8;
-            if (j0 + rr >= end)
+            if (j0 + rr >= end || (SH && j0 + rr < cur_lo))
               *reinterpret_cast<uint4 *>(vrows + h * RB + (r0 + rr) * 128 + cc * 16) =
                   make_uint4(0, 0, 0, 0);
           }
@@ -1162,10 +1232,12 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
 #pragma unroll
           for (int uu = 0; uu < NTP; ++uu) {
             const int t0 = j0 + 16 * (ps * NTP + uu) + g8, t1 = t0 + 8;
-            sv[uu][0] = t0 < end ? sc2[n][uu][0] * slA : -INFINITY;
-            sv[uu][1] = t0 < end ? sc2[n][uu][1] * slB : -INFINITY;
-            sv[uu][2] = t1 < end ? sc2[n][uu][2] * slA : -INFINITY;
-            sv[uu][3] = t1 < end ? sc2[n][uu][3] * slB : -INFINITY;
+            const bool in0 = t0 < end && (!SH || t0 >= cur_lo);
+            const bool in1 = t1 < end && (!SH || t1 >= cur_lo);
+            sv[uu][0] = in0 ? sc2[n][uu][0] * slA : -INFINITY;
+            sv[uu][1] = in0 ? sc2[n][uu][1] * slB : -INFINITY;
+            sv[uu][2] = in1 ? sc2[n][uu][2] * slA : -INFINITY;
+            sv[uu][3] = in1 ? sc2[n][uu][3] * slB : -INFINITY;
             mx0 = fmaxf(mx0, fmaxf(sv[uu][0], sv[uu][2]));
             mx1 = fmaxf(mx1, fmaxf(sv[uu][1], sv[uu][3]));
           }
@@ -1408,12 +1480,12 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode_combine_kernel(cons
   }
 }
 
-template <class E, int D, bool BAL, int KVF, int NG, bool WR = false>
+template <class E, int D, bool BAL, int KVF, int NG, bool WR = false, bool SH = false>
 cudaError_t launch_kernel(const DecodeArgs &a, const DecodeParams &p, cudaStream_t stream) {
   using S = DecodeSmem<D, KVF != 0>;
-  const int smem = S::bytes(a.num_seqs, p.max_ids);
-  auto kernel = decode_persistent_kernel<E, D, BAL, KVF, NG, WR>;
-  cudaError_t e = allow_dynamic_smem<decode_persistent_kernel<E, D, BAL, KVF, NG, WR>>();
+  const int smem = S::bytes(a.num_seqs, p.max_ids) + (SH ? 4 * a.num_seqs : 0);
+  auto kernel = decode_persistent_kernel<E, D, BAL, KVF, NG, WR, SH>;
+  cudaError_t e = allow_dynamic_smem<decode_persistent_kernel<E, D, BAL, KVF, NG, WR, SH>>();
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(a.grid)), dim3(threads_for(WR)), smem,
                     stream,
@@ -1459,6 +1531,9 @@ cudaError_t launch_family(const DecodeArgs &a, const DecodeParams &p, cudaStream
 }
 
 }  // namespace dec
+
+// The kernels' arguments of a decode.
+dec::DecodeParams decode_params(const DecodeArgs &a);
 
 // One translation unit per (element type, pool format).
 cudaError_t launch_decode_f16(const DecodeArgs &a, const dec::DecodeParams &p, cudaStream_t s);

@@ -413,19 +413,19 @@ pa_status pa_decode_plan(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_h
 
 namespace {
 
-// pa_decode, optionally preceded by the step's cache write `write` (launched
-// first, after every check has passed, so an error enqueues nothing).
-pa_status decode_call(void *out, int64_t out_row_stride, const void *query, int64_t q_row_stride,
-                      const void *key_cache, const void *value_cache, const int32_t *block_table,
-                      int64_t block_table_stride, int32_t max_blocks_per_seq,
-                      const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads,
-                      int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
-                      int64_t num_blocks, float scale, int32_t max_context_len,
-                      int32_t partition_size, void *workspace, size_t workspace_bytes,
-                      pa_dtype dtype, int32_t *d_error, void *stream,
-                      const pa::ReshapeArgs *write, const float *k_scale = nullptr,
-                      const float *v_scale = nullptr, bool fp8 = false) {
-  const bool int8 = k_scale != nullptr || v_scale != nullptr;
+// The checks of a decode's arguments and the launch arguments that follow
+// from them alone; `empty`: no sequence to attend for.
+struct DecodeSetup {
+  bool empty = true;
+  pa::DecodeArgs args;
+};
+pa_status check_decode(void *out, int64_t out_row_stride, const void *query, int64_t q_row_stride,
+                       const void *key_cache, const void *value_cache, const int32_t *block_table,
+                       int64_t block_table_stride, int32_t max_blocks_per_seq,
+                       const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads,
+                       int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                       int64_t num_blocks, float scale, int32_t max_context_len,
+                       int32_t partition_size, pa_dtype dtype, DecodeSetup *setup) {
   if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq < 0 || max_context_len < 0 ||
       partition_size < 0)
@@ -438,13 +438,8 @@ pa_status decode_call(void *out, int64_t out_row_stride, const void *query, int6
   if (!valid_block_size(block_size)) return PA_ERR_UNSUPPORTED;
   if (num_blocks * block_size > INT32_MAX) return PA_ERR_UNSUPPORTED;
   if (partition_size % pa::kDecodeSub != 0) return PA_ERR_SHAPE;
-  if (num_seqs == 0) {  // nothing to attend: only the step's write, if any
-    if (!write) return PA_OK;
-    pa::ReshapeArgs w = *write;
-    cudaError_t e = current_num_sms(&w.num_sms);
-    if (e == cudaSuccess) e = pa::launch_reshape_and_cache(w, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? PA_OK : cuda_fail(e);
-  }
+  setup->empty = num_seqs == 0;
+  if (num_seqs == 0) return PA_OK;
   if (!out || !query || !key_cache || !value_cache || !block_table || !context_lens)
     return PA_ERR_NULL;
   const int64_t qrow = static_cast<int64_t>(num_q_heads) * head_dim;
@@ -452,24 +447,7 @@ pa_status decode_call(void *out, int64_t out_row_stride, const void *query, int6
   if (q_row_stride % 8 || out_row_stride % 8) return PA_ERR_ALIGN;
   if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache))
     return PA_ERR_ALIGN;
-  if (int8) {
-    if (!k_scale || !v_scale) return PA_ERR_NULL;
-    if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u)
-      return PA_ERR_ALIGN;
-  }
-
-  int32_t P = 0;
-  size_t need = 0;
-  pa_status st = pa_decode_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
-                                partition_size, &P, &need);
-  if (st != PA_OK) return st;
-  const bool balanced = P == 0;
-  const int32_t nparts = balanced ? 0 : (max_context_len > 0 ? (max_context_len + P - 1) / P : 1);
-  if (need > 0 && (!workspace || workspace_bytes < need ||
-                   (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
-    return PA_ERR_WORKSPACE;
-
-  pa::DecodeArgs a;
+  pa::DecodeArgs &a = setup->args;
   a.out = out;
   a.out_row_stride = out_row_stride;
   a.query = query;
@@ -487,26 +465,83 @@ pa_status decode_call(void *out, int64_t out_row_stride, const void *query, int6
   a.num_blocks = num_blocks;
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   a.max_context_len = max_context_len;
-  a.partition_size = P;
-  a.num_partitions = nparts;
   a.ws_o = nullptr;
   a.ws_ml = nullptr;
   a.ws_pref = nullptr;
   a.slices = pa::decode_slices(num_q_heads / num_kv_heads);
+  a.dtype = dtype;
+  a.box_rows = block_size < pa::kDecodeSub ? block_size : pa::kDecodeSub;
+  return PA_OK;
+}
+
+// The balanced split's launch shape (num_sms known) and its workspace.
+void set_balanced(pa::DecodeArgs *a, void *workspace) {
+  const pa::DecodeBalance d = pa::decode_balance(
+      a->num_seqs, a->num_kv_heads * a->slices.nc, a->max_context_len, a->num_sms);
+  a->partition_size = 0;
+  a->num_partitions = 0;
+  a->grid = d.grid;
+  a->merge = true;
+  const size_t rows = static_cast<size_t>(d.pieces) * a->slices.hs;
+  char *w = static_cast<char *>(workspace);
+  a->ws_o = reinterpret_cast<float *>(w);
+  w += align256(rows * a->head_dim * sizeof(float));
+  a->ws_ml = reinterpret_cast<float *>(w);
+  w += align256(rows * 2 * sizeof(float));
+  a->ws_pref = reinterpret_cast<int32_t *>(w);
+}
+
+// pa_decode, optionally preceded by the step's cache write `write` (launched
+// first, after every check has passed, so an error enqueues nothing).
+pa_status decode_call(void *out, int64_t out_row_stride, const void *query, int64_t q_row_stride,
+                      const void *key_cache, const void *value_cache, const int32_t *block_table,
+                      int64_t block_table_stride, int32_t max_blocks_per_seq,
+                      const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads,
+                      int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                      int64_t num_blocks, float scale, int32_t max_context_len,
+                      int32_t partition_size, void *workspace, size_t workspace_bytes,
+                      pa_dtype dtype, int32_t *d_error, void *stream,
+                      const pa::ReshapeArgs *write, const float *k_scale = nullptr,
+                      const float *v_scale = nullptr, bool fp8 = false) {
+  const bool int8 = k_scale != nullptr || v_scale != nullptr;
+  DecodeSetup setup;
+  pa_status st = check_decode(out, out_row_stride, query, q_row_stride, key_cache, value_cache,
+                              block_table, block_table_stride, max_blocks_per_seq, context_lens,
+                              num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                              num_blocks, scale, max_context_len, partition_size, dtype, &setup);
+  if (st != PA_OK) return st;
+  if (setup.empty) {  // nothing to attend: only the step's write, if any
+    if (!write) return PA_OK;
+    pa::ReshapeArgs w = *write;
+    cudaError_t e = current_num_sms(&w.num_sms);
+    if (e == cudaSuccess) e = pa::launch_reshape_and_cache(w, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+  }
+  if (int8) {
+    if (!k_scale || !v_scale) return PA_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u)
+      return PA_ERR_ALIGN;
+  }
+
+  int32_t P = 0;
+  size_t need = 0;
+  st = pa_decode_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
+                      partition_size, &P, &need);
+  if (st != PA_OK) return st;
+  const bool balanced = P == 0;
+  const int32_t nparts = balanced ? 0 : (max_context_len > 0 ? (max_context_len + P - 1) / P : 1);
+  if (need > 0 && (!workspace || workspace_bytes < need ||
+                   (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+    return PA_ERR_WORKSPACE;
+
+  pa::DecodeArgs &a = setup.args;
+  a.partition_size = P;
+  a.num_partitions = nparts;
   const int units = num_kv_heads * a.slices.nc;  // decode units per sequence
   cudaError_t e = current_num_sms(&a.num_sms);
   if (e != cudaSuccess) return cuda_fail(e);
   if (balanced) {
-    const pa::DecodeBalance d = pa::decode_balance(num_seqs, units, max_context_len, a.num_sms);
-    a.grid = d.grid;
-    a.merge = true;
-    const size_t rows = static_cast<size_t>(d.pieces) * a.slices.hs;
-    char *w = static_cast<char *>(workspace);
-    a.ws_o = reinterpret_cast<float *>(w);
-    w += align256(rows * head_dim * sizeof(float));
-    a.ws_ml = reinterpret_cast<float *>(w);
-    w += align256(rows * 2 * sizeof(float));
-    a.ws_pref = reinterpret_cast<int32_t *>(w);
+    set_balanced(&a, workspace);
   } else {
     // Items are at most S * units * partitions; kDecodeCtasPerSm CTAs per SM,
     // kDecodeWarps workers each.
@@ -525,9 +560,7 @@ pa_status decode_call(void *out, int64_t out_row_stride, const void *query, int6
     }
   }
   a.d_error = d_error;
-  a.dtype = dtype;
   a.wait_ns = pa::pipeline_wait_ns();
-  a.box_rows = block_size < pa::kDecodeSub ? block_size : pa::kDecodeSub;
   // The item schedule keeps per-sequence prefix sums in shared memory.
   if (pa::decode_smem_bytes(head_dim, num_seqs, P, block_size, int8) > 227 * 1024)
     return PA_ERR_UNSUPPORTED;
@@ -835,6 +868,132 @@ pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *que
                        kv_row_stride, 128))
     return cuda_fail(cudaErrorInvalidValue);
   e = pa::launch_attention_varlen(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Sizes of a shared-prefix decode; `shared` false: it is a plain decode (no
+// group, no prefix, or a batch too long for the balanced split's 32-bit
+// positions).
+struct SharedPlan {
+  bool shared = false;
+  int sms = 0, runs = 0;
+  size_t decode_bytes = 0, o_bytes = 0, ml_bytes = 0, bytes = 0;
+};
+pa_status shared_plan(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
+                      int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
+                      int32_t max_prefix_len, SharedPlan *out) {
+  if (num_groups < 0 || max_prefix_len < 0) return PA_ERR_SHAPE;
+  int32_t P = 0;
+  SharedPlan s;
+  const pa_status st = pa_decode_plan(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                      max_context_len, 0, &P, &s.decode_bytes);
+  if (st != PA_OK) return st;
+  const cudaError_t e = current_num_sms(&s.sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  s.shared = num_seqs > 0 && num_groups > 0 && max_prefix_len > 0 && max_context_len > 0 && P == 0;
+  s.bytes = s.decode_bytes;
+  if (s.shared) {
+    s.runs = pa::shared_runs(num_seqs, num_groups, num_q_heads, num_kv_heads, max_prefix_len,
+                             s.sms);
+    const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads + 256 * static_cast<size_t>(s.runs);
+    s.o_bytes = align256(rows * head_dim * sizeof(float));
+    s.ml_bytes = align256(rows * 2 * sizeof(float));
+    s.bytes += s.o_bytes + s.ml_bytes + align256((static_cast<size_t>(num_seqs) + 1) * 32);
+  }
+  *out = s;
+  return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_decode_shared_plan(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
+                                int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
+                                int32_t max_prefix_len, size_t *workspace_bytes_out) {
+  SharedPlan s;
+  const pa_status st = shared_plan(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim,
+                                   max_context_len, max_prefix_len, &s);
+  if (st == PA_OK && workspace_bytes_out) *workspace_bytes_out = s.bytes;
+  return st;
+}
+
+pa_status pa_decode_shared(void *out, int64_t out_row_stride, const void *query,
+                           int64_t q_row_stride, const void *key_cache, const void *value_cache,
+                           const int32_t *block_table, int64_t block_table_stride,
+                           int32_t max_blocks_per_seq, const int32_t *context_lens,
+                           const int32_t *group_starts, const int32_t *prefix_lens,
+                           int32_t num_groups, int32_t num_seqs, int32_t num_q_heads,
+                           int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                           int64_t num_blocks, float scale, int32_t max_context_len,
+                           int32_t max_prefix_len, void *workspace, size_t workspace_bytes,
+                           pa_dtype dtype, int32_t *d_error, void *stream) {
+  if (num_groups < 0 || max_prefix_len < 0) return PA_ERR_SHAPE;
+  DecodeSetup c;
+  pa_status st = check_decode(out, out_row_stride, query, q_row_stride, key_cache, value_cache,
+                              block_table, block_table_stride, max_blocks_per_seq, context_lens,
+                              num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                              num_blocks, scale, max_context_len, 0, dtype, &c);
+  if (st != PA_OK || c.empty) return st;
+  if (num_groups > 0 && max_prefix_len > 0) {
+    if (!group_starts || !prefix_lens) return PA_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(group_starts) | reinterpret_cast<uintptr_t>(prefix_lens)) & 3u)
+      return PA_ERR_ALIGN;
+  }
+  SharedPlan s;
+  st = shared_plan(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, max_context_len,
+                   max_prefix_len, &s);
+  if (st != PA_OK) return st;
+  if (!s.shared)
+    return decode_call(out, out_row_stride, query, q_row_stride, key_cache, value_cache,
+                       block_table, block_table_stride, max_blocks_per_seq, context_lens,
+                       num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                       scale, max_context_len, 0, workspace, workspace_bytes, dtype, d_error,
+                       stream, nullptr);
+  if (!workspace || workspace_bytes < s.bytes ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return PA_ERR_WORKSPACE;
+  if (pa::decode_smem_bytes(head_dim, num_seqs, 0, block_size) + 4 * static_cast<size_t>(num_seqs) >
+      227 * 1024)
+    return PA_ERR_UNSUPPORTED;
+  pa::DecodeSharedArgs a;
+  pa::DecodeArgs &d = a.decode;
+  d = c.args;
+  d.num_sms = s.sms;
+  set_balanced(&d, workspace);
+  d.wait_ns = pa::pipeline_wait_ns();
+  d.d_error = d_error;
+  a.group_starts = group_starts;
+  a.prefix_lens = prefix_lens;
+  a.num_groups = num_groups;
+  a.max_prefix = max_prefix_len;
+  a.runs = s.runs;
+  a.packed_heads = pa::flash_packed_heads(num_q_heads / num_kv_heads);
+  flash_scale(scale, &a.scale_log2, &a.negate);
+  char *w = static_cast<char *>(workspace) + s.decode_bytes;
+  a.ws_o = reinterpret_cast<float *>(w);
+  w += s.o_bytes;
+  a.ws_ml = reinterpret_cast<float *>(w);
+  w += s.ml_bytes;
+  a.ws_info = reinterpret_cast<int32_t *>(w);
+  const int64_t rows = num_blocks * block_size;
+  const int64_t row_stride = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (!encode_rows_map(&d.tm_k, key_cache, dtype, head_dim, num_kv_heads, rows, row_stride,
+                       d.box_rows) ||
+      !encode_rows_map(&d.tm_v, value_cache, dtype, head_dim, num_kv_heads, rows, row_stride,
+                       d.box_rows) ||
+      !encode_rows_map(&a.tm_q, query, dtype, head_dim, num_q_heads, num_seqs, q_row_stride,
+                       128 / a.packed_heads, false, a.packed_heads) ||
+      !encode_rows_map(&a.tm_k, key_cache, dtype, head_dim, num_kv_heads, rows, row_stride,
+                       block_size) ||
+      !encode_rows_map(&a.tm_v, value_cache, dtype, head_dim, num_kv_heads, rows, row_stride,
+                       block_size))
+    return cuda_fail(cudaErrorInvalidValue);
+  const cudaError_t e = pa::launch_decode_shared(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 

@@ -223,4 +223,30 @@ struct AttentionVarlenArgs {
 };
 cudaError_t launch_attention_varlen(const AttentionVarlenArgs &a, cudaStream_t stream);
 
+// Runs of the prefix pass: one per CTA, at most one per SM; a run takes at
+// least two K/V tiles of one query tile (see flash_kernel.cuh).
+inline int shared_runs(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
+                       int max_prefix, int num_sms) {
+  const int pg = flash_packed_heads(num_q_heads / num_kv_heads), tpt = 128 / pg;
+  const int64_t tiles = (static_cast<int64_t>(num_seqs) / tpt + num_groups) * (num_q_heads / pg);
+  const int64_t cost = tiles * ((max_prefix + 127) / 128);
+  const int64_t runs = (cost + 1) / 2;
+  return static_cast<int>(runs < 1 ? 1 : (runs < num_sms ? runs : num_sms));
+}
+
+struct DecodeSharedArgs {
+  DecodeArgs decode;  // the whole decode, balanced split, its workspace
+  const int32_t *group_starts, *prefix_lens;
+  int32_t num_groups, max_prefix;
+  int runs;            // CTAs of the prefix pass
+  int packed_heads;
+  float scale_log2;    // |scale| * log2(e), not 0
+  bool negate;         // the scale is negative
+  CUtensorMap tm_q;    // box 64 x packed_heads x 128 / packed_heads
+  CUtensorMap tm_k, tm_v;  // box 64 x 1 x block_size
+  float *ws_o, *ws_ml;     // [num_seqs * num_q_heads + 256 * runs, D] and [.., 2]
+  int32_t *ws_info;        // 8 words, then 8 per sequence
+};
+cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream);
+
 }  // namespace pa
