@@ -251,19 +251,28 @@ def pa_copy_blocks(key_cache, value_cache, block_mapping, *, d_error=None, strea
     _check(lib, st, "pa_copy_blocks")
 
 
-def _on_device(where, **tensors):
-    """Every tensor given is on the current CUDA device (where the kernel is
-    launched) -- a pointer of another device, or of the host, would fault."""
-    cur = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != cur:
-            raise ValueError(f"{where}: {name} is not on the current CUDA device ({cur})")
-
-
-def _vector(t, n, dtype, name):
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+def _bad_vector(t, n, dtype, name, dev):
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values".replace(
             "torch.", ""))
+    _bad_device(name, dev)
+
+
+def _bad_device(name, dev):
+    raise ValueError(f"{name} is not on the CUDA device of the call ({dev}): a pointer of another "
+                     "device, or of the host, would fault")
+
+
+def _current(dev):
+    """The call's device is the current one, where its kernels are launched."""
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError("the tensors must be on the current CUDA device")
+
+
+def _raw_stream(stream, dev):
+    """The cudaStream_t of `stream`, or of the current stream (without building
+    a stream object, which takes 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def pa_build_tables(block_table, context_lens, query_lens, free_blocks, num_free,
@@ -277,35 +286,41 @@ def pa_build_tables(block_table, context_lens, query_lens, free_blocks, num_free
     taken off the end of free_blocks[:num_free], and num_free_out int32 [1].
     No output may overlap an input."""
     lib = lib or library()
-    s, t = context_lens.shape[0], slot_mapping.shape[0]
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != s \
-            or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be int32 [num_seqs, max_blocks] with contiguous rows")
-    _vector(context_lens, s, torch.int32, "context_lens")
-    _vector(query_lens, s, torch.int32, "query_lens")
-    _vector(free_blocks, free_blocks.shape[0], torch.int32, "free_blocks")
-    _vector(num_free, 1, torch.int32, "num_free")
-    _vector(context_lens_out, s, torch.int32, "context_lens_out")
-    _vector(cu_seqlens_q, s + 1, torch.int32, "cu_seqlens_q")
-    _vector(slot_mapping, t, torch.int64, "slot_mapping")
-    _vector(num_free_out, 1, torch.int32, "num_free_out")
+    s, t, nfree = context_lens.shape[0], slot_mapping.shape[0], free_blocks.shape[0]
+    i32, dev = torch.int32, context_lens.get_device()
+    if block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != s:
+        raise ValueError("block_table must be int32 [num_seqs, max_blocks]")
+    stride, inner = block_table.stride()
+    width = block_table.shape[1]
+    if width > 1 and inner != 1:
+        raise ValueError("block_table must have contiguous rows")
+    vectors = [(context_lens, s, i32, "context_lens"), (query_lens, s, i32, "query_lens"),
+               (free_blocks, nfree, i32, "free_blocks"), (num_free, 1, i32, "num_free"),
+               (context_lens_out, s, i32, "context_lens_out"),
+               (cu_seqlens_q, s + 1, i32, "cu_seqlens_q"),
+               (slot_mapping, t, torch.int64, "slot_mapping"),
+               (num_free_out, 1, i32, "num_free_out")]
     if positions is not None:
-        _vector(positions, t, torch.int32, "positions")
-    _on_device("pa_build_tables", block_table=block_table, context_lens=context_lens,
-               query_lens=query_lens, free_blocks=free_blocks, num_free=num_free,
-               context_lens_out=context_lens_out, cu_seqlens_q=cu_seqlens_q,
-               slot_mapping=slot_mapping, positions=positions, num_free_out=num_free_out,
-               d_error=d_error)
-    stride = block_table.stride(0) if s > 1 else block_table.shape[1]
-    st = lib.pa_build_tables(block_table.data_ptr(), stride, block_table.shape[1],
+        vectors.append((positions, t, i32, "positions"))
+    for v in vectors:
+        x = v[0]
+        if x.dtype is not v[2] or x.numel() != v[1] or x.get_device() != dev \
+                or not x.is_contiguous():
+            _bad_vector(*v, dev)
+    if block_table.get_device() != dev or (d_error is not None and d_error.get_device() != dev):
+        _bad_device("block_table or d_error", dev)
+    _current(dev)
+    st = lib.pa_build_tables(block_table.data_ptr(), stride if s > 1 else width, width,
                              context_lens.data_ptr(), query_lens.data_ptr(),
-                             free_blocks.data_ptr(), num_free.data_ptr(), free_blocks.shape[0],
+                             free_blocks.data_ptr(), num_free.data_ptr(), nfree,
                              context_lens_out.data_ptr(), cu_seqlens_q.data_ptr(),
                              slot_mapping.data_ptr(),
                              None if positions is None else positions.data_ptr(),
                              num_free_out.data_ptr(), s, t, block_size, num_blocks,
-                             None if d_error is None else d_error.data_ptr(), _stream(stream))
-    _check(lib, st, "pa_build_tables")
+                             None if d_error is None else d_error.data_ptr(),
+                             _raw_stream(stream, dev))
+    if st:
+        _check(lib, st, "pa_build_tables")
 
 
 def pa_debug_set_wait_limit_ns(ns: int, *, lib=None):
@@ -511,26 +526,31 @@ def pa_attention_varlen(out, query, key, value, cu_seqlens, *, scale, max_seqlen
     upper bound of the lengths; rows past cu_seqlens[S] are left alone."""
     lib = lib or library()
     t, hq, d = query.shape
-    if out.shape != query.shape or key.shape != value.shape or key.shape[0] != t \
-            or key.shape[2] != d:
+    shape, dtype, n, dev = key.shape, query.dtype, cu_seqlens.numel(), query.get_device()
+    if out.shape != query.shape or shape != value.shape or shape[0] != t or shape[2] != d:
         raise ValueError("out/query must be [T, Hq, D] and key/value [T, Hkv, D]")
-    if not (out.dtype == query.dtype == key.dtype == value.dtype) or query.dtype not in _DTYPE:
+    if dtype not in _DTYPE or out.dtype is not dtype or key.dtype is not dtype \
+            or value.dtype is not dtype:
         raise ValueError("out, query, key and value must share a dtype, float16 or bfloat16")
     os, qs, ks = _rows(out, "out"), _rows(query, "query"), _rows(key, "key")
     if _rows(value, "value") != ks:
         raise ValueError("key and value must share a row stride")
-    _vector(cu_seqlens, cu_seqlens.numel(), torch.int32, "cu_seqlens")
-    if cu_seqlens.numel() < 1:
-        raise ValueError("cu_seqlens must hold num_seqs + 1 values")
-    _on_device("pa_attention_varlen", out=out, query=query, key=key, value=value,
-               cu_seqlens=cu_seqlens, d_error=d_error)
+    if cu_seqlens.dtype is not torch.int32 or n < 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous int32 tensor of num_seqs + 1 values")
+    for x in (out, key, value, cu_seqlens):
+        if x.get_device() != dev:
+            _bad_device("out, key, value or cu_seqlens", dev)
+    if d_error is not None and d_error.get_device() != dev:
+        _bad_device("d_error", dev)
+    _current(dev)
     st = lib.pa_attention_varlen(out.data_ptr(), os, query.data_ptr(), qs, key.data_ptr(),
-                                 value.data_ptr(), ks, cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, t,
-                                 int(max_seqlen), hq, key.shape[1], d, float(scale),
-                                 1 if causal else 0, _DTYPE[query.dtype],
+                                 value.data_ptr(), ks, cu_seqlens.data_ptr(), n - 1, t,
+                                 int(max_seqlen), hq, shape[1], d, float(scale),
+                                 1 if causal else 0, _DTYPE[dtype],
                                  None if d_error is None else d_error.data_ptr(),
-                                 _stream(stream))
-    _check(lib, st, "pa_attention_varlen")
+                                 _raw_stream(stream, dev))
+    if st:
+        _check(lib, st, "pa_attention_varlen")
     return out
 
 
@@ -557,35 +577,41 @@ def pa_decode_shared(out, query, key_cache, value_cache, block_table, context_le
     lib = lib or library()
     s, hq, d = query.shape
     nb, bs, hkv, dk = key_cache.shape
-    g = prefix_lens.shape[0]
+    g, dtype, i32, dev = prefix_lens.shape[0], query.dtype, torch.int32, query.get_device()
     if out.shape != query.shape or dk != d or value_cache.shape != key_cache.shape:
         raise ValueError("out/query must be [S, Hq, D], the caches [NB, bs, Hkv, D]")
-    if not (out.dtype == query.dtype == key_cache.dtype == value_cache.dtype) \
-            or query.dtype not in _DTYPE:
+    if dtype not in _DTYPE or out.dtype is not dtype or key_cache.dtype is not dtype \
+            or value_cache.dtype is not dtype:
         raise ValueError("out, query and caches must share a dtype, float16 or bfloat16")
     if not key_cache.is_contiguous() or not value_cache.is_contiguous():
         raise ValueError("caches must be contiguous [num_blocks, block_size, Hkv, D]")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != s \
-            or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be int32 [num_seqs, max_blocks] with contiguous rows")
-    _vector(context_lens, s, torch.int32, "context_lens")
-    _vector(group_starts, g + 1, torch.int32, "group_starts")
-    _vector(prefix_lens, g, torch.int32, "prefix_lens")
+    if block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != s:
+        raise ValueError("block_table must be int32 [num_seqs, max_blocks]")
+    stride, inner = block_table.stride()
+    width = block_table.shape[1]
+    if width > 1 and inner != 1:
+        raise ValueError("block_table must have contiguous rows")
+    for v in ((context_lens, s, i32, "context_lens"), (group_starts, g + 1, i32, "group_starts"),
+              (prefix_lens, g, i32, "prefix_lens")):
+        x = v[0]
+        if x.dtype is not i32 or x.numel() != v[1] or x.get_device() != dev \
+                or not x.is_contiguous():
+            _bad_vector(*v, dev)
     os, qs = _rows(out, "out"), _rows(query, "query")
-    _on_device("pa_decode_shared", out=out, query=query, key_cache=key_cache,
-               value_cache=value_cache, block_table=block_table, context_lens=context_lens,
-               group_starts=group_starts, prefix_lens=prefix_lens, workspace=workspace,
-               d_error=d_error)
+    for x in (out, key_cache, value_cache, block_table, workspace, d_error):
+        if x is not None and x.get_device() != dev:
+            _bad_device("out, caches, block_table, workspace or d_error", dev)
+    _current(dev)
     if workspace is None:
         need = pa_decode_shared_plan(s, g, hq, hkv, d, max_context_len, max_prefix_len, lib=lib)
         workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
-    stride = block_table.stride(0) if s > 1 else block_table.shape[1]
     st = lib.pa_decode_shared(
         out.data_ptr(), os, query.data_ptr(), qs, key_cache.data_ptr(), value_cache.data_ptr(),
-        block_table.data_ptr(), stride, block_table.shape[1], context_lens.data_ptr(),
+        block_table.data_ptr(), stride if s > 1 else width, width, context_lens.data_ptr(),
         group_starts.data_ptr(), prefix_lens.data_ptr(), g, s, hq, hkv, d, bs, nb, float(scale),
         int(max_context_len), int(max_prefix_len), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _DTYPE[query.dtype],
-        None if d_error is None else d_error.data_ptr(), _stream(stream))
-    _check(lib, st, "pa_decode_shared")
+        workspace.numel() * workspace.element_size(), _DTYPE[dtype],
+        None if d_error is None else d_error.data_ptr(), _raw_stream(stream, dev))
+    if st:
+        _check(lib, st, "pa_decode_shared")
     return out
