@@ -22,10 +22,12 @@
 //
 // Bound by latency, not by bytes: launch, lengths, sums, search, block ids,
 // stores follow one another.  Measured (graph replay, GB300): 3.0 us for one
-// token of one request, 4.7 us for 1024 requests of 16 tokens, 8.6 us for 1024
-// of 1000 (12.6 MB written).  One CTA per SM, in several steps: more CTAs
-// repeat the sums more often (1024 x 1000 with 2 / 3 of them: 8.7 / 12.4 us,
-// 4096 x 250: 18 / 26 against 16).
+// token of one request, 4.7 us for 1024 requests of 16 tokens, 11.0 us for
+// 1024 prompts of up to 2000 tokens (a million in all, 12.6 MB written).  Two
+// CTAs per SM at most, in several steps: a third repeats the sums more often
+// and takes registers from the token loop (1024 x 1000 tokens: 12.4 us against
+// 8.7), one alone leaves no room for the next launch's start beside it
+// (back-to-back calls 15.0 us against 11.2).
 #include "pa_device.cuh"
 #include "pa_internal.h"
 
@@ -35,7 +37,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 1;
+constexpr int kCtasPerSm = 2;
 constexpr int kGroup = 4;       // tokens per thread and step: one 16-byte store of
                                 // positions, two of slots
 constexpr int kMaxEntries = 4096;  // most sums kept per CTA (32 KB: no opt-in size)
