@@ -39,10 +39,10 @@ cudaError_t launch_attention_varlen(const AttentionVarlenArgs &a, cudaStream_t s
   const int grid = static_cast<int>(pairs * p.hu);
   const bool bf = a.dtype == PA_BF16;
   if (a.head_dim == 64)
-    return bf ? flash::launch<BF16, 64, false>(p, a.tm_q, a.tm_k, a.tm_v, grid, stream)
-              : flash::launch<F16, 64, false>(p, a.tm_q, a.tm_k, a.tm_v, grid, stream);
-  return bf ? flash::launch<BF16, 128, false>(p, a.tm_q, a.tm_k, a.tm_v, grid, stream)
-            : flash::launch<F16, 128, false>(p, a.tm_q, a.tm_k, a.tm_v, grid, stream);
+    return bf ? flash::launch<BF16, 64, flash::kPacked>(p, a.tm_q, a.tm_k, a.tm_v, grid, stream)
+              : flash::launch<F16, 64, flash::kPacked>(p, a.tm_q, a.tm_k, a.tm_v, grid, stream);
+  return bf ? flash::launch<BF16, 128, flash::kPacked>(p, a.tm_q, a.tm_k, a.tm_v, grid, stream)
+            : flash::launch<F16, 128, flash::kPacked>(p, a.tm_q, a.tm_k, a.tm_v, grid, stream);
 }
 
 }  // namespace pa

@@ -167,7 +167,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 template <class E, int D>
 cudaError_t launch_all(const DecodeSharedArgs &a, const flash::Params &f,
                        const dec::DecodeParams &p, cudaStream_t stream) {
-  cudaError_t e = flash::launch<E, D, true>(f, a.tm_q, a.tm_k, a.tm_v, a.runs, stream);
+  // No group has more rows than the batch: within one query tile, the single-
+  // tile build, which has more K and V in flight.
+  cudaError_t e =
+      p.num_seqs <= f.tpt
+          ? flash::launch<E, D, flash::kPagedSingle>(f, a.tm_q, a.tm_k, a.tm_v, a.runs, stream)
+          : flash::launch<E, D, flash::kPaged>(f, a.tm_q, a.tm_k, a.tm_v, a.runs, stream);
   if (e != cudaSuccess) return e;
   e = p.hs > 8 ? dec::launch_kernel<E, D, true, 0, 2, false, true>(a.decode, p, stream)
                : dec::launch_kernel<E, D, true, 0, 1, false, true>(a.decode, p, stream);

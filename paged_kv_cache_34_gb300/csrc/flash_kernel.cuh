@@ -61,12 +61,29 @@ constexpr int kKeys = 128;                 // keys per K/V tile
 constexpr int kItemRing = 4;
 constexpr int kItemTakers = 15;  // 8 softmax warps, 4 epilogue warps, TMA, 2 MMA
 
-template <int D>
+// What a launch is built for.
+enum Mode {
+  kPacked = 0,       // packed prompts over plain rows
+  kPaged = 1,        // prefix pass
+  kPagedSingle = 2,  // ... where no group has more rows than one query tile
+};
+
+template <int D, int MODE>
 struct Layout {
   static constexpr int kHalves = D / 64;         // 128-byte halves per tile row
   static constexpr int kTile = kHalves * kHalf;  // one Q, K or V tile
-  // Three Q buffers and two each of K and V fill the 227 KB at head_dim 128.
-  static constexpr int NQ = D == 128 ? 3 : 4, NK = D == 128 ? 2 : 4, NV = D == 128 ? 2 : 4;
+  // Buffers of 32 KB (16 at head_dim 64), in what the 227 KB hold.  Packed
+  // prompts run through many items: a third Q buffer lets the next one's first
+  // query tile load early.  The prefix pass has few items and K and V from
+  // memory: they get the room (72 us against TODO with the packed split on 8
+  // sequences behind 16384 tokens, 32/32 heads).
+  static constexpr int kUnit = D == 128 ? 1 : 2;
+  // Q buffers of stream A and B; a single-tile launch's streams share theirs.
+  static constexpr int kQA = (MODE == kPacked ? 2 : 1) * kUnit;
+  static constexpr int kQB = (MODE == kPagedSingle ? 0 : 1) * kUnit;
+  static constexpr int NQ = kQA + kQB;
+  static constexpr int NK = (MODE == kPagedSingle ? 3 : 2) * kUnit;
+  static constexpr int NV = (MODE == kPacked ? 2 : 3) * kUnit;
   static constexpr int kQOff = 0;
   static constexpr int kKOff = NQ * kTile;
   static constexpr int kVOff = kKOff + NK * kTile;
@@ -94,6 +111,14 @@ struct Layout {
     kNumBars = kFin + 2
   };
   static constexpr int kNextOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // the answer, 16 B
+  // Buffer and use count of a stream's query tile number q (counted by stream,
+  // or, where they share, by item).
+  static __device__ __forceinline__ int q_slot(int t, int q) {
+    return t == 0 || kQB == 0 ? q % kQA : kQA + q % (kQB > 0 ? kQB : 1);
+  }
+  static __device__ __forceinline__ int q_use(int t, int q) {
+    return t == 0 || kQB == 0 ? q / kQA : q / (kQB > 0 ? kQB : 1);
+  }
   static constexpr int kItemOff = kNextOff + 16;
   static constexpr int kItemWords = 20;
   static constexpr int kMiscOff = kItemOff + kItemRing * kItemWords * 4;  // TMEM base, abort
@@ -117,10 +142,9 @@ struct Item {
   int kv0;       // packed: K/V row of key 0; paged: the block table's row
   int ws_row;    // prefix pass: first workspace row of the item's states
   int base;      // ring position of the first K/V tile
-  int qbase;     // Q buffers taken by earlier items
   int bad;       // prefix pass: a block id was outside the pool
 };
-constexpr int kItemFields = 17;
+constexpr int kItemFields = 16;
 static_assert(sizeof(Item) == kItemFields * 4, "item words");
 enum { kSingle = 1, kTurns = 2, kTail = 4, kTailOdd = 8 };
 
@@ -497,12 +521,13 @@ __device__ __forceinline__ int use_count(const Item &it, int t) {
 __device__ __forceinline__ int use_step(const Item &it) { return (it.flags & kTurns) ? 2 : 1; }
 
 // -------------------------------------------------------------- the kernel --
-template <class E, int D, bool PAGED>
+template <class E, int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     flash_kernel(const Params p, const __grid_constant__ CUtensorMap tmq,
                  const __grid_constant__ CUtensorMap tmk,
                  const __grid_constant__ CUtensorMap tmv) {
-  using L = Layout<D>;
+  using L = Layout<D, MODE>;
+  constexpr bool PAGED = MODE != kPacked;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
   float *s_m = reinterpret_cast<float *>(smem + L::kMlOff), *s_l = s_m + 256;
@@ -548,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n = 1;
       if ((i >= L::kPFull && i < L::kPFull + 2) || (i >= L::kOFree && i < L::kOFree + 2)) n = 4;
       if (i >= L::kMLFull && i < L::kMLFull + 2) n = 128;
+      if (i >= L::kQEmpty && i < L::kQEmpty + L::NQ) n = MODE == kPagedSingle ? 2 : 1;
       if (i >= L::kKEmpty && i < L::kKEmpty + L::NK) n = 2;    // either stream
       if (i >= L::kVEmpty && i < L::kVEmpty + L::NV) n = 2;
       if (i >= L::kVFixed && i < L::kVFixed + L::NV) n = 4;    // the epilogue's warps
@@ -570,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kSchedWarp) {
       // ----------------------------------------------------- scheduler --
       bool ok = true;
-      int base = 0, qbase = 0;
+      int base = 0;
       uint32_t tails = 0;  // parity of each V buffer's tails so far
       PackedSched ps;
       PrefixSched xs;
@@ -592,7 +618,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.flags = 0;
         it.bad = 0;
         it.base = base;
-        it.qbase = qbase;
         if constexpr (PAGED) {
           GroupGeom g;
           int head, pair, i0, i1;
@@ -678,7 +703,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           base += it.nkv;
-          qbase += (it.cnt[0] > 0 ? 1 : 0) + (it.cnt[1] > 0 ? 1 : 0);
         }
         if (j >= kItemRing)
           ok = warp_wait(L::kItemEmpty + j % kItemRing, ((j / kItemRing) - 1) & 1);
@@ -705,7 +729,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nbox = kKeys / bs;  // boxes per tile, lane k loads box k
       const uint32_t q_bytes = static_cast<uint32_t>(p.tpt) * p.pg * D * 2;
       bool ok = true;
-      int nk = 0, nv = 0, nq = 0;   // loads issued
+      int nk = 0, nv = 0;           // loads issued
+      int nq0 = 0, nq1 = 0;         // ... of query tiles, by stream
       // V runs one tile behind K, also from one item to the next
       int v_pos = -1, v_row = 0, v_kvh = 0;
       bool v_valid = false, v_tail = false;
@@ -736,8 +761,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++nv;
         return true;
       };
-      auto load_q = [&](const Item &it, int t, int qi) {
-        const int slot = qi % L::NQ, use = qi / L::NQ;
+      auto load_q = [&](const Item &it, int t) {
+        const int qi = t ? nq1 : nq0;
+        const int slot = L::q_slot(t, qi), use = L::q_use(t, qi);
         if (use > 0 && !warp_wait(L::kQEmpty + slot, (use - 1) & 1)) return false;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(L::kQFull + slot), q_bytes);
@@ -748,7 +774,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(dst + h * kHalf, &tmq, bar(L::kQFull + slot), h * 64, it.head0, tok);
         }
         __syncwarp();
-        ++nq;
+        if (t) ++nq1;
+        else ++nq0;
         return true;
       };
       for (int j = 0; ok; ++j) {
@@ -756,8 +783,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = peek_item(j, &it);
         if (!ok || !it.live || misc[1]) break;
         if (lane == 0) mbar_arrive(bar(L::kBegun));
-        const int t_first = it.cnt[0] > 0 ? 0 : 1;
-        const bool two = it.cnt[0] > 0 && it.cnt[1] > 0;
+        // the streams' query tiles: the first one's before the item's first K
+        // (a shared one counts as stream A's)
+        const bool two = MODE != kPagedSingle && it.cnt[0] > 0 && it.cnt[1] > 0;
+        const int t_first = MODE == kPagedSingle || it.cnt[0] > 0 ? 0 : 1;
         // PAGED: this lane's block ids, the next tile's in flight
         const int32_t *bt = PAGED ? p.block_table + it.kv0 * p.bt_stride : nullptr;
         auto load_id = [&](int i) {
@@ -770,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = load_v();
           v_pos = -1;
         }
-        if (ok) ok = load_q(it, t_first, it.qbase);
+        if (ok) ok = load_q(it, t_first);
         for (int i = 0; ok && i < it.nkv; ++i) {
           const int id_next = PAGED ? load_id(i + 1) : 0;
           int row;
@@ -791,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           ++nk;
           if (v_pos >= 0) ok = load_v();
-          if (ok && i == 0 && two) ok = load_q(it, 1, it.qbase + 1);
+          if (ok && i == 0 && two) ok = load_q(it, 1);
           v_tail = (it.flags & kTail) && i + 1 == it.nkv;
           v_pos = it.base + i;
           v_row = row;
@@ -806,8 +835,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok && lane == 0 && !misc[1]) give_up();
       // Do not leave while copies this CTA issued may still land.
       if (lane == 0) {
-        for (int n = nq - 1; n >= 0 && n >= nq - L::NQ; --n)
-          wait_for(bar(L::kQFull + n % L::NQ), (n / L::NQ) & 1, static_cast<uint32_t>(kWaitLimitNs));
+        for (int n = nq0 - 1; n >= 0 && n >= nq0 - L::kQA; --n)
+          wait_for(bar(L::kQFull + L::q_slot(0, n)), L::q_use(0, n) & 1,
+                   static_cast<uint32_t>(kWaitLimitNs));
+        for (int n = nq1 - 1; n >= 0 && n >= nq1 - L::kQB; --n)
+          wait_for(bar(L::kQFull + L::q_slot(1, n)), L::q_use(1, n) & 1,
+                   static_cast<uint32_t>(kWaitLimitNs));
         for (int n = nk - 1; n >= 0 && n >= nk - L::NK; --n)
           wait_for(bar(L::kKFull + n % L::NK), (n / L::NK) & 1, static_cast<uint32_t>(kWaitLimitNs));
         for (int n = nv - 1; n >= 0 && n >= nv - L::NV; --n)
@@ -825,10 +858,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // measured 1740 cycles per tile step on long prompts, 1064 of them
       // issuing), and P V and the stream's next Q K^T go out in one block.
       //
-      // Each stream accounts for every K and V buffer use, in ring order: by
-      // a commit after the MMAs that read it, or, for a tile it does not use,
-      // by an arrival once the tile has landed (an earlier one would count
-      // towards the buffer's use before).
+      // Each stream accounts for every use of a K or V buffer (and of a Q
+      // buffer, where the streams share it), in order: by a commit after the
+      // MMAs that read it, or, for a tile it does not use, by an arrival once
+      // the tile has landed (an earlier one would count towards the buffer's
+      // use before).  So a stream sees every phase of the buffers it waits
+      // for, and no wait can take an older phase for its own.
       const int t = warp - kMmaWarp0;
       const uint32_t id_qk = idesc_f16(E::kBF16, 128, 128, false) | (p.negate << 13);
       const uint32_t id_pv = idesc_f16(E::kBF16, 128, D, true);
@@ -848,8 +883,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int j = -1;              // the item whose tiles are being issued ...
       int end = 0, left = 0;   // ... its end, its Q K^T still to issue
       int np = kNone;          // ring position of the next Q K^T, where it is known
-      int step = 1, q = 0;     // ring step and Q buffer of the item
-      bool first = false, tail = false, odd = false, ended = false;
+      int step = 1;            // the item's ring step
+      int q = -1;              // the stream's current query tile
+      bool first = false, tail = false, odd = false, ended = false, unused = false;
       int kdone = 0, vdone = 0;  // K and V uses accounted for
       int items = 0, psteps = 0; // items begun (P V), P tiles taken
       // the step whose Q K^T is out and whose P V is to come
@@ -875,7 +911,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         first = true;
         tail = (it.flags & kTail) != 0;
         odd = (it.flags & kTailOdd) != 0;
-        q = it.qbase + (t == 1 && it.cnt[0] > 0 ? 1 : 0);
+        if (left > 0 || MODE == kPagedSingle) ++q;
+        unused = left == 0;
       };
       // Accounts for the tiles before ring position m that this stream does
       // not use.
@@ -893,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // The elected lane's part of S = Q K_n^T.
       auto issue_qk = [&](int n) {
-        const int qs = q % L::NQ;
+        const int qs = L::q_slot(t, q);
         const uint64_t qd = q_desc0 + static_cast<uint64_t>(qs) * (L::kTile >> 4);
         const uint64_t kd = k_desc0 + static_cast<uint64_t>(n % L::NK) * (L::kTile >> 4);
         // K step k: 16 columns = 32 bytes into a 128-byte swizzled row, the
@@ -927,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool along = false;
           if (ok && np <= n + 2) {
             along = ready(L::kKFull + np % L::NK, (np / L::NK) & 1);
-            if (along && first) along = ready(L::kQFull + q % L::NQ, (q / L::NQ) & 1);
+            if (along && first) along = ready(L::kQFull + L::q_slot(t, q), L::q_use(t, q) & 1);
           }
           if (ok && pfirst) {  // O of the stream's previous item has been read
             if (items > 0) ok = wait(L::kOFree + t, (items - 1) & 1);
@@ -968,6 +1005,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Otherwise walk to the next tile the stream uses.
         while (ok && !ended && left == 0) {
           skip_to(end);
+          if (MODE == kPagedSingle && unused && ok) {
+            ok = wait(L::kQFull + L::q_slot(t, q), L::q_use(t, q) & 1);
+            if (lane == 0) mbar_arrive(bar(L::kQEmpty + L::q_slot(t, q)));
+          }
           if (ok) next_item();
         }
         if (ended) {
@@ -977,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const int m = np;
         skip_to(m);
-        if (ok && first) ok = wait(L::kQFull + q % L::NQ, (q / L::NQ) & 1);
+        if (ok && first) ok = wait(L::kQFull + L::q_slot(t, q), L::q_use(t, q) & 1);
         if (ok) ok = wait(L::kKFull + m % L::NK, (m / L::NK) & 1);
         if (!ok) break;
         tc_fence_after();
@@ -1271,14 +1312,14 @@ cudaError_t check_register_pool() {
   return status;
 }
 
-template <class E, int D, bool PAGED>
+template <class E, int D, int MODE>
 cudaError_t launch(const Params &p, const CUtensorMap &tmq, const CUtensorMap &tmk,
                    const CUtensorMap &tmv, int grid, cudaStream_t stream) {
-  constexpr auto kernel = flash_kernel<E, D, PAGED>;
+  constexpr auto kernel = flash_kernel<E, D, MODE>;
   cudaError_t e = allow_dynamic_smem<kernel>();
   if (e == cudaSuccess) e = check_register_pool<kernel>();
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), Layout<D>::kBytes,
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), Layout<D, MODE>::kBytes,
                     stream, p, tmq, tmk, tmv);
 }
 
