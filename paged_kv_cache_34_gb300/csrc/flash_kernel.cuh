@@ -206,6 +206,20 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, uint32_t
   return ok;
 }
 
+// Whether the phase is over, without waiting (try_wait suspends the thread for
+// microseconds where it is not).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -963,7 +977,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (left == 0) next_item();  // where the stream goes on, if at once
           bool along = false;
           if (ok && np <= n + 2) {
-            along = ready(L::kKFull + np % L::NK, (np / L::NK) & 1);
+            const int kb = L::kKFull + np % L::NK;
+            const uint32_t kp = (np / L::NK) & 1;
+            // By turns the load of K is what the stream waits for: only look.
+            // Else K is about to land, and waiting for it keeps P V and Q K^T
+            // in one block (prefix pass, looking / waiting: 64 / 72 us on 64
+            // sequences in 6 groups, 365 / 351 on 256 of one).
+            along = PAGED && step == 2 ? __all_sync(0xffffffffu, mbar_test(bar(kb), kp)) != 0
+                                       : ready(kb, kp);
             if (along && first) along = ready(L::kQFull + L::q_slot(t, q), L::q_use(t, q) & 1);
           }
           if (ok && pfirst) {  // O of the stream's previous item has been read
