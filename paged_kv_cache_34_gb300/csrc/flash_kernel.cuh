@@ -362,9 +362,9 @@ __device__ inline bool check_cu(const Params &p, int lane) {
 // at U (cost w per tile) belongs to run (U + w i) / C.  C >= 2 leaves no run
 // inside a unit without a tile, so a unit's states are those of runs
 // U / C .. (U + w (nkt - 1)) / C.  Warp-collective.
+// All costs fit 31 bits (the host sends larger batches elsewhere).
 struct GroupGeom {
-  int first, n, nkt, prefix;
-  int64_t cost;
+  int first, n, nkt, prefix, cost;
 };
 __device__ __forceinline__ GroupGeom group_geom(const Params &p, int g) {
   GroupGeom r;
@@ -377,7 +377,7 @@ __device__ __forceinline__ GroupGeom group_geom(const Params &p, int g) {
   if (len < 0 || len > p.max_prefix || len > p.capacity) return r;  // reported by check_groups
   r.prefix = len;
   r.nkt = (len + kKeys - 1) / kKeys;
-  r.cost = static_cast<int64_t>(p.hu) * tiles_of(p, r.n) * r.nkt;
+  r.cost = p.hu * tiles_of(p, r.n) * r.nkt;
   return r;
 }
 
@@ -385,23 +385,22 @@ __device__ __forceinline__ GroupGeom group_geom(const Params &p, int g) {
 // else makes the whole call a plain decode (no prefix is shared).  A prefix
 // length that does not fit is taken as none.  Returns whether the groups are
 // usable; *total is the batch's cost.
-__device__ inline bool check_groups(const Params &p, int lane, bool report, int64_t *total) {
+__device__ inline bool check_groups(const Params &p, int lane, bool report, int *total) {
   bool bad = false, bad_len = false;
-  int64_t sum = 0;
+  int sum = 0;
   if (lane == 0)
     bad = __ldg(p.group_starts) != 0 || __ldg(p.group_starts + p.num_groups) != p.num_seqs;
   for (int g = lane; g < p.num_groups; g += 32) {
     const int a = __ldg(p.group_starts + g), e = __ldg(p.group_starts + g + 1);
-    bad |= a < 0 || e < a || e > p.num_seqs;
     const int len = __ldg(p.prefix_lens + g);
+    const bool odd = a < 0 || e < a || e > p.num_seqs;
+    bad |= odd;
     bad_len |= len < 0 || len > p.max_prefix || len > p.capacity;
-    sum += group_geom(p, g).cost;
+    if (!odd) sum += group_geom(p, g).cost;
   }
   bad = __any_sync(0xffffffffu, bad);
   bad_len = __any_sync(0xffffffffu, bad_len);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  *total = bad ? 0 : sum;
+  *total = bad ? 0 : __reduce_add_sync(0xffffffffu, sum);
   if (report && lane == 0) {
     if (bad) raise_error(p.err, PA_DEVERR_CU_SEQLENS);
     if (bad_len) raise_error(p.err, PA_DEVERR_CONTEXT);
@@ -409,57 +408,58 @@ __device__ inline bool check_groups(const Params &p, int lane, bool report, int6
   return !bad;
 }
 
-__host__ __device__ __forceinline__ int64_t run_cost(int64_t total, int runs) {
-  const int64_t c = (total + runs - 1) / runs;
+__device__ __forceinline__ int run_cost(int total, int runs) {
+  const int c = static_cast<int>((static_cast<unsigned>(total) + runs - 1) / runs);
   return c < 2 ? 2 : c;
 }
 
-// What the joining kernel needs: int32 words 0-1 the run cost C (int64), then
-// from word 8 on 8 words per sequence: prefix length (0: none), the group's
-// first sequence, its size, 0, and its first cost position (int64).
-constexpr int kInfoWords = 8;
+// Sum of v over the lanes up to this one.
+__device__ __forceinline__ int warp_scan(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  return v;
+}
 
-// Warp-collective.
-__device__ inline void write_info(const Params &p, int lane, bool good, int64_t total) {
-  if (lane == 0) *reinterpret_cast<int64_t *>(p.ws_info) = run_cost(total, gridDim.x);
+// What the joining kernel needs, in words of 4: first the run cost C, then for
+// each sequence its prefix length (0: none), the group's first sequence, its
+// size and its first cost position.  Warp-collective.
+constexpr int kInfoWords = 4;
+__device__ inline void write_info(const Params &p, int lane, bool good, int total) {
+  if (lane == 0) p.ws_info[0] = run_cost(total, gridDim.x);
   if (!good) {
     for (int b = lane; b < p.num_seqs; b += 32)
       p.ws_info[static_cast<int64_t>(b + 1) * kInfoWords] = 0;
     return;
   }
-  int64_t gbase = 0;
+  int gbase = 0;
   for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
     const GroupGeom r = group_geom(p, g0 + lane);
-    int64_t incl = r.cost;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const int64_t lo = gbase + incl - r.cost;
-    gbase = __shfl_sync(0xffffffffu, gbase + incl, 31);
+    const int incl = warp_scan(r.cost, lane);
+    const int lo = gbase + incl - r.cost;
+    gbase += __shfl_sync(0xffffffffu, incl, 31);
     for (int i = 0; i < 32 && g0 + i < p.num_groups; ++i) {
       const int first = __shfl_sync(0xffffffffu, r.first, i);
       const int n = __shfl_sync(0xffffffffu, r.n, i);
       const int pre = __shfl_sync(0xffffffffu, r.prefix, i);
-      const int64_t at = __shfl_sync(0xffffffffu, lo, i);
-      for (int b = lane; b < n; b += 32) {
-        int32_t *w = p.ws_info + static_cast<int64_t>(first + b + 1) * kInfoWords;
-        *reinterpret_cast<int4 *>(w) = make_int4(pre, first, n, 0);
-        *reinterpret_cast<int64_t *>(w + 4) = at;
-      }
+      const int at = __shfl_sync(0xffffffffu, lo, i);
+      for (int b = lane; b < n; b += 32)
+        *reinterpret_cast<int4 *>(p.ws_info + static_cast<int64_t>(first + b + 1) * kInfoWords) =
+            make_int4(pre, first, n, at);
     }
   }
 }
 
 struct PrefixSched {
-  int64_t x, xend, gbase;
-  int g0;
+  int x, xend, gbase, g0;
 
-  __device__ void init(const Params &p, int64_t total) {
-    const int64_t C = run_cost(total, gridDim.x);
-    x = min(static_cast<int64_t>(blockIdx.x) * C, total);
-    xend = min(x + C, total);
+  __device__ void init(const Params &p, int total) {
+    const int C = run_cost(total, gridDim.x);
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * C;
+    x = at < total ? static_cast<int>(at) : total;
+    xend = total - x > C ? x + C : total;
     gbase = 0;
     g0 = 0;
   }
@@ -469,13 +469,8 @@ struct PrefixSched {
     while (x < xend) {
       for (; g0 < p.num_groups; g0 += 32) {
         const GroupGeom r = group_geom(p, g0 + lane);
-        int64_t incl = r.cost;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
-        }
-        const int64_t lo = gbase + incl - r.cost, hi = gbase + incl;
+        const int incl = warp_scan(r.cost, lane);
+        const int hi = gbase + incl, lo = hi - r.cost;
         const unsigned hit = __ballot_sync(0xffffffffu, x >= lo && x < hi);
         if (hit) {
           const int src = __ffs(hit) - 1;
@@ -484,23 +479,22 @@ struct PrefixSched {
           s.n = __shfl_sync(0xffffffffu, r.n, src);
           s.nkt = __shfl_sync(0xffffffffu, r.nkt, src);
           s.prefix = __shfl_sync(0xffffffffu, r.prefix, src);
-          const int64_t start = __shfl_sync(0xffffffffu, lo, src);
-          const int64_t per_head = static_cast<int64_t>(tiles_of(p, s.n)) * s.nkt;
-          const int64_t rem = x - start;
-          const int64_t h = rem / per_head;
-          const int64_t in_head = rem - h * per_head;
-          const int64_t q = in_head / (2 * static_cast<int64_t>(s.nkt));
-          const int w = 2 * q + 1 < tiles_of(p, s.n) ? 2 : 1;
-          const int64_t U = start + h * per_head + q * 2 * s.nkt;
-          const int64_t a = (x - U + w - 1) / w;
-          const int64_t b = min(static_cast<int64_t>(s.nkt), (xend - U + w - 1) / w);
-          x = min(xend, U + static_cast<int64_t>(w) * s.nkt);
+          const int start = __shfl_sync(0xffffffffu, lo, src);
+          const int tiles = tiles_of(p, s.n);
+          const unsigned per_head = static_cast<unsigned>(tiles) * s.nkt;
+          const unsigned rem = x - start, h = rem / per_head, in_head = rem - h * per_head;
+          const unsigned q = in_head / (2u * s.nkt);
+          const int w = 2 * static_cast<int>(q) + 1 < tiles ? 2 : 1;
+          const int U = start + static_cast<int>(h * per_head + q * 2u * s.nkt);
+          const int a = (x - U + w - 1) >> (w - 1);
+          const int b = min(s.nkt, (xend - U + w - 1) >> (w - 1));
+          x = min(xend, U + w * s.nkt);
           if (a >= b) break;  // the rest of the unit's last tile lies in the run before
           *geom = s;
           *head = static_cast<int>(h);
           *pair = static_cast<int>(q);
-          *i0 = static_cast<int>(a);
-          *i1 = static_cast<int>(b);
+          *i0 = a;
+          *i1 = b;
           return true;
         }
         gbase = __shfl_sync(0xffffffffu, hi, 31);
@@ -600,6 +594,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(const_cast<int *>(misc)), kTmemCols);
     tmem_relinquish();
   }
+  // The scheduler reads the batch while the others set up.
+  PackedSched ps;
+  PrefixSched xs;
+  bool groups_ok = true;
+  int groups_cost = 0;
+  if (warp == kSchedWarp) {
+    if constexpr (PAGED) {
+      groups_ok = check_groups(p, lane, blockIdx.x == 0, &groups_cost);
+      xs.init(p, groups_cost);
+    } else {
+      ps.init(p, lane);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -612,18 +619,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int base = 0;
       uint32_t tails = 0;  // parity of each V buffer's tails so far
-      PackedSched ps;
-      PrefixSched xs;
-      if constexpr (PAGED) {
-        int64_t total;
-        const bool good = check_groups(p, lane, blockIdx.x == 0, &total);
-        xs.init(p, total);
-        if (blockIdx.x == 0) write_info(p, lane, good, total);
-      } else {
-        if (blockIdx.x == 0 && !check_cu(p, lane) && lane == 0)
-          raise_error(p.err, PA_DEVERR_CU_SEQLENS);
-        ps.init(p, lane);
-      }
       int x = blockIdx.x;  // packed prompts: the item in hand
       int asked = 0;       // ... and requests made for the next
       for (int j = 0;; ++j) {
@@ -732,6 +727,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a request that was given up on still lands before the CTA leaves
       if (asked > 0 && lane == 0) wait_for(bar(L::kNext), (asked - 1) & 1, static_cast<uint32_t>(kWaitLimitNs));
       if (!ok && lane == 0) give_up();
+      if (blockIdx.x == 0) {
+        if constexpr (PAGED) {
+          write_info(p, lane, groups_ok, groups_cost);
+        } else {
+          if (!check_cu(p, lane) && lane == 0) raise_error(p.err, PA_DEVERR_CU_SEQLENS);
+        }
+      }
     } else if (warp == kTmaWarp) {
       // ----------------------------------------------------------- TMA --
       if (lane == 0) {

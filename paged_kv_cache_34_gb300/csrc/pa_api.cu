@@ -894,7 +894,10 @@ pa_status shared_plan(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
   if (st != PA_OK) return st;
   const cudaError_t e = current_num_sms(&s.sms);
   if (e != cudaSuccess) return cuda_fail(e);
-  s.shared = num_seqs > 0 && num_groups > 0 && max_prefix_len > 0 && max_context_len > 0 && P == 0;
+  s.shared = num_seqs > 0 && num_groups > 0 && max_prefix_len > 0 && max_context_len > 0 &&
+             P == 0 &&
+             pa::shared_cost(num_seqs, num_groups, num_q_heads, num_kv_heads, max_prefix_len) <
+                 (1LL << 30);
   s.bytes = s.decode_bytes;
   if (s.shared) {
     s.runs = pa::shared_runs(num_seqs, num_groups, num_q_heads, num_kv_heads, max_prefix_len,
@@ -902,7 +905,7 @@ pa_status shared_plan(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
     const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads + 256 * static_cast<size_t>(s.runs);
     s.o_bytes = align256(rows * head_dim * sizeof(float));
     s.ml_bytes = align256(rows * 2 * sizeof(float));
-    s.bytes += s.o_bytes + s.ml_bytes + align256((static_cast<size_t>(num_seqs) + 1) * 32);
+    s.bytes += s.o_bytes + s.ml_bytes + align256((static_cast<size_t>(num_seqs) + 1) * 16);
   }
   *out = s;
   return PA_OK;

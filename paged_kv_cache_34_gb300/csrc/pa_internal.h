@@ -223,13 +223,20 @@ struct AttentionVarlenArgs {
 };
 cudaError_t launch_attention_varlen(const AttentionVarlenArgs &a, cudaStream_t stream);
 
-// Runs of the prefix pass: one per CTA, at most one per SM; a run takes at
-// least two K/V tiles of one query tile (see flash_kernel.cuh).
+// The most the prefix pass can cost, and its runs: one per CTA, at most one per
+// SM; a run takes at least two K/V tiles of one query tile (see
+// flash_kernel.cuh).
+inline int64_t shared_cost(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
+                           int max_prefix) {
+  const int pg = flash_packed_heads(num_q_heads / num_kv_heads), tpt = 128 / pg;
+  const int64_t tiles =
+      (static_cast<int64_t>(num_seqs) / tpt + num_groups) * (num_q_heads / pg);
+  return tiles * ((max_prefix + 127) / 128);
+}
 inline int shared_runs(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
                        int max_prefix, int num_sms) {
-  const int pg = flash_packed_heads(num_q_heads / num_kv_heads), tpt = 128 / pg;
-  const int64_t tiles = (static_cast<int64_t>(num_seqs) / tpt + num_groups) * (num_q_heads / pg);
-  const int64_t cost = tiles * ((max_prefix + 127) / 128);
+  const int64_t cost =
+      shared_cost(num_seqs, num_groups, num_q_heads, num_kv_heads, max_prefix);
   const int64_t runs = (cost + 1) / 2;
   return static_cast<int>(runs < 1 ? 1 : (runs < num_sms ? runs : num_sms));
 }
@@ -245,7 +252,7 @@ struct DecodeSharedArgs {
   CUtensorMap tm_q;    // box 64 x packed_heads x 128 / packed_heads
   CUtensorMap tm_k, tm_v;  // box 64 x 1 x block_size
   float *ws_o, *ws_ml;     // [num_seqs * num_q_heads + 256 * runs, D] and [.., 2]
-  int32_t *ws_info;        // 8 words, then 8 per sequence
+  int32_t *ws_info;        // 4 words, then 4 per sequence
 };
 cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream);
 
