@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
             mbar_wait_bounded(smem_u32(full + (k % NS)), (k / NS) & 1);
         }
         cp_async_wait_all();
-        if constexpr (SH) griddep_wait();
+        if (SH && blockIdx.x == 0) griddep_wait();
         return;
       }
       if (live == 0) {
@@ -720,7 +720,9 @@ __global__ void __launch_bounds__(threads_for(WR), kDecodeCtasPerSm)
             mbar_wait_bounded(smem_u32(full + (k % NS)), (k / NS) & 1);
         }
         cp_async_wait_all();
-        if constexpr (SH) griddep_wait();  // the join waits for both launches by this one
+        // the join waits for both launches by this one; one block is enough,
+        // the others leave their SMs to blocks that still wait for one
+        if (SH && blockIdx.x == 0) griddep_wait();
         return;
       }
       const uint32_t bar = smem_u32(full + s);

@@ -223,9 +223,8 @@ struct AttentionVarlenArgs {
 };
 cudaError_t launch_attention_varlen(const AttentionVarlenArgs &a, cudaStream_t stream);
 
-// The most the prefix pass can cost, and its runs: one per CTA, at most one per
-// SM; a run takes at least two K/V tiles of one query tile (see
-// flash_kernel.cuh).
+// The most the prefix pass can cost (see flash_kernel.cuh), and its runs: one per
+// CTA, at most one per SM; a run costs at least 2.
 inline int64_t shared_cost(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
                            int max_prefix) {
   const int pg = flash_packed_heads(num_q_heads / num_kv_heads), tpt = 128 / pg;
@@ -233,12 +232,20 @@ inline int64_t shared_cost(int num_seqs, int num_groups, int num_q_heads, int nu
       (static_cast<int64_t>(num_seqs) / tpt + num_groups) * (num_q_heads / pg);
   return tiles * ((max_prefix + 127) / 128);
 }
+
+
+// The own parts start on the SMs that the prefix pass leaves free, so a pass of
+// a few tiles per SM, which is mostly start-up, takes half of the SMs (32
+// sequences over 4000 tokens: 27.6 us against 30.5 with all of them).  A
+// longer pass takes them all: beside it the own parts would only take its
+// bandwidth (64 sequences in 6 groups: 57.5 us with all, 69 with half; 256
+// sequences over 32768 tokens: 322 with all, 328 / 360 with 16 / 32 fewer).
 inline int shared_runs(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
                        int max_prefix, int num_sms) {
   const int64_t cost =
       shared_cost(num_seqs, num_groups, num_q_heads, num_kv_heads, max_prefix);
-  const int64_t runs = (cost + 1) / 2;
-  return static_cast<int>(runs < 1 ? 1 : (runs < num_sms ? runs : num_sms));
+  const int64_t runs = (cost + 1) / 2, most = cost <= 6LL * num_sms ? num_sms / 2 : num_sms;
+  return static_cast<int>(runs < 1 ? 1 : (runs < most ? runs : most));
 }
 
 struct DecodeSharedArgs {
