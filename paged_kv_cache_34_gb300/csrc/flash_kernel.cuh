@@ -52,7 +52,7 @@ constexpr int kThreads = 512;
 constexpr int kEpiWarp0 = 8, kTmaWarp = 12, kMmaWarp0 = 13, kSchedWarp = 15;  // MMA: 13 A, 14 B
 // Registers per thread after the split (setmaxnreg, per warpgroup); they must
 // fit in what the CTA is launched with (checked on the host).
-constexpr int kSoftmaxRegs = 152, kEpilogueRegs = 104, kProducerRegs = 104;
+constexpr int kSoftmaxRegs = 168, kEpilogueRegs = 88, kProducerRegs = 88;
 constexpr int kRegPoolNeeded = 128 * (2 * kSoftmaxRegs + kEpilogueRegs + kProducerRegs);
 constexpr int kHalf = 128 * 128;  // 128 rows x 64 elements x 2 B
 constexpr uint32_t kTmemCols = 512;        // S_A | S_B | O_A | O_B (P_t overlays S_t)
@@ -594,17 +594,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(const_cast<int *>(misc)), kTmemCols);
     tmem_relinquish();
   }
-  // The scheduler reads the batch while the others set up.
-  PackedSched ps;
+  // The prefix pass's scheduler reads the batch while the others set up.
   PrefixSched xs;
   bool groups_ok = true;
   int groups_cost = 0;
-  if (warp == kSchedWarp) {
-    if constexpr (PAGED) {
+  if constexpr (PAGED) {
+    if (warp == kSchedWarp) {
       groups_ok = check_groups(p, lane, blockIdx.x == 0, &groups_cost);
       xs.init(p, groups_cost);
-    } else {
-      ps.init(p, lane);
     }
   }
   tc_fence_before();
@@ -619,6 +616,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int base = 0;
       uint32_t tails = 0;  // parity of each V buffer's tails so far
+      PackedSched ps;
+      if constexpr (!PAGED) {
+        if (blockIdx.x == 0 && !check_cu(p, lane) && lane == 0)
+          raise_error(p.err, PA_DEVERR_CU_SEQLENS);
+        ps.init(p, lane);
+      }
       int x = blockIdx.x;  // packed prompts: the item in hand
       int asked = 0;       // ... and requests made for the next
       for (int j = 0;; ++j) {
@@ -727,12 +730,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a request that was given up on still lands before the CTA leaves
       if (asked > 0 && lane == 0) wait_for(bar(L::kNext), (asked - 1) & 1, static_cast<uint32_t>(kWaitLimitNs));
       if (!ok && lane == 0) give_up();
-      if (blockIdx.x == 0) {
-        if constexpr (PAGED) {
-          write_info(p, lane, groups_ok, groups_cost);
-        } else {
-          if (!check_cu(p, lane) && lane == 0) raise_error(p.err, PA_DEVERR_CU_SEQLENS);
-        }
+      if constexpr (PAGED) {
+        if (blockIdx.x == 0) write_info(p, lane, groups_ok, groups_cost);
       }
     } else if (warp == kTmaWarp) {
       // ----------------------------------------------------------- TMA --
