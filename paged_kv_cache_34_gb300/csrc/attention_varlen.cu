@@ -28,6 +28,7 @@ cudaError_t launch_attention_varlen(const AttentionVarlenArgs &a, cudaStream_t s
   p.max_seqlen = a.max_seqlen;
   p.err = a.d_error;
   p.wait_ns = flash::wait_limit(a.wait_ns);
+  p.out_wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_row_stride % 16 == 0;
   p.kv_bytes = 4 * a.head_dim;
   // One CTA per item, pairs of query tiles x head units: at most one pair of
   // a sequence is partly filled.

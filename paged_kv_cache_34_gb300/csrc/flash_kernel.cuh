@@ -154,6 +154,7 @@ struct Params {
   int64_t out_row_stride;
   int32_t hq, group, pg, tpt;  // heads, per KV head, per tile row group; rows (tokens) per tile
   int32_t hu;               // head units: hq / pg
+  bool out_wide;            // packed: output rows are 32-byte aligned
   float scale_log2;         // |scale| * log2 e
   uint32_t negate;          // 1: the scale is negative, Q enters the product negated
   int32_t causal;
@@ -1145,34 +1146,61 @@ __global__ void __launch_bounds__(kThreads, 1)
           orow = static_cast<typename E::T *>(p.out) +
                  static_cast<int64_t>(it.q0 + tok) * p.out_row_stride + (it.head0 + hl) * D;
         }
+        const int t0 = use[0] ? 0 : 1;
+        const bool both = use[0] && use[1];
+        const uint64_t fa = f2_pack(t0 ? f[1] : f[0], t0 ? f[1] : f[0]);
+        const uint64_t fb = f2_pack(f[1], f[1]);
+        // rows that saw no key are 0, whatever O holds
+        const bool none = !(ll > 0.f) || bad;
+        const bool any_none = __any_sync(0xffffffffu, none && row_ok);
+        // 32 bytes a lane and store: a store's 32 rows are 32 lines to the
+        // load/store unit either way
+        const bool wide = PAGED || p.out_wide;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.f;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (!use[t]) continue;
-            uint32_t v[32];
-            tmem_ld32(o_tm + t * 128 + c * 32, v);
+        for (int c = 0; c < D; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(o_tm + t0 * 128 + c, v);
+          uint64_t o[16];  // column pairs
+          if (both) {
+            uint32_t x[32];
+            tmem_ld32(o_tm + 128 + c, x);
             tmem_wait_ld();
-            // a row that saw no key (f = 0) adds nothing, whatever O holds
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              o[i] = f[t] != 0.f ? fmaf(__uint_as_float(v[i]), f[t], o[i]) : o[i];
+            for (int i = 0; i < 16; ++i)
+              o[i] = f2_fma(f2_words(x[2 * i], x[2 * i + 1]), fb,
+                            f2_mul(f2_words(v[2 * i], v[2 * i + 1]), fa));
+          } else {
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = f2_mul(f2_words(v[2 * i], v[2 * i + 1]), fa);
+          }
+          if (any_none) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = none ? 0ull : o[i];
+          }
+          constexpr int kWords = PAGED ? 32 : 16;
+          uint32_t w[kWords];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float a, b;
+            f2_unpack(o[i], a, b);
+            if constexpr (PAGED) {
+              w[2 * i] = __float_as_uint(a);
+              w[2 * i + 1] = __float_as_uint(b);
+            } else {
+              w[i] = E::pack2(a, b);
+            }
           }
           if (row_ok) {
-            if constexpr (PAGED) {
+            uint32_t *dst = PAGED ? reinterpret_cast<uint32_t *>(wrow + c)
+                                  : reinterpret_cast<uint32_t *>(orow + c);
+            if (wide) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<float4 *>(wrow + c * 32 + i * 4) =
-                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              for (int i = 0; i < kWords; i += 8) store_32b(dst + i, w + i);
             } else {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4 *>(orow + c * 32 + i * 8) = make_uint4(
-                    E::pack2(o[8 * i], o[8 * i + 1]), E::pack2(o[8 * i + 2], o[8 * i + 3]),
-                    E::pack2(o[8 * i + 4], o[8 * i + 5]), E::pack2(o[8 * i + 6], o[8 * i + 7]));
+              for (int i = 0; i < kWords; i += 4)
+                *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
             }
           }
         }
