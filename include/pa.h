@@ -544,8 +544,8 @@ pa_status pa_copy_blocks(void *key_cache, void *value_cache, int64_t block_bytes
  *   slot_mapping      int64 [max_tokens];
  *   positions         int32 [max_tokens], nullable.
  *   num_free_out      int32 [1].
- * No output may overlap an input (PA_ERR_SHAPE where context_lens_out or
- * num_free_out does); the same inputs give the same outputs again.
+ * No output may overlap an input (PA_ERR_SHAPE); the same inputs give the same
+ * outputs again.
  *
  * A request that cannot be served takes no blocks, its tokens get slot -1 and
  * its context_lens_out is 0 (its cached tokens stay where they are; the
@@ -635,10 +635,11 @@ pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *que
  * alone, like pa_decode.  A bad block id sets PA_DEVERR_BLOCK_ID and its
  * piece of the context adds nothing.
  * The workspace (256-byte aligned) is of pa_decode_shared_plan's size for the
- * same shape.  Without groups, or where num_seqs * num_kv_heads *
- * max_context_len reaches 2^30 (and a GQA group of more than 16 heads counts
- * once per 16), the call is pa_decode.
- * Supported: 16-bit pools; head_dim 64 or 128; block_size 8, 16, 32, 64 or
+ * same shape.  Without groups, or with max_prefix_len 0, the call is pa_decode.
+ * K and V of all P positions of a prefix must be finite for the outputs of the
+ * group's shorter sequences (L < P) to be.
+ * Supported: num_seqs * num_kv_heads * max_context_len < 2^30 (a GQA group of
+ * more than 16 heads counts once per 16) and bounds < 2^30; 16-bit pools; head_dim 64 or 128; block_size 8, 16, 32, 64 or
  * 128; any num_q_heads % num_kv_heads == 0.
  */
 pa_status pa_decode_shared_plan(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,

@@ -263,6 +263,13 @@ def _bad_device(name, dev):
                      "device, or of the host, would fault")
 
 
+def _check_error(t, dev):
+    if t.dtype is not torch.int32 or t.numel() < 1:
+        raise ValueError("d_error must be an int32 tensor")
+    if t.get_device() != dev:
+        _bad_device("d_error", dev)
+
+
 def _current(dev):
     """The call's device is the current one, where its kernels are launched."""
     if dev < 0 or dev != torch._C._cuda_getDevice():
@@ -307,8 +314,10 @@ def pa_build_tables(block_table, context_lens, query_lens, free_blocks, num_free
         if x.dtype is not v[2] or x.numel() != v[1] or x.get_device() != dev \
                 or not x.is_contiguous():
             _bad_vector(*v, dev)
-    if block_table.get_device() != dev or (d_error is not None and d_error.get_device() != dev):
-        _bad_device("block_table or d_error", dev)
+    if block_table.get_device() != dev:
+        _bad_device("block_table", dev)
+    if d_error is not None:
+        _check_error(d_error, dev)
     _current(dev)
     st = lib.pa_build_tables(block_table.data_ptr(), stride if s > 1 else width, width,
                              context_lens.data_ptr(), query_lens.data_ptr(),
@@ -540,8 +549,8 @@ def pa_attention_varlen(out, query, key, value, cu_seqlens, *, scale, max_seqlen
     for x in (out, key, value, cu_seqlens):
         if x.get_device() != dev:
             _bad_device("out, key, value or cu_seqlens", dev)
-    if d_error is not None and d_error.get_device() != dev:
-        _bad_device("d_error", dev)
+    if d_error is not None:
+        _check_error(d_error, dev)
     _current(dev)
     st = lib.pa_attention_varlen(out.data_ptr(), os, query.data_ptr(), qs, key.data_ptr(),
                                  value.data_ptr(), ks, cu_seqlens.data_ptr(), n - 1, t,
@@ -598,13 +607,17 @@ def pa_decode_shared(out, query, key_cache, value_cache, block_table, context_le
                 or not x.is_contiguous():
             _bad_vector(*v, dev)
     os, qs = _rows(out, "out"), _rows(query, "query")
-    for x in (out, key_cache, value_cache, block_table, workspace, d_error):
+    for x in (out, key_cache, value_cache, block_table, workspace):
         if x is not None and x.get_device() != dev:
-            _bad_device("out, caches, block_table, workspace or d_error", dev)
+            _bad_device("out, caches, block_table or workspace", dev)
+    if d_error is not None:
+        _check_error(d_error, dev)
     _current(dev)
     if workspace is None:
         need = pa_decode_shared_plan(s, g, hq, hkv, d, max_context_len, max_prefix_len, lib=lib)
-        workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+        # on the call's stream: a later allocation of another one must not get it
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
     st = lib.pa_decode_shared(
         out.data_ptr(), os, query.data_ptr(), qs, key_cache.data_ptr(), value_cache.data_ptr(),
         block_table.data_ptr(), stride if s > 1 else width, width, context_lens.data_ptr(),

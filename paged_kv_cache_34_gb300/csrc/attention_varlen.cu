@@ -30,14 +30,7 @@ cudaError_t launch_attention_varlen(const AttentionVarlenArgs &a, cudaStream_t s
   p.wait_ns = flash::wait_limit(a.wait_ns);
   p.out_wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_row_stride % 16 == 0;
   p.kv_bytes = 4 * a.head_dim;
-  // One CTA per item, pairs of query tiles x head units: at most one pair of
-  // a sequence is partly filled.
-  const int64_t longest = a.max_seqlen < a.total ? a.max_seqlen : a.total;
-  int64_t pairs = a.total / (2 * p.tpt) + static_cast<int64_t>(a.num_seqs);
-  const int64_t most = a.num_seqs * ((longest + 2 * p.tpt - 1) / (2 * p.tpt));
-  if (pairs > most) pairs = most;
-  if (pairs * p.hu > 0x7fffffff) return cudaErrorInvalidValue;
-  const int grid = static_cast<int>(pairs * p.hu);
+  const int grid = static_cast<int>(a.grid);
   const bool bf = a.dtype == PA_BF16;
   if (a.head_dim == 64)
     return bf ? flash::launch<BF16, 64, flash::kPacked>(p, a.tm_q, a.tm_k, a.tm_v, grid, stream)

@@ -123,8 +123,8 @@ bool use_balanced(int num_seqs, int units, int max_ctx, int partition_size) {
 }
 
 // Fixed split-KV plan.  Auto: every worker warp (kDecodeWarps per CTA,
-// kDecodeCtasPerSm CTAs per SM) should get about eight items of the largest possible batch, so the static
-// item schedule balances; a partition is at least 64 tokens (128 when eight
+// kDecodeCtasPerSm CTAs per SM) should get about eight items of the largest
+// possible batch, so the static item schedule balances; a partition is at least 64 tokens (128 when eight
 // query heads share a KV head) so the partial states stay a few percent of the
 // K/V bytes.
 int plan_partition(int num_seqs, int num_q_heads, int num_kv_heads, int max_ctx,
@@ -316,14 +316,30 @@ pa_status pa_build_tables(int32_t *block_table, int64_t block_table_stride,
        reinterpret_cast<uintptr_t>(num_free_out)) & 3u)
     return PA_ERR_ALIGN;
   if (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) return PA_ERR_ALIGN;
-  // every CTA reads the lengths and the list's length while others write
-  auto overlaps = [](const int32_t *x, int64_t nx, const int32_t *y, int64_t ny) {
-    return nx > 0 && ny > 0 && x < y + ny && y < x + nx;
+  // Every CTA reads the inputs while others write.  (The block table is both:
+  // entries that are read are not written.)
+  struct Range {
+    const void *p;
+    int64_t bytes;
   };
-  if (overlaps(context_lens_out, num_seqs, context_lens, num_seqs) ||
-      overlaps(context_lens_out, num_seqs, query_lens, num_seqs) ||
-      overlaps(num_free_out, 1, num_free, 1))
-    return PA_ERR_SHAPE;
+  const int64_t seqs = num_seqs;
+  const Range table = {block_table, seqs > 0 && max_blocks_per_seq > 0
+                                        ? ((seqs - 1) * block_table_stride + max_blocks_per_seq) * 4
+                                        : 0};
+  const Range in[] = {{context_lens, seqs * 4}, {query_lens, seqs * 4},
+                      {free_blocks, free_capacity * 4LL}, {num_free, 4}, table};
+  const Range written[] = {{context_lens_out, seqs * 4}, {cu_seqlens_q, (seqs + 1) * 4},
+                           {slot_mapping, max_tokens * 8LL},
+                           {positions, positions ? max_tokens * 4LL : 0}, {num_free_out, 4}};
+  auto overlaps = [](const Range &x, const Range &y) {
+    const char *a = static_cast<const char *>(x.p), *b = static_cast<const char *>(y.p);
+    return x.bytes > 0 && y.bytes > 0 && a < b + y.bytes && b < a + x.bytes;
+  };
+  for (const Range &x : in) {
+    for (const Range &y : written)
+      if (overlaps(x, y)) return PA_ERR_SHAPE;
+    if (&x != in + 4 && overlaps(x, table)) return PA_ERR_SHAPE;
+  }
   pa::BuildTablesArgs a;
   a.block_table = block_table;
   a.block_table_stride = block_table_stride;
@@ -853,6 +869,8 @@ pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *que
   a.num_kv_heads = num_kv_heads;
   a.head_dim = head_dim;
   a.packed_heads = pa::flash_packed_heads(num_q_heads / num_kv_heads);
+  a.grid = pa::varlen_items(num_seqs, total_tokens, max_seqlen, num_q_heads, a.packed_heads);
+  if (a.grid > INT32_MAX) return PA_ERR_UNSUPPORTED;
   flash_scale(scale, &a.scale_log2, &a.negate);
   a.causal = causal ? 1 : 0;
   a.d_error = d_error;
@@ -876,8 +894,7 @@ pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *que
 namespace {
 
 // Sizes of a shared-prefix decode; `shared` false: it is a plain decode (no
-// group, no prefix, or a batch too long for the balanced split's 32-bit
-// positions).
+// group, no prefix, nothing to attend to).
 struct SharedPlan {
   bool shared = false;
   int sms = 0, runs = 0;
@@ -886,23 +903,33 @@ struct SharedPlan {
 pa_status shared_plan(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
                       int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
                       int32_t max_prefix_len, SharedPlan *out) {
-  if (num_groups < 0 || max_prefix_len < 0) return PA_ERR_SHAPE;
+  if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_context_len < 0 ||
+      num_groups < 0 || max_prefix_len < 0 || num_q_heads % num_kv_heads != 0)
+    return PA_ERR_SHAPE;
   int32_t P = 0;
   SharedPlan s;
+  s.shared = num_seqs > 0 && num_groups > 0 && max_prefix_len > 0 && max_context_len > 0;
+  // The schedules count in 32 bits.  (A plain decode would not do in their
+  // place: it reads each row's own entries for the prefix, and a row need not
+  // hold them.)
+  const int64_t most = 1LL << 30;
+  const int units = num_kv_heads * pa::decode_slices(num_q_heads / num_kv_heads).nc;
+  if (s.shared &&
+      (max_context_len >= most || max_prefix_len >= most ||
+       !use_balanced(num_seqs, units, max_context_len, 0) ||
+       pa::shared_cost(num_seqs, num_groups, num_q_heads, num_kv_heads, max_prefix_len) >= most))
+    return PA_ERR_UNSUPPORTED;
   const pa_status st = pa_decode_plan(num_seqs, num_q_heads, num_kv_heads, head_dim,
                                       max_context_len, 0, &P, &s.decode_bytes);
   if (st != PA_OK) return st;
   const cudaError_t e = current_num_sms(&s.sms);
   if (e != cudaSuccess) return cuda_fail(e);
-  s.shared = num_seqs > 0 && num_groups > 0 && max_prefix_len > 0 && max_context_len > 0 &&
-             P == 0 &&
-             pa::shared_cost(num_seqs, num_groups, num_q_heads, num_kv_heads, max_prefix_len) <
-                 (1LL << 30);
   s.bytes = s.decode_bytes;
   if (s.shared) {
     s.runs = pa::shared_runs(num_seqs, num_groups, num_q_heads, num_kv_heads, max_prefix_len,
                              s.sms);
-    const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads + 256 * static_cast<size_t>(s.runs);
+    const size_t rows =
+        static_cast<size_t>(num_seqs) * num_q_heads + 256 * static_cast<size_t>(s.runs);
     s.o_bytes = align256(rows * head_dim * sizeof(float));
     s.ml_bytes = align256(rows * 2 * sizeof(float));
     s.bytes += s.o_bytes + s.ml_bytes + align256((static_cast<size_t>(num_seqs) + 1) * 16);

@@ -204,6 +204,16 @@ inline int flash_packed_heads(int group) {
   return 1;
 }
 
+// The most items a batch of packed prompts has (one CTA per item): pairs of
+// query tiles x head units; at most one pair of a sequence is partly filled.
+inline int64_t varlen_items(int num_seqs, int total, int max_seqlen, int num_q_heads,
+                            int packed_heads) {
+  const int64_t rows = 2 * (128 / packed_heads);
+  const int64_t longest = max_seqlen < total ? max_seqlen : total;
+  const int64_t pairs = total / rows + num_seqs, most = num_seqs * ((longest + rows - 1) / rows);
+  return (pairs < most ? pairs : most) * (num_q_heads / packed_heads);
+}
+
 struct AttentionVarlenArgs {
   void *out;
   int64_t out_row_stride;
@@ -211,6 +221,7 @@ struct AttentionVarlenArgs {
   int32_t num_seqs, total, max_seqlen;
   int32_t num_q_heads, num_kv_heads, head_dim;
   int packed_heads;
+  int64_t grid;      // varlen_items
   float scale_log2;  // |scale| * log2(e), not 0
   bool negate;       // the scale is negative
   int32_t causal;
@@ -230,9 +241,8 @@ inline int64_t shared_cost(int num_seqs, int num_groups, int num_q_heads, int nu
   const int pg = flash_packed_heads(num_q_heads / num_kv_heads), tpt = 128 / pg;
   const int64_t tiles =
       (static_cast<int64_t>(num_seqs) / tpt + num_groups) * (num_q_heads / pg);
-  return tiles * ((max_prefix + 127) / 128);
+  return tiles * ((static_cast<int64_t>(max_prefix) + 127) / 128);
 }
-
 
 // The own parts start on the SMs that the prefix pass leaves free, so a pass of
 // a few tiles per SM, which is mostly start-up, takes half of the SMs (32

@@ -33,6 +33,8 @@ def call(lib, **kw):
     (dict(qs=8 * 128 + 4), 4), (dict(ks=2 * 128 + 4), 4), (dict(os=8 * 128 + 4), 4),
     (dict(out=0x100008), 4), (dict(q=0x200008), 4), (dict(k=0x300008), 4), (dict(v=0x310002), 4),
     (dict(cu=0x400002), 4), (dict(out=0), 1), (dict(q=0), 1), (dict(k=0), 1), (dict(v=0), 1),
+    # more pairs of query tiles x heads than a grid has blocks
+    (dict(s=1 << 30, t=1 << 30, mx=1), 3),
     (dict(cu=0), 1), (dict(s=0), 0), (dict(t=0), 0), (dict(mx=0), 0),
 ])
 def test_refusals(lib, kw, status):

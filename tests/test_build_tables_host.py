@@ -37,6 +37,10 @@ def call(lib, **kw):
     (dict(out=0x200000), 2),            # in place: other CTAs still read the lengths
     (dict(out=0x200008), 2),            # partial overlap
     (dict(out=0x210004), 2), (dict(nfo=0x230000), 2),
+    # any output over any input: cumulative lengths, slots, positions, table
+    (dict(cu=0x200000), 2), (dict(cu=0x21000c), 2), (dict(slots=0x220000), 2),
+    (dict(pos=0x100000 - 252), 2), (dict(cu=0x1000f8), 2), (dict(nfo=0x22018c), 2),
+    (dict(free=0x100000), 2), (dict(ctx=0x1000fc), 2), (dict(slots=0x1fff00), 2),
 ])
 def test_refusals(lib, kw, status):
     assert call(lib, **kw) == status

@@ -35,9 +35,20 @@ def call(lib, **kw):
     (dict(ctx=0), 1), (dict(gs=0), 1), (dict(pl=0), 1), (dict(gs=0x340002), 4),
     (dict(pl=0x350001), 4), (dict(q=0x200008), 4), (dict(v=0x310004), 4), (dict(qs=1000), 2),
     (dict(qs=8 * 128 + 4), 4), (dict(nb=1 << 28), 3), (dict(s=0), 0),
+    # beyond the schedules' 32 bits: refused (a plain decode would read other rows)
+    (dict(s=1 << 10, mc=1 << 19), 3), (dict(mc=2**31 - 1), 3), (dict(mp=2**31 - 1), 3),
+    (dict(s=1 << 14, g=1 << 14, mp=1 << 22), 3),
 ])
 def test_refusals(lib, kw, status):
     assert call(lib, **kw) == status
+
+
+def test_the_plan_refuses_what_the_call_refuses(lib):
+    for s, g, mc, mp in ((1 << 10, 2, 1 << 19, 50), (4, 2, 2**31 - 1, 50),
+                         (4, 2, 100, 2**31 - 1), (1 << 14, 1 << 14, 100, 1 << 22)):
+        assert lib.pa_decode_shared_plan(s, g, 8, 2, 128, mc, mp, None) == 3
+    assert lib.pa_decode_shared_plan(4, 2, 8, 3, 128, 100, 50, None) == 2
+    assert lib.pa_decode_shared_plan(4, -1, 8, 2, 128, 100, 50, None) == 2
 
 
 def test_python_argument_checks():

@@ -157,6 +157,21 @@ def test_padding_and_neighbours_may_hold_anything():
         verify(x, seqs=[0, 2])
 
 
+@pytest.mark.parametrize("at,row", [(8, 32), (0, 8), (16, 24)])
+def test_output_rows_on_16_bytes(at, row):
+    # output rows that start on 16 bytes but not on 32 (by the first row, by
+    # the row stride, by both)
+    require_gpu()
+    x = make([200, 1, 150], 8, 2, 64, F16, seed=9)
+    t, n = 351, 8 * 64
+    flat = torch.full((t * (n + row) + at,), CANARY, dtype=F16, device="cuda")
+    x["out"] = flat[at:].view(t, n + row)[:, :n].view(t, 8, 64)
+    run(x)
+    verify(x)
+    assert bool((flat[:at] == CANARY).all())
+    assert bool((flat[at:].view(t, n + row)[:, n:] == CANARY).all())
+
+
 def test_equals_the_paged_prefill_in_value():
     # the same prompts through the cache: both are within half of the paged
     # call's stated bound of the exact values, so within it of each other

@@ -278,6 +278,20 @@ def test_repeated_captured_and_on_two_streams():
     assert int(x["err"]) == 0 and int(y["err"]) == 0
 
 
+def test_own_workspace_on_another_stream():
+    # no workspace given: the call's own belongs to the stream it runs on, so
+    # what the current stream allocates and writes meanwhile is not it
+    require_gpu()
+    x = make([(700, [3, 40, 9, 100])], 8, 2, 128, 16, BF16, seed=15)
+    n = pa.pa_decode_shared_plan(4, 1, 8, 2, 128, x["max_ctx"], x["max_prefix"])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        run(x, stream=s)
+        torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")
+    verify(x)
+
+
 def test_behind_a_write_and_before_a_read():
     # the launches around the call in its stream: the step's cache write
     # before it, a copy of its output and a reuse of its inputs behind it
