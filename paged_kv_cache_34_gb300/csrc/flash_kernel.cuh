@@ -75,7 +75,7 @@ struct Layout {
   // Buffers of 32 KB (16 at head_dim 64), in what the 227 KB hold.  Packed
   // prompts run through many items: a third Q buffer lets the next one's first
   // query tile load early.  The prefix pass has few items and K and V from
-  // memory: they get the room (72 us against TODO with the packed split on 8
+  // memory: they get the room (67 us against 82 with the packed split on 8
   // sequences behind 16384 tokens, 32/32 heads).
   static constexpr int kUnit = D == 128 ? 1 : 2;
   // Q buffers of stream A and B; a single-tile launch's streams share theirs.
@@ -177,7 +177,8 @@ struct Params {
   uint32_t wait_ns;
 };
 
-// The waits' bound for a launch (at most the 2 s of the library).
+// The full bound, for what must have ended before a CTA leaves, and a launch's.
+constexpr uint32_t kFullWait = static_cast<uint32_t>(kWaitLimitNs);
 inline uint32_t wait_limit(uint64_t ns) {
   return static_cast<uint32_t>(ns < kWaitLimitNs ? ns : kWaitLimitNs);
 }
@@ -729,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!it.live) break;
       }
       // a request that was given up on still lands before the CTA leaves
-      if (asked > 0 && lane == 0) wait_for(bar(L::kNext), (asked - 1) & 1, static_cast<uint32_t>(kWaitLimitNs));
+      if (asked > 0 && lane == 0) wait_for(bar(L::kNext), (asked - 1) & 1, kFullWait);
       if (!ok && lane == 0) give_up();
       if constexpr (PAGED) {
         if (blockIdx.x == 0) write_info(p, lane, groups_ok, groups_cost);
@@ -852,15 +853,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Do not leave while copies this CTA issued may still land.
       if (lane == 0) {
         for (int n = nq0 - 1; n >= 0 && n >= nq0 - L::kQA; --n)
-          wait_for(bar(L::kQFull + L::q_slot(0, n)), L::q_use(0, n) & 1,
-                   static_cast<uint32_t>(kWaitLimitNs));
+          wait_for(bar(L::kQFull + L::q_slot(0, n)), L::q_use(0, n) & 1, kFullWait);
         for (int n = nq1 - 1; n >= 0 && n >= nq1 - L::kQB; --n)
-          wait_for(bar(L::kQFull + L::q_slot(1, n)), L::q_use(1, n) & 1,
-                   static_cast<uint32_t>(kWaitLimitNs));
+          wait_for(bar(L::kQFull + L::q_slot(1, n)), L::q_use(1, n) & 1, kFullWait);
         for (int n = nk - 1; n >= 0 && n >= nk - L::NK; --n)
-          wait_for(bar(L::kKFull + n % L::NK), (n / L::NK) & 1, static_cast<uint32_t>(kWaitLimitNs));
+          wait_for(bar(L::kKFull + n % L::NK), (n / L::NK) & 1, kFullWait);
         for (int n = nv - 1; n >= 0 && n >= nv - L::NV; --n)
-          wait_for(bar(L::kVFull + n % L::NV), (n / L::NV) & 1, static_cast<uint32_t>(kWaitLimitNs));
+          wait_for(bar(L::kVFull + n % L::NV), (n / L::NV) & 1, kFullWait);
       }
       __syncwarp();
     } else {
@@ -1055,7 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // full bound: TMEM is freed after it).
       if (elect_one()) umma_commit(bar(L::kFin + t));
       __syncwarp();
-      if (lane == 0) wait_for(bar(L::kFin + t), 0, static_cast<uint32_t>(kWaitLimitNs));
+      if (lane == 0) wait_for(bar(L::kFin + t), 0, kFullWait);
       __syncwarp();
     }
   } else if (warp >= kEpiWarp0) {
@@ -1141,7 +1140,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (PAGED) {
           const int64_t ws = static_cast<int64_t>(it.ws_row) + u * p.tpt * p.pg + r;
           wrow = p.ws_o + ws * D;
-          if (row_ok) *reinterpret_cast<float2 *>(p.ws_ml + ws * 2) = make_float2(mm, bad ? 0.f : ll);
+          if (row_ok)
+            *reinterpret_cast<float2 *>(p.ws_ml + ws * 2) = make_float2(mm, bad ? 0.f : ll);
         } else {
           orow = static_cast<typename E::T *>(p.out) +
                  static_cast<int64_t>(it.q0 + tok) * p.out_row_stride + (it.head0 + hl) * D;
@@ -1153,8 +1153,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // rows that saw no key are 0, whatever O holds
         const bool none = !(ll > 0.f) || bad;
         const bool any_none = __any_sync(0xffffffffu, none && row_ok);
-        // 32 bytes a lane and store: a store's 32 rows are 32 lines to the
-        // load/store unit either way
+        // 32 bytes a lane and store where rows allow it: a store's 32 rows are
+        // 32 lines to the load/store unit either way (24 prompts of 2691 tokens
+        // on average, 40/8: 497 us, with 16 bytes 515)
         const bool wide = PAGED || p.out_wide;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -1200,7 +1201,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
 #pragma unroll
               for (int i = 0; i < kWords; i += 4)
-                *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                *reinterpret_cast<uint4 *>(dst + i) =
+                    make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
             }
           }
         }
@@ -1369,8 +1371,8 @@ cudaError_t launch(const Params &p, const CUtensorMap &tmq, const CUtensorMap &t
   cudaError_t e = allow_dynamic_smem<kernel>();
   if (e == cudaSuccess) e = check_register_pool<kernel>();
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), Layout<D, MODE>::kBytes,
-                    stream, p, tmq, tmk, tmv);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
+                    Layout<D, MODE>::kBytes, stream, p, tmq, tmk, tmv);
 }
 
 }  // namespace flash

@@ -124,9 +124,9 @@ bool use_balanced(int num_seqs, int units, int max_ctx, int partition_size) {
 
 // Fixed split-KV plan.  Auto: every worker warp (kDecodeWarps per CTA,
 // kDecodeCtasPerSm CTAs per SM) should get about eight items of the largest
-// possible batch, so the static item schedule balances; a partition is at least 64 tokens (128 when eight
-// query heads share a KV head) so the partial states stay a few percent of the
-// K/V bytes.
+// possible batch, so the static item schedule balances; a partition is at least
+// 64 tokens (128 when eight query heads share a KV head) so the partial states
+// stay a few percent of the K/V bytes.
 int plan_partition(int num_seqs, int num_q_heads, int num_kv_heads, int max_ctx,
                    int partition_size, int num_sms) {
   if (partition_size > 0) return partition_size;
