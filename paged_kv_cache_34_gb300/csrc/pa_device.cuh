@@ -295,6 +295,11 @@ __device__ __forceinline__ void f2_unpack(uint64_t v, float &lo, float &hi) {
 __device__ __forceinline__ uint64_t f2_words(uint32_t lo, uint32_t hi) {
   return f2_pack(__uint_as_float(lo), __uint_as_float(hi));
 }
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
