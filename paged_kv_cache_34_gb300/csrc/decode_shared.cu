@@ -31,15 +31,19 @@ namespace {
 // kJoinBatch at a time with every load in flight, and the warps' results are
 // folded in shared memory.  Little code, it starts from a cold instruction
 // cache: one loop over both parts' states took 62 us where this takes 58 on
-// 64 sequences in 6 groups.
+// 64 sequences in 6 groups, and the block search for every group 30.0 where the
+// build without it takes @@ on 32 sequences over 4000 tokens.
 constexpr int kJoinWarps = 4;
 constexpr int kJoinBatch = 4;
-// Up to this many rows, four warps to a row: 32 sequences' own parts come in a
-// dozen pieces each (the whole call 30.7 us, with one warp 34.0).  Beyond it
-// the rows alone fill the GPU (16384 rows: 345 us with four, 322 with one).
-constexpr int kJoinWideRows = 2048;
+// Four warps to a row where the own parts' workers are this many to a unit (a
+// sequence and KV head), so that a row can have a batch of states for each warp
+// (4 sequences of 8000 own tokens, 8/2 heads: 19.4 us for the call, with one
+// warp 35.4); else one (8 sequences behind 16384 tokens, 32/32 heads: 64.2 us,
+// with four 65.2; 256 behind 32768, 64/8: 296 and 345).
+constexpr int kJoinWideStates = 16;
 
-template <class E, int D, int W>
+// BLOCKS: a group may have more than two query tiles.
+template <class E, int D, int W, bool BLOCKS>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     shared_join_kernel(const dec::DecodeParams p, const float *px_o, const float *px_ml,
                        const int32_t *info, int pg, int tpt) {
@@ -51,22 +55,38 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int L = checked_context_len(__ldg(p.context_lens + b), p.capacity, p.max_ctx, p.err, false);
   griddep_wait();  // both launches' states
   griddep_launch_dependents();
-  const int4 seq = *reinterpret_cast<const int4 *>(info + static_cast<int64_t>(b + 1) *
-                                                              flash::kInfoWords);
+  const int32_t *seq_info = info + static_cast<int64_t>(b + 1) * flash::kInfoWords;
+  const int4 seq = *reinterpret_cast<const int4 *>(seq_info);
   const unsigned run_c = static_cast<unsigned>(info[0]);
   const int total = p.ws_pref[p.num_seqs], pref = p.ws_pref[b];
   const int prefix = seq.x, first = seq.y, n = seq.z;
+  const int ws0 = BLOCKS ? seq_info[4] : first * p.hq;  // the group's first workspace row
 
   const int own = L > prefix ? L - dec::own_start(prefix, p.box_rows) : 0;
 
   float M = -INFINITY, l = 0.f, acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  // The prefix's states: those of a head unit's tiles in each block of its
+  // group's line, for up to two query tiles one block (part 1), else lane i
+  // looking at block blk0 + i (parts 2, 3, ...).
+  const int head = h / pg, pair = (b - first) / (2 * tpt);
+  const int nkt = (prefix + flash::kKeys - 1) / flash::kKeys;
+  int T = 0, line = 0, ks = 1, blk0 = 0, blocks = 0;
+  if (prefix > 0 && L > 0) {
+    T = (n - 1) / tpt + 1;
+    if (BLOCKS && T > 2) {
+      line = p.hq / pg * nkt;
+      ks = flash::block_tiles(T, run_c, line);
+      blk0 = head * nkt / ks;
+      blocks = (head * nkt + nkt - 1) / ks - blk0 + 1;
+    }
+  }
 #pragma unroll 1
-  for (int part = 0; part < 2; ++part) {
-    const float *o = nullptr, *ml = nullptr;  // the part's states, `step` rows apart
-    int64_t at = 0;
-    int count = 0, step = 0;
+  for (int part = 0; part < 2 || (BLOCKS && (part - 2) * 32 < blocks); ++part) {
+    const float *o = px_o, *ml = px_ml;  // the part's states, `step` rows apart
+    int count = 0, step = 256, ends = 0, at = 0;
+    int64_t at0 = 0;
     if (part == 0 && own > 0) {
       const int kvh = h / p.group, hg = h - kvh * p.group;
       const int sl = hg / p.hs, g = kvh * p.nc + sl;
@@ -74,31 +94,41 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
           static_cast<unsigned>(dec::balanced_chunk(total, p.num_workers, p.chunk_cap));
       const unsigned U = pref + g * dec::ceil16(own), c0 = U / C;
       count = static_cast<int>((U + own - 1) / C - c0) + 1;
-      at = (static_cast<int64_t>(b) * p.vh + g + c0) * p.hs + hg - sl * p.hs;
+      at0 = (static_cast<int64_t>(b) * p.vh + g + c0) * p.hs + hg - sl * p.hs;
       o = p.ws_o;
       ml = p.ws_ml;
       step = p.hs;
-    } else if (part == 1 && prefix > 0 && L > 0) {
-      const int nkt = (prefix + flash::kKeys - 1) / flash::kKeys;
-      const int tiles = (n - 1) / tpt + 1, head = h / pg, pair = (b - first) / (2 * tpt);
-      const int cost = 2 * pair + 1 < tiles ? 2 : 1;
-      const unsigned U = seq.w + (head * tiles + 2 * pair) * nkt, c0 = U / run_c;
-      count = static_cast<int>((U + cost * (nkt - 1)) / run_c - c0) + 1;
-      at = static_cast<int64_t>(first) * p.hq + static_cast<int64_t>(head) * n * pg +
-           (b - first) * pg + h - head * pg + static_cast<int64_t>(c0) * 256;
-      o = px_o;
-      ml = px_ml;
-      step = 256;
+    } else if (part == 1 && T > 0 && (!BLOCKS || T <= 2)) {
+      const unsigned U = seq.w + T * head * nkt, c0 = U / run_c;
+      count = static_cast<int>((U + T * (nkt - 1)) / run_c - c0) + 1;
+      at0 = ws0 + 256 * static_cast<int64_t>(c0) + head * n * pg + (b - first) * pg + h - head * pg;
+    } else if (BLOCKS && part > 1) {
+      const int i = (part - 2) * 32 + lane, blk = blk0 + i;
+      if (i < blocks) {
+        const int t0 = blk * ks, len = min(ks, line - t0);
+        const int lo = max(head * nkt - t0, 0), hi = min(head * nkt + nkt - t0, len);
+        const int w = 2 * pair + 1 < T ? 2 : 1, U = seq.w + t0 * T + pair * 2 * len;
+        const int c0 = (U + w * lo) / static_cast<int>(run_c);
+        count = (U + w * (hi - 1)) / static_cast<int>(run_c) - c0 + 1;
+        at = ws0 + flash::item_row(n, pg, tpt, nkt, blk, t0, len, pair, head) + 256 * c0 +
+             (b - first - pair * 2 * tpt) * pg + h - head * pg;
+      }
+      ends = flash::warp_scan(count, lane);
+      at -= 256 * (ends - count);  // state k of the part is at row at + 256 k of its lane
+      count = __shfl_sync(0xffffffffu, ends, 31);
     }
-    o += at * D + lane * V;
-    ml += at * 2;
+    o += lane * V;
 #pragma unroll 1
     for (int i0 = w; i0 < count; i0 += W * kJoinBatch) {
       float2 st[kJoinBatch];
       float ov[kJoinBatch][V];
 #pragma unroll
       for (int k = 0; k < kJoinBatch; ++k) {
-        const int64_t i = static_cast<int64_t>(step) * (i0 + k * W < count ? i0 + k * W : i0);
+        const int at_k = i0 + k * W < count ? i0 + k * W : i0;
+        int64_t i = at0 + static_cast<int64_t>(step) * at_k;
+        if (BLOCKS && part > 1)
+          i += __shfl_sync(0xffffffffu, at,
+                           __ffs(__ballot_sync(0xffffffffu, ends > at_k)) - 1);
         st[k] = *reinterpret_cast<const float2 *>(ml + i * 2);
         if constexpr (V == 4) {
           const float4 x = *reinterpret_cast<const float4 *>(o + i * D);
@@ -185,13 +215,17 @@ cudaError_t launch_all(const DecodeSharedArgs &a, const flash::Params &f,
                : dec::launch_kernel<E, D, true, 0, 1, false, true>(a.decode, p, stream);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.hq;
-  const bool wide = rows <= kJoinWideRows;
+  const bool wide =
+      p.num_workers >= kJoinWideStates * static_cast<int64_t>(p.num_seqs) * p.vh;
   const int64_t blocks = wide ? rows : (rows + kJoinWarps - 1) / kJoinWarps;
-  return launch_pdl(wide ? shared_join_kernel<E, D, kJoinWarps> : shared_join_kernel<E, D, 1>,
-                    dim3(static_cast<unsigned>(blocks)), dim3(kJoinWarps * 32), 0, stream, p,
-                    static_cast<const float *>(a.ws_o), static_cast<const float *>(a.ws_ml),
-                    static_cast<const int32_t *>(a.ws_info), a.packed_heads,
-                    128 / a.packed_heads);
+  auto join = f.blocks ? (wide ? shared_join_kernel<E, D, kJoinWarps, true>
+                               : shared_join_kernel<E, D, 1, true>)
+                       : (wide ? shared_join_kernel<E, D, kJoinWarps, false>
+                               : shared_join_kernel<E, D, 1, false>);
+  return launch_pdl(join, dim3(static_cast<unsigned>(blocks)), dim3(kJoinWarps * 32), 0,
+                    stream, p, static_cast<const float *>(a.ws_o),
+                    static_cast<const float *>(a.ws_ml), static_cast<const int32_t *>(a.ws_info),
+                    a.packed_heads, 128 / a.packed_heads);
 }
 
 }  // namespace
@@ -220,6 +254,7 @@ cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream)
   f.group_starts = a.group_starts;
   f.prefix_lens = a.prefix_lens;
   f.num_groups = a.num_groups;
+  f.blocks = d.num_seqs > 2 * f.tpt;
   f.max_prefix = a.max_prefix;
   f.block_size = d.block_size;
   f.num_blocks = d.num_blocks;

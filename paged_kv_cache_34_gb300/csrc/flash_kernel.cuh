@@ -171,6 +171,7 @@ struct Params {
   int32_t capacity, max_ctx;
   const int32_t *group_starts, *prefix_lens;
   int32_t num_groups, max_prefix;
+  bool blocks;              // a group may have more than two query tiles
   int32_t block_size;
   int64_t num_blocks;
   float *ws_o, *ws_ml;
@@ -359,17 +360,47 @@ __device__ inline bool check_cu(const Params &p, int lane) {
   return !__any_sync(0xffffffffu, bad);
 }
 
-// Prefix pass.  The unit is a (group, head unit, pair of query tiles) with
-// nkt K/V tiles; a tile of a pair costs 2, of a single query tile 1, so a
-// group's cost is head units x query tiles x nkt.  The units are laid end to
-// end and cut into runs of C cost, one per CTA; tile i of a unit that starts
-// at U (cost w per tile) belongs to run (U + w i) / C.  C >= 2 leaves no run
-// inside a unit without a tile, so a unit's states are those of runs
-// U / C .. (U + w (nkt - 1)) / C.  Warp-collective.
-// All costs fit 31 bits (the host sends larger batches elsewhere).
+// Prefix pass.  A group of n rows with T query tiles per head unit and nkt K/V
+// tiles has a line of (head units x nkt) K/V tiles, each needed by its pairs of
+// query tiles; a tile costs a pair 2, a single query tile 1.  The line is cut
+// into blocks; within a block the pairs follow one another, each with the
+// block's tiles ("row").  All rows are laid end to end and cut into runs of C
+// cost, one per CTA; tile i of a row that starts at U (cost w per tile) belongs
+// to run (U + w i) / C.  C >= 2 leaves no run inside a row without a tile, so
+// the runs of its tiles i .. k are (U + w i) / C .. (U + w k) / C.
+//
+// A block is as long as a run of a pair: the CTAs that work beside each other
+// are then a block's pairs over the same K and V, which come from memory once
+// (256 sequences over 32768 tokens, 64/8 heads, 8 pairs: 142 MB read where whole
+// lines one after the other read 850, the pass 170 us against 198).  Two query
+// tiles or less are one pair, whose line is one block.  A run holds no two rows of
+// one pair: three tiles' other row is a run long with blocks of C.
+//
+// A work item is a row's tiles of one head unit in one run; its states start at
+// a workspace row that grows along the line by at least its rows (item_row) plus
+// 256 per run, so no two items share one.  Warp-collective.
 struct GroupGeom {
   int first, n, nkt, prefix, cost;
 };
+// K/V tiles per block of a line for T query tiles and runs of C.
+__device__ __forceinline__ int block_tiles(int T, int C, int line) {
+  return T <= 2 ? line : min(line, T == 3 ? C : (C + 1) >> 1);
+}
+// Workspace rows of a group (its runs' 256 aside): rows of a head unit x
+// (blocks + head units), as item_row counts.
+__device__ __forceinline__ int group_rows(const Params &p, const GroupGeom &g, int C) {
+  if (g.cost == 0) return 0;
+  const int line = p.hu * g.nkt, ks = block_tiles(tiles_of(p, g.n), C, line);
+  return g.n * p.pg * ((line + ks - 1) / ks + p.hu);
+}
+// ... and of the item of block `blk` (first tile at, len tiles), pair q and head
+// unit h, from the group's first on.
+__device__ __forceinline__ int item_row(int n, int pg, int tpt, int nkt, int blk, int at, int len,
+                                        int q, int h) {
+  const int h0 = at / nkt, heads = (at + len - 1) / nkt - h0 + 1;
+  return n * pg * (blk + h0) + q * 2 * tpt * pg * heads +
+         (h - h0) * min(2 * tpt, n - q * 2 * tpt) * pg;
+}
 __device__ __forceinline__ GroupGeom group_geom(const Params &p, int g) {
   GroupGeom r;
   r.first = r.n = r.nkt = r.prefix = 0;
@@ -427,54 +458,73 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {
   return v;
 }
 
-// What the joining kernel needs, in words of 4: first the run cost C, then for
-// each sequence its prefix length (0: none), the group's first sequence, its
-// size and its first cost position.  Warp-collective.
-constexpr int kInfoWords = 4;
+// What the joining kernel needs, in kInfoWords words: first the run cost C, then
+// for each sequence its prefix length (0: none), the group's first sequence, its
+// size, its first cost position and workspace row.  Warp-collective.
+constexpr int kInfoWords = 8;
 __device__ inline void write_info(const Params &p, int lane, bool good, int total) {
-  if (lane == 0) p.ws_info[0] = run_cost(total, gridDim.x);
+  const int C = run_cost(total, gridDim.x);
+  if (lane == 0) p.ws_info[0] = C;
   if (!good) {
     for (int b = lane; b < p.num_seqs; b += 32)
       p.ws_info[static_cast<int64_t>(b + 1) * kInfoWords] = 0;
     return;
   }
-  int gbase = 0;
+  int gbase = 0, rbase = 0;
   for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
     const GroupGeom r = group_geom(p, g0 + lane);
     const int incl = warp_scan(r.cost, lane);
     const int lo = gbase + incl - r.cost;
     gbase += __shfl_sync(0xffffffffu, incl, 31);
+    int row = r.first * p.hq;
+    if (p.blocks) {
+      const int rows = group_rows(p, r, C), rincl = warp_scan(rows, lane);
+      row = rbase + rincl - rows;
+      rbase += __shfl_sync(0xffffffffu, rincl, 31);
+    }
     for (int i = 0; i < 32 && g0 + i < p.num_groups; ++i) {
       const int first = __shfl_sync(0xffffffffu, r.first, i);
       const int n = __shfl_sync(0xffffffffu, r.n, i);
       const int pre = __shfl_sync(0xffffffffu, r.prefix, i);
       const int at = __shfl_sync(0xffffffffu, lo, i);
-      for (int b = lane; b < n; b += 32)
-        *reinterpret_cast<int4 *>(p.ws_info + static_cast<int64_t>(first + b + 1) * kInfoWords) =
-            make_int4(pre, first, n, at);
+      const int ws = __shfl_sync(0xffffffffu, row, i);
+      for (int b = lane; b < n; b += 32) {
+        int32_t *w = p.ws_info + static_cast<int64_t>(first + b + 1) * kInfoWords;
+        *reinterpret_cast<int4 *>(w) = make_int4(pre, first, n, at);
+        w[4] = ws;
+      }
     }
   }
 }
 
+template <bool BLOCKS>  // false: no group has more than one query tile
 struct PrefixSched {
-  int x, xend, gbase, g0;
+  int x, xend, gbase, rbase, g0, C;
 
   __device__ void init(const Params &p, int total) {
-    const int C = run_cost(total, gridDim.x);
+    C = run_cost(total, gridDim.x);
     const int64_t at = static_cast<int64_t>(blockIdx.x) * C;
     x = at < total ? static_cast<int>(at) : total;
     xend = total - x > C ? x + C : total;
     gbase = 0;
+    rbase = 0;
     g0 = 0;
   }
-  // The next piece: tiles [i0, i1) of a unit.
+  // The next piece: tiles [i0, i1) of a head unit for a pair, and the workspace
+  // row of its states.
   __device__ bool next(const Params &p, int lane, GroupGeom *geom, int *head, int *pair, int *i0,
-                       int *i1) {
+                       int *i1, int *ws_row) {
     while (x < xend) {
       for (; g0 < p.num_groups; g0 += 32) {
         const GroupGeom r = group_geom(p, g0 + lane);
         const int incl = warp_scan(r.cost, lane);
         const int hi = gbase + incl, lo = hi - r.cost;
+        int rincl = 0, row = r.first * p.hq;  // workspace rows, the group's first
+        if (BLOCKS && p.blocks) {
+          const int rows = group_rows(p, r, C);
+          rincl = warp_scan(rows, lane);
+          row = rbase + rincl - rows;
+        }
         const unsigned hit = __ballot_sync(0xffffffffu, x >= lo && x < hi);
         if (hit) {
           const int src = __ffs(hit) - 1;
@@ -484,24 +534,38 @@ struct PrefixSched {
           s.nkt = __shfl_sync(0xffffffffu, r.nkt, src);
           s.prefix = __shfl_sync(0xffffffffu, r.prefix, src);
           const int start = __shfl_sync(0xffffffffu, lo, src);
-          const int tiles = tiles_of(p, s.n);
-          const unsigned per_head = static_cast<unsigned>(tiles) * s.nkt;
-          const unsigned rem = x - start, h = rem / per_head, in_head = rem - h * per_head;
-          const unsigned q = in_head / (2u * s.nkt);
-          const int w = 2 * static_cast<int>(q) + 1 < tiles ? 2 : 1;
-          const int U = start + static_cast<int>(h * per_head + q * 2u * s.nkt);
+          const int row0 = __shfl_sync(0xffffffffu, row, src);
+          const int T = tiles_of(p, s.n), line = p.hu * s.nkt;
+          int t0 = 0, blk = 0, len = line, q = 0, U = start;
+          if (BLOCKS && T > 2) {
+            const int ks = block_tiles(T, C, line);
+            blk = (x - start) / (ks * T);
+            t0 = blk * ks;
+            len = min(ks, line - t0);
+            q = (x - start - t0 * T) / (2 * len);
+            U = start + t0 * T + q * 2 * len;
+          }
+          const int w = 2 * q + 1 < T ? 2 : 1;
           const int a = (x - U + w - 1) >> (w - 1);
-          const int b = min(s.nkt, (xend - U + w - 1) >> (w - 1));
-          x = min(xend, U + w * s.nkt);
-          if (a >= b) break;  // the rest of the unit's last tile lies in the run before
+          const int b = min(len, (xend - U + w - 1) >> (w - 1));
+          if (a >= b) {  // the rest of the row's last tile lies in the run before
+            x = min(xend, U + w * len);
+            break;
+          }
+          const int at = t0 + a, h = at / s.nkt;
           *geom = s;
-          *head = static_cast<int>(h);
-          *pair = static_cast<int>(q);
-          *i0 = a;
-          *i1 = b;
+          *head = h;
+          *pair = q;
+          *i0 = at - h * s.nkt;
+          *i1 = min(s.nkt, *i0 + b - a);
+          x = min(xend, U + w * (a + *i1 - *i0));
+          *ws_row = row0 + 256 * static_cast<int>(blockIdx.x) +
+                    (BLOCKS && T > 2 ? item_row(s.n, p.pg, p.tpt, s.nkt, blk, t0, len, q, h)
+                                     : h * s.n * p.pg);
           return true;
         }
         gbase = __shfl_sync(0xffffffffu, hi, 31);
+        if (BLOCKS && p.blocks) rbase += __shfl_sync(0xffffffffu, rincl, 31);
       }
       if (g0 >= p.num_groups) return false;
     }
@@ -599,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   // The prefix pass's scheduler reads the batch while the others set up.
-  PrefixSched xs;
+  PrefixSched<MODE == kPaged> xs;
   bool groups_ok = true;
   int groups_cost = 0;
   if constexpr (PAGED) {
@@ -637,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (PAGED) {
           GroupGeom g;
           int head, pair, i0, i1;
-          if (xs.next(p, lane, &g, &head, &pair, &i0, &i1)) {
+          if (xs.next(p, lane, &g, &head, &pair, &i0, &i1, &it.ws_row)) {
             it.live = 1;
             it.q0 = g.first;
             it.ntok = g.n;
@@ -647,8 +711,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             it.key0 = i0 * kKeys;
             it.kend = min(g.prefix, i1 * kKeys);
             it.kv0 = g.first;
-            it.ws_row = g.first * p.hq + head * g.n * p.pg + pair * 2 * p.tpt * p.pg +
-                        static_cast<int>(blockIdx.x) * 256;
             const bool single = 2 * pair + 1 >= tiles_of(p, g.n);
             it.cnt[0] = it.cnt[1] = it.nkv;
             if (single) it.flags |= kSingle;

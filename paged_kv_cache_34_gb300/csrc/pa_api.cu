@@ -926,13 +926,15 @@ pa_status shared_plan(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
   if (e != cudaSuccess) return cuda_fail(e);
   s.bytes = s.decode_bytes;
   if (s.shared) {
+    const int pg = pa::flash_packed_heads(num_q_heads / num_kv_heads);
     s.runs = pa::shared_runs(num_seqs, num_groups, num_q_heads, num_kv_heads, max_prefix_len,
                              s.sms);
-    const size_t rows =
-        static_cast<size_t>(num_seqs) * num_q_heads + 256 * static_cast<size_t>(s.runs);
+    const size_t rows = static_cast<size_t>(num_seqs) * (num_q_heads + pg) +
+                        512 * static_cast<size_t>(s.runs);
+    if (rows > INT32_MAX) return PA_ERR_UNSUPPORTED;
     s.o_bytes = align256(rows * head_dim * sizeof(float));
     s.ml_bytes = align256(rows * 2 * sizeof(float));
-    s.bytes += s.o_bytes + s.ml_bytes + align256((static_cast<size_t>(num_seqs) + 1) * 16);
+    s.bytes += s.o_bytes + s.ml_bytes + align256((static_cast<size_t>(num_seqs) + 1) * 32);
   }
   *out = s;
   return PA_OK;

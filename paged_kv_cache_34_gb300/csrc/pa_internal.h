@@ -268,8 +268,12 @@ struct DecodeSharedArgs {
   bool negate;         // the scale is negative
   CUtensorMap tm_q;    // box 64 x packed_heads x 128 / packed_heads
   CUtensorMap tm_k, tm_v;  // box 64 x 1 x block_size
-  float *ws_o, *ws_ml;     // [num_seqs * num_q_heads + 256 * runs, D] and [.., 2]
-  int32_t *ws_info;        // 4 words, then 4 per sequence
+  // [rows, D] and [rows, 2] states.  A group of n sequences takes n x packed_heads
+  // rows per (head unit + block of its line): num_seqs x num_q_heads for the
+  // head units, num_seqs x packed_heads + 256 x runs for the blocks (a block is
+  // half a run long or more, or a group's last); 256 x runs keep runs apart.
+  float *ws_o, *ws_ml;
+  int32_t *ws_info;        // 8 words, then 8 per sequence
 };
 cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream);
 

@@ -138,6 +138,27 @@ def test_group_sizes(n, hq, hkv, p):
     verify(x, seqs=set(rng.sample(range(n), min(n, 40))) | {0, n - 1})
 
 
+@pytest.mark.parametrize("hq,hkv,groups", [
+    # (prefix, sequences): groups of 1 to 5 query tiles and more side by side, lines
+    # of many short head units and of few long ones, rows cut across head units
+    (32, 4, [(900, 50), (130, 3), (600, 70), (1, 40), (2000, 17)]),
+    (32, 4, [(128, 130), (0, 5), (4000, 33), (129, 49)]),
+    (5, 5, [(700, 400), (300, 260), (50, 129)]),
+    (16, 1, [(3000, 24), (250, 25), (640, 9)]),
+    (2, 2, [(6000, 513)]),
+    (1, 1, [(19500, 400)]),
+])
+def test_groups_of_many_query_tiles(hq, hkv, groups):
+    require_gpu()
+    rng = random.Random(hq * len(groups))
+    x = make([(p, [rng.randint(0, 20) for _ in range(n)]) for p, n in groups], hq, hkv, 64, 16,
+             BF16, seed=hq)
+    run(x)
+    s = x["starts_list"]
+    verify(x, seqs=set(rng.sample(range(s[-1]), min(s[-1], 60))) | set(s[:-1])
+           | {e - 1 for e in s[1:]})
+
+
 @pytest.mark.parametrize("bs", [8, 32])
 def test_sequences_shorter_than_their_prefix(bs):
     # as in a padded batch: rows of length 0, 1 and less than the prefix
