@@ -246,15 +246,24 @@ inline int64_t shared_cost(int num_seqs, int num_groups, int num_q_heads, int nu
 
 // The own parts start on the SMs that the prefix pass leaves free, so a pass of
 // a few tiles per SM, which is mostly start-up, takes half of the SMs (32
-// sequences over 4000 tokens: 27.6 us against 30.5 with all of them).  A
-// longer pass takes them all: beside it the own parts would only take its
-// bandwidth (64 sequences in 6 groups: 57.5 us with all, 69 with half; 256
-// sequences over 32768 tokens: 322 with all, 328 / 360 with 16 / 32 fewer).
+// sequences over 4000 tokens: 27.5 us against 29.8 with all of them).  Of longer
+// passes, one of single query tiles waits for memory, which fewer SMs keep as
+// busy: it takes the largest power of two, 128 of 152, whose runs also end
+// where heads do when tiles and heads are powers of two (8 sequences over 16384
+// tokens, 32/32 heads: 58.0 us, with 152 / 136 / 116 SMs 64.9 / 63.4 / 63.4;
+// 16 over 32768, 32/8: 52.6, with 152 54.4).  One of tile pairs waits for the
+// tensor cores and takes them all (256 sequences over 32768 tokens: 296 us,
+// with 16 fewer 306, with half 386).
 inline int shared_runs(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
                        int max_prefix, int num_sms) {
   const int64_t cost =
       shared_cost(num_seqs, num_groups, num_q_heads, num_kv_heads, max_prefix);
-  const int64_t runs = (cost + 1) / 2, most = cost <= 6LL * num_sms ? num_sms / 2 : num_sms;
+  int64_t most = num_sms;
+  if (cost <= 6LL * num_sms)
+    most = num_sms / 2;
+  else if (num_seqs <= 128 / flash_packed_heads(num_q_heads / num_kv_heads))
+    for (most = 1; 2 * most <= num_sms;) most *= 2;
+  const int64_t runs = (cost + 1) / 2;
   return static_cast<int>(runs < 1 ? 1 : (runs < most ? runs : most));
 }
 
