@@ -597,7 +597,12 @@ __device__ __forceinline__ int use_count(const Item &it, int t) {
 __device__ __forceinline__ int use_step(const Item &it) { return (it.flags & kTurns) ? 2 : 1; }
 
 // -------------------------------------------------------------- the kernel --
-template <class E, int D, int MODE>
+// COMPACT: P is formed by a loop over 32 columns at a time, their S read once
+// more from TMEM, instead of 128 columns unrolled: a third of the softmax's
+// instructions, but each of its steps fills and drains the pipelines.  While
+// both streams' softmaxes run at once, as at the start of an item, they wait
+// for instructions, in the steady state for each other: see the launchers.
+template <class E, int D, int MODE, bool COMPACT>
 __global__ void __launch_bounds__(kThreads, 1)
     flash_kernel(const Params p, const __grid_constant__ CUtensorMap tmq,
                  const __grid_constant__ CUtensorMap tmk,
@@ -1362,19 +1367,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mu = m_new == -INFINITY ? 0.f : m_new;
         const uint64_t sl2 = f2_pack(sl, sl), nmu2 = f2_pack(-mu, -mu);
         uint64_t rs[2] = {0, 0};  // the row's sum, in four parts
-        uint32_t pw[64];
+        auto form = [&](const uint32_t *y, int pairs, uint32_t dst) {  // column pairs of S to P
+          uint32_t pw[8];
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {  // column pair
-          float x0, x1;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), sl2,
-                           nmu2),
-                    x0, x1);
-          x0 = fast_exp2(x0);  // 2^-inf = 0 where masked
-          x1 = fast_exp2(x1);
-          pw[c] = E::pack2(x0, x1);
-          rs[c & 1] = f2_add(rs[c & 1], f2_pack(x0, x1));
-          if ((c & 7) == 7)
-            tmem_st8(s_tm + c - 7, *reinterpret_cast<uint32_t(*)[8]>(pw + c - 7));
+          for (int c = 0; c < pairs; ++c) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_words(y[2 * c], y[2 * c + 1]), sl2, nmu2), x0, x1);
+            x0 = fast_exp2(x0);  // 2^-inf = 0 where masked
+            x1 = fast_exp2(x1);
+            pw[c & 7] = E::pack2(x0, x1);
+            rs[c & 1] = f2_add(rs[c & 1], f2_pack(x0, x1));
+            if ((c & 7) == 7) tmem_st8(dst + c - 7, pw);
+          }
+        };
+        if constexpr (COMPACT) {
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += 32) {
+            uint32_t y[32];
+            tmem_ld32(s_tm + c, y);
+            tmem_wait_ld();
+            form(y, 16, s_tm + c / 2);
+          }
+        } else {
+          form(v, 64, s_tm);
         }
         tmem_wait_st();
         if (i > 0 && __any_sync(0xffffffffu, raise)) {
@@ -1432,10 +1447,10 @@ cudaError_t check_register_pool() {
   return status;
 }
 
-template <class E, int D, int MODE>
+template <class E, int D, int MODE, bool COMPACT>
 cudaError_t launch(const Params &p, const CUtensorMap &tmq, const CUtensorMap &tmk,
                    const CUtensorMap &tmv, int grid, cudaStream_t stream) {
-  constexpr auto kernel = flash_kernel<E, D, MODE>;
+  constexpr auto kernel = flash_kernel<E, D, MODE, COMPACT>;
   cudaError_t e = allow_dynamic_smem<kernel>();
   if (e == cudaSuccess) e = check_register_pool<kernel>();
   if (e != cudaSuccess) return e;

@@ -1004,6 +1004,8 @@ pa_status pa_decode_shared(void *out, int64_t out_row_stride, const void *query,
   a.num_groups = num_groups;
   a.max_prefix = max_prefix_len;
   a.runs = s.runs;
+  a.prefix_cost =
+      pa::shared_cost(num_seqs, num_groups, num_q_heads, num_kv_heads, max_prefix_len);
   a.packed_heads = pa::flash_packed_heads(num_q_heads / num_kv_heads);
   flash_scale(scale, &a.scale_log2, &a.negate);
   char *w = static_cast<char *>(workspace) + s.decode_bytes;

@@ -250,8 +250,8 @@ inline int64_t shared_cost(int num_seqs, int num_groups, int num_q_heads, int nu
 // passes, one of single query tiles waits for memory, which fewer SMs keep as
 // busy: it takes the largest power of two, 128 of 152, whose runs also end
 // where heads do when tiles and heads are powers of two (8 sequences over 16384
-// tokens, 32/32 heads: 58.0 us, with 152 / 136 / 116 SMs 64.9 / 63.4 / 63.4;
-// 16 over 32768, 32/8: 52.6, with 152 54.4).  One of tile pairs waits for the
+// tokens, 32/32 heads: 57.6 us, with 152 / 136 / 116 SMs 64.9 / 63.4 / 63.4;
+// 16 over 32768, 32/8: 53.1, with 152 54.4).  One of tile pairs waits for the
 // tensor cores and takes them all (256 sequences over 32768 tokens: 296 us,
 // with 16 fewer 306, with half 386).
 inline int shared_runs(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
@@ -272,6 +272,7 @@ struct DecodeSharedArgs {
   const int32_t *group_starts, *prefix_lens;
   int32_t num_groups, max_prefix;
   int runs;            // CTAs of the prefix pass
+  int64_t prefix_cost; // the most it can cost (shared_cost)
   int packed_heads;
   float scale_log2;    // |scale| * log2(e), not 0
   bool negate;         // the scale is negative
