@@ -151,9 +151,10 @@ def _stream(stream):
 def _rows(t, name):
     """(row stride in elements) of a [rows, heads, head_dim] view with
     contiguous heads."""
-    if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+    st = t.stride()
+    if len(st) != 3 or st[2] != 1 or st[1] != t.shape[2]:
         raise ValueError(f"{name} must be [rows, heads, head_dim] with contiguous heads")
-    return t.stride(0)
+    return st[0]
 
 
 def pa_reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, *,
@@ -292,7 +293,7 @@ def pa_build_tables(block_table, context_lens, query_lens, free_blocks, num_free
     and 0), the block_table (int32 [S, max_blocks]) entries of the blocks
     taken off the end of free_blocks[:num_free], and num_free_out int32 [1].
     No output may overlap an input."""
-    lib = lib or library()
+    lib = lib or _lib or library()
     s, t, nfree = context_lens.shape[0], slot_mapping.shape[0], free_blocks.shape[0]
     i32, dev = torch.int32, context_lens.get_device()
     if block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != s:
@@ -301,19 +302,38 @@ def pa_build_tables(block_table, context_lens, query_lens, free_blocks, num_free
     width = block_table.shape[1]
     if width > 1 and inner != 1:
         raise ValueError("block_table must have contiguous rows")
-    vectors = [(context_lens, s, i32, "context_lens"), (query_lens, s, i32, "query_lens"),
-               (free_blocks, nfree, i32, "free_blocks"), (num_free, 1, i32, "num_free"),
-               (context_lens_out, s, i32, "context_lens_out"),
-               (cu_seqlens_q, s + 1, i32, "cu_seqlens_q"),
-               (slot_mapping, t, torch.int64, "slot_mapping"),
-               (num_free_out, 1, i32, "num_free_out")]
-    if positions is not None:
-        vectors.append((positions, t, i32, "positions"))
-    for v in vectors:
-        x = v[0]
-        if x.dtype is not v[2] or x.numel() != v[1] or x.get_device() != dev \
-                or not x.is_contiguous():
-            _bad_vector(*v, dev)
+    # one expression for what a right call passes (a loop over the tensors takes
+    # 1.4 us longer, and the host's time is this call's); which is wrong, below
+    pos_ok = positions is None or (positions.dtype is i32 and positions.numel() == t
+                                   and positions.get_device() == dev
+                                   and positions.is_contiguous())
+    if not (pos_ok and context_lens.dtype is i32 and query_lens.dtype is i32
+            and free_blocks.dtype is i32 and num_free.dtype is i32
+            and context_lens_out.dtype is i32 and cu_seqlens_q.dtype is i32
+            and num_free_out.dtype is i32 and slot_mapping.dtype is torch.int64
+            and context_lens.numel() == s and query_lens.numel() == s
+            and free_blocks.numel() == nfree and num_free.numel() == 1
+            and context_lens_out.numel() == s and cu_seqlens_q.numel() == s + 1
+            and num_free_out.numel() == 1 and slot_mapping.numel() == t
+            and query_lens.get_device() == dev and free_blocks.get_device() == dev
+            and num_free.get_device() == dev and context_lens_out.get_device() == dev
+            and cu_seqlens_q.get_device() == dev and num_free_out.get_device() == dev
+            and slot_mapping.get_device() == dev and context_lens.is_contiguous()
+            and query_lens.is_contiguous() and free_blocks.is_contiguous()
+            and context_lens_out.is_contiguous() and cu_seqlens_q.is_contiguous()
+            and slot_mapping.is_contiguous()):
+        vectors = [(context_lens, s, i32, "context_lens"), (query_lens, s, i32, "query_lens"),
+                   (free_blocks, nfree, i32, "free_blocks"), (num_free, 1, i32, "num_free"),
+                   (context_lens_out, s, i32, "context_lens_out"),
+                   (cu_seqlens_q, s + 1, i32, "cu_seqlens_q"),
+                   (slot_mapping, t, torch.int64, "slot_mapping"),
+                   (num_free_out, 1, i32, "num_free_out")]
+        if positions is not None:
+            vectors.append((positions, t, i32, "positions"))
+        for v in vectors:
+            if v[0].dtype is not v[2] or v[0].numel() != v[1] or v[0].get_device() != dev \
+                    or not v[0].is_contiguous():
+                _bad_vector(*v, dev)
     if block_table.get_device() != dev:
         _bad_device("block_table", dev)
     if d_error is not None:
@@ -533,7 +553,7 @@ def pa_attention_varlen(out, query, key, value, cu_seqlens, *, scale, max_seqlen
     out/query [T, Hq, D], key/value [T, Hkv, D] (equal row strides, e.g. views
     into one QKV buffer), cu_seqlens int32 [S+1].  ``max_seqlen`` is the host
     upper bound of the lengths; rows past cu_seqlens[S] are left alone."""
-    lib = lib or library()
+    lib = lib or _lib or library()
     t, hq, d = query.shape
     shape, dtype, n, dev = key.shape, query.dtype, cu_seqlens.numel(), query.get_device()
     if out.shape != query.shape or shape != value.shape or shape[0] != t or shape[2] != d:
@@ -546,9 +566,9 @@ def pa_attention_varlen(out, query, key, value, cu_seqlens, *, scale, max_seqlen
         raise ValueError("key and value must share a row stride")
     if cu_seqlens.dtype is not torch.int32 or n < 1 or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be a contiguous int32 tensor of num_seqs + 1 values")
-    for x in (out, key, value, cu_seqlens):
-        if x.get_device() != dev:
-            _bad_device("out, key, value or cu_seqlens", dev)
+    if not (out.get_device() == dev and key.get_device() == dev and value.get_device() == dev
+            and cu_seqlens.get_device() == dev):
+        _bad_device("out, key, value or cu_seqlens", dev)
     if d_error is not None:
         _check_error(d_error, dev)
     _current(dev)
@@ -583,7 +603,7 @@ def pa_decode_shared(out, query, key_cache, value_cache, block_table, context_le
     block_table row and are read once for the group.  ``max_context_len`` and
     ``max_prefix_len`` are host upper bounds.  A workspace is allocated with
     torch when none is given."""
-    lib = lib or library()
+    lib = lib or _lib or library()
     s, hq, d = query.shape
     nb, bs, hkv, dk = key_cache.shape
     g, dtype, i32, dev = prefix_lens.shape[0], query.dtype, torch.int32, query.get_device()
@@ -600,16 +620,22 @@ def pa_decode_shared(out, query, key_cache, value_cache, block_table, context_le
     width = block_table.shape[1]
     if width > 1 and inner != 1:
         raise ValueError("block_table must have contiguous rows")
-    for v in ((context_lens, s, i32, "context_lens"), (group_starts, g + 1, i32, "group_starts"),
-              (prefix_lens, g, i32, "prefix_lens")):
-        x = v[0]
-        if x.dtype is not i32 or x.numel() != v[1] or x.get_device() != dev \
-                or not x.is_contiguous():
-            _bad_vector(*v, dev)
+    if not (context_lens.dtype is i32 and group_starts.dtype is i32 and prefix_lens.dtype is i32
+            and context_lens.numel() == s and group_starts.numel() == g + 1
+            and prefix_lens.numel() == g and context_lens.get_device() == dev
+            and group_starts.get_device() == dev and prefix_lens.get_device() == dev
+            and context_lens.is_contiguous() and group_starts.is_contiguous()
+            and prefix_lens.is_contiguous()):
+        for v in ((context_lens, s, i32, "context_lens"),
+                  (group_starts, g + 1, i32, "group_starts"), (prefix_lens, g, i32, "prefix_lens")):
+            if v[0].dtype is not i32 or v[0].numel() != v[1] or v[0].get_device() != dev \
+                    or not v[0].is_contiguous():
+                _bad_vector(*v, dev)
     os, qs = _rows(out, "out"), _rows(query, "query")
-    for x in (out, key_cache, value_cache, block_table, workspace):
-        if x is not None and x.get_device() != dev:
-            _bad_device("out, caches, block_table or workspace", dev)
+    if not (out.get_device() == dev and key_cache.get_device() == dev
+            and value_cache.get_device() == dev and block_table.get_device() == dev
+            and (workspace is None or workspace.get_device() == dev)):
+        _bad_device("out, caches, block_table or workspace", dev)
     if d_error is not None:
         _check_error(d_error, dev)
     _current(dev)
@@ -623,8 +649,8 @@ def pa_decode_shared(out, query, key_cache, value_cache, block_table, context_le
         block_table.data_ptr(), stride if s > 1 else width, width, context_lens.data_ptr(),
         group_starts.data_ptr(), prefix_lens.data_ptr(), g, s, hq, hkv, d, bs, nb, float(scale),
         int(max_context_len), int(max_prefix_len), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _DTYPE[dtype],
-        None if d_error is None else d_error.data_ptr(), _raw_stream(stream, dev))
+        workspace.nbytes, _DTYPE[dtype], None if d_error is None else d_error.data_ptr(),
+        _raw_stream(stream, dev))
     if st:
         _check(lib, st, "pa_decode_shared")
     return out

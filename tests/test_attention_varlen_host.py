@@ -52,8 +52,12 @@ def test_python_argument_checks():
     for i, t in bad:
         args = list(good)
         args[i] = t
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="^(out|query|key|value|cu_seqlens)"):
             pa.pa_attention_varlen(*args, scale=1.0, max_seqlen=8)
+    with pytest.raises(ValueError, match="d_error must be"):
+        pa.pa_attention_varlen(*good, scale=1.0, max_seqlen=8, d_error=torch.zeros(1))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        pa.pa_attention_varlen(*good, scale=1.0, max_seqlen=8)
 
 
 def test_packed_heads_rule():

@@ -53,10 +53,21 @@ def test_python_argument_checks():
                 query_lens=i(s), free_blocks=i(8), num_free=i(1), context_lens_out=i(s),
                 cu_seqlens_q=i(s + 1), slot_mapping=i(t, torch.int64), num_free_out=i(1))
     bad = [dict(query_lens=i(s + 1)), dict(cu_seqlens_q=i(s)), dict(slot_mapping=i(t)),
-           dict(context_lens=i(s, torch.int64)), dict(num_free=i(2)),
+           dict(context_lens=i(s, torch.int64)), dict(query_lens=i(s, torch.int64)),
+           dict(num_free=i(2)), dict(num_free_out=i(1, torch.float32)),
+           dict(context_lens_out=i(2 * s)[::2]), dict(cu_seqlens_q=i(2 * s + 2)[::2]),
+           dict(slot_mapping=i(2 * t, torch.int64)[::2]), dict(free_blocks=i(16)[::2]),
            dict(block_table=torch.zeros((4, s), dtype=torch.int32).t()),
-           dict(block_table=torch.zeros((s + 1, 4), dtype=torch.int32)),
-           dict(free_blocks=i(16)[::2])]
-    for b in bad:
-        with pytest.raises(ValueError):
+           dict(block_table=torch.zeros((s + 1, 4), dtype=torch.int32))]
+    for b in bad:  # refused by name, before the device is looked at
+        name = "context_lens" if "context_lens" in b else next(iter(b))
+        with pytest.raises(ValueError, match=f"^{name} must"):
             pa.pa_build_tables(*{**good, **b}.values(), block_size=16, num_blocks=8)
+    more = dict(block_size=16, num_blocks=8)
+    for kw, text in ((dict(positions=i(t + 1)), "^positions must"),
+                     (dict(positions=i(t, torch.int64)), "^positions must"),
+                     (dict(d_error=i(1, torch.int64)), "d_error must be"),
+                     (dict(d_error=i(0)), "d_error must be"),
+                     (dict(), "current CUDA device")):
+        with pytest.raises(ValueError, match=text):
+            pa.pa_build_tables(*good.values(), **more, **kw)
