@@ -61,7 +61,8 @@ def test_python_argument_checks():
     for n, t in bad:
         args = list(good)
         args[n] = t
-        with pytest.raises(ValueError, match="^(out|caches|block_table|context_lens|group_starts|prefix_lens)"):
+        with pytest.raises(ValueError, match="^(out|caches|block_table|context_lens|group_starts|"
+                                             "prefix_lens)"):
             pa.pa_decode_shared(*args, scale=1.0, max_context_len=8, max_prefix_len=4)
     for kw, text in ((dict(d_error=torch.zeros(1)), "d_error must be"),
                      (dict(), "current CUDA device")):
