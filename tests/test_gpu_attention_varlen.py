@@ -59,15 +59,25 @@ def verify(x, causal=True, seqs=None, err=0, what=""):
     assert bool((x["wide"][x["cu_list"][-1]:] == CANARY).all())
 
 
+# A long bound takes the build for long prompts, the lengths' own the one for
+# short ones.
+BUILDS = pytest.mark.parametrize("bound", [None, 1 << 20])
+
+
+def built(bound):
+    return {} if bound is None else {"max_seqlen": bound}
+
+
 HEADS = [(1, 1), (2, 2), (8, 2), (5, 1), (12, 4), (26, 2), (96, 1), (32, 4)]
 
 
 @pytest.mark.parametrize("n", [1, 2, 31, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300])
 @pytest.mark.parametrize("hq,hkv,d,dtype", [(1, 1, 128, BF16), (8, 2, 64, F16)])
-def test_one_prompt(n, hq, hkv, d, dtype):
+@BUILDS
+def test_one_prompt(n, hq, hkv, d, dtype, bound):
     require_gpu()
     x = make([n], hq, hkv, d, dtype, seed=n)
-    run(x)
+    run(x, **built(bound))
     verify(x)
 
 
@@ -75,21 +85,23 @@ def test_one_prompt(n, hq, hkv, d, dtype):
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("causal", [True, False])
-def test_heads(hq, hkv, d, dtype, causal):
+@BUILDS
+def test_heads(hq, hkv, d, dtype, causal, bound):
     require_gpu()
     x = make([130, 0, 1, 77, 256, 3, 391], hq, hkv, d, dtype, seed=hq + d)
-    run(x, causal)
+    run(x, causal, **built(bound))
     verify(x, causal)
 
 
 @pytest.mark.parametrize("lens", [[900, 1], [1, 900], [640, 640, 640], [1153], [0, 0, 5, 0],
                                   [2000, 40, 1024]])
 @pytest.mark.parametrize("causal", [True, False])
-def test_longer_prompts(lens, causal):
+@BUILDS
+def test_longer_prompts(lens, causal, bound):
     # several tile pairs, odd tile counts, a last tile on both streams
     require_gpu()
     x = make(lens, 4, 2, 128, BF16, seed=len(lens))
-    run(x, causal)
+    run(x, causal, **built(bound))
     verify(x, causal)
 
 
@@ -110,28 +122,31 @@ def test_many_prompts(s, hi):
     verify(x)
 
 
-def test_more_items_than_ctas():
+@BUILDS
+def test_more_items_than_ctas(bound):
     # each CTA walks a long list of short and long items
     require_gpu()
     rng = random.Random(9)
     x = make([rng.choice([1, 100, 128, 200, 333, 700]) for _ in range(40)], 32, 8, 128, BF16,
              seed=9)
-    run(x)
+    run(x, **built(bound))
     verify(x, seqs=[0, 1, 7, 20, 38, 39])
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.11, 1.0, 3.0])
 @pytest.mark.parametrize("dtype", [F16, BF16])
-def test_scales(scale, dtype):
+@BUILDS
+def test_scales(scale, dtype, bound):
     # no preference, reversed preference, nearly one-hot weights
     require_gpu()
     x = make([200, 129], 6, 2, 64, dtype, seed=3)
     x["scale"] = scale
-    run(x)
+    run(x, **built(bound))
     verify(x)
 
 
-def test_rising_scores_rescale_the_running_sum():
+@BUILDS
+def test_rising_scores_rescale_the_running_sum(bound):
     # keys that grow along the sequence: the running maximum jumps by far
     # more than the threshold from tile to tile, in some rows only
     require_gpu()
@@ -139,7 +154,7 @@ def test_rising_scores_rescale_the_running_sum():
     ramp = torch.linspace(0.1, 12.0, 700, device="cuda")[:, None, None]
     x["k"] = (x["k"].float() * ramp).to(BF16)
     x["q"][::3] *= 0.01
-    run(x)
+    run(x, **built(bound))
     verify(x)
 
 
@@ -170,6 +185,28 @@ def test_output_rows_on_16_bytes(at, row):
     verify(x)
     assert bool((flat[:at] == CANARY).all())
     assert bool((flat[at:].view(t, n + row)[:, n:] == CANARY).all())
+
+
+def test_rows_beyond_32_bits_of_elements():
+    # rows of one wide buffer, the last prompts' more than 2^32 bytes and 2^31
+    # elements behind the first's
+    require_gpu()
+    lens, hq, hkv, d, width = [100] * 660, 4, 2, 128, 1 << 15
+    t = sum(lens)
+    assert t * width > 1 << 31
+    buf = torch.empty((t, width // d, d), dtype=F16, device="cuda")
+    q, k, v, out = buf[:, :hq], buf[:, 9:9 + hkv], buf[:, 20:20 + hkv], buf[:, 200:200 + hq]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    for x in (q, k, v):
+        x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+    buf[:, 200 + hq] = CANARY
+    cu = list(range(0, t + 1, 100))
+    x = dict(lens=lens, cu_list=cu, q=q, k=k, v=v, out=out, wide=buf[:, 200:201 + hq],
+             cu=torch.tensor(cu, dtype=torch.int32, device="cuda"), err=new_err(),
+             scale=d ** -0.5)
+    run(x)
+    verify(x, seqs=[0, 1, 327, 328, 655, 656, 658, 659])
 
 
 def test_equals_the_paged_prefill_in_value():

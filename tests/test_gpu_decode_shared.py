@@ -102,6 +102,14 @@ def verify(x, seqs=None, err=0):
     assert bool((x["wide"][:, x["hq"]:] == -3.0).all())
 
 
+# A long bound gives the prefix pass more runs, and the build for long runs.
+BUILDS = pytest.mark.parametrize("bound", [None, 1 << 20])
+
+
+def built(bound):
+    return {} if bound is None else {"max_prefix": bound}
+
+
 @pytest.mark.parametrize("p", [1, 15, 16, 17, 127, 128, 129, 300, 1000])
 @pytest.mark.parametrize("bs", [8, 16, 128])
 def test_prefix_lengths(p, bs):
@@ -116,25 +124,27 @@ def test_prefix_lengths(p, bs):
                                     (26, 2)])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("dtype", [F16, BF16])
-def test_heads(hq, hkv, d, dtype):
+@BUILDS
+def test_heads(hq, hkv, d, dtype, bound):
     # several groups, one of a single sequence, one without a prefix, an empty
     # one, one of empty sequences
     require_gpu()
     x = make([(200, [1, 7, 33]), (70, [9]), (0, [50, 300]), (50, []), (0, [0, 0]), (129, [0, 2])],
              hq, hkv, d, 16, dtype, seed=hq + d)
-    run(x)
+    run(x, **built(bound))
     verify(x)
 
 
 @pytest.mark.parametrize("n,hq,hkv,p", [(3, 4, 4, 900), (31, 8, 2, 400), (32, 8, 2, 400),
                                         (33, 8, 2, 260), (70, 8, 2, 384), (200, 4, 4, 257),
                                         (300, 2, 1, 1000)])
-def test_group_sizes(n, hq, hkv, p):
+@BUILDS
+def test_group_sizes(n, hq, hkv, p, bound):
     # rows of one tile, of two, of a tile pair and a half
     require_gpu()
     rng = random.Random(n)
     x = make([(p, [rng.randint(0, 30) for _ in range(n)])], hq, hkv, 128, 32, BF16, seed=n)
-    run(x)
+    run(x, **built(bound))
     verify(x, seqs=set(rng.sample(range(n), min(n, 40))) | {0, n - 1})
 
 
@@ -148,12 +158,13 @@ def test_group_sizes(n, hq, hkv, p):
     (2, 2, [(6000, 513)]),
     (1, 1, [(19500, 400)]),
 ])
-def test_groups_of_many_query_tiles(hq, hkv, groups):
+@BUILDS
+def test_groups_of_many_query_tiles(hq, hkv, groups, bound):
     require_gpu()
     rng = random.Random(hq * len(groups))
     x = make([(p, [rng.randint(0, 20) for _ in range(n)]) for p, n in groups], hq, hkv, 64, 16,
              BF16, seed=hq)
-    run(x)
+    run(x, **built(bound))
     s = x["starts_list"]
     verify(x, seqs=set(rng.sample(range(s[-1]), min(s[-1], 60))) | set(s[:-1])
            | {e - 1 for e in s[1:]})
@@ -297,6 +308,22 @@ def test_repeated_captured_and_on_two_streams():
     torch.cuda.synchronize()
     assert torch.equal(x["out"], first[0]) and torch.equal(y["out"], first[1])
     assert int(x["err"]) == 0 and int(y["err"]) == 0
+
+
+def test_pools_beyond_32_bits_of_elements():
+    # the batch's blocks moved to the end of pools of more than 2^31 elements
+    require_gpu()
+    x = make([(300, [5, 70, 1]), (130, [9, 200])], 16, 8, 128, 128, BF16, seed=16)
+    nb, n = 16800, x["k_pool"].shape[0]
+    assert nb * 128 * 8 * 128 > 1 << 31
+    for name in ("k_pool", "v_pool"):
+        pool = torch.empty((nb, 128, 8, 128), dtype=BF16, device="cuda")
+        pool[nb - n:] = x[name]
+        x[name] = pool
+    x["table"] = torch.where(x["table"] >= 0, x["table"] + (nb - n), x["table"])
+    x["rows"] = [[r + (nb - n) * 128 for r in rows] for rows in x["rows"]]
+    run(x)
+    verify(x)
 
 
 def test_own_workspace_on_another_stream():
