@@ -635,7 +635,8 @@ pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *que
  * alone, like pa_decode.  A bad block id sets PA_DEVERR_BLOCK_ID and its
  * piece of the context adds nothing.
  * The workspace (256-byte aligned) is of pa_decode_shared_plan's size for the
- * same shape; calls that may run at the same time need one each.  Without groups, or with max_prefix_len 0, the call is pa_decode.
+ * same shape; calls that may run at the same time need one each.  Without
+ * groups, or with max_prefix_len 0, the call is pa_decode.
  * K and V of all P positions of a prefix must be finite for the outputs of the
  * group's shorter sequences (L < P) to be.
  * Supported: num_seqs * num_kv_heads * max_context_len < 2^30 (a GQA group of

@@ -46,8 +46,9 @@
 // sequences x 64/8 heads over 32768 tokens 1640 (170 us).  In the long run a
 // step's length is one stream's chain (softmax and its own MMAs, 2400 cycles,
 // 2048 of them with the tensor core busy); around items, where both streams'
-// softmaxes run at once, it is the fetching of their instructions (ncu: 2.5
-// warps an issue wait for one on 16 x 1000 tokens, 0.6 on 2 x 8192).
+// softmaxes run at once, it is the fetching of their instructions and the pipes
+// they share (ncu: 1.0 warps an issue wait for an instruction on the 24 prompts,
+// with the compact softmax 0.4 on the 16 of up to 2000; 0.6 on 2 x 8192).
 #pragma once
 
 #include <math.h>
