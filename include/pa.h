@@ -640,8 +640,9 @@ pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *que
  * K and V of all P positions of a prefix must be finite for the outputs of the
  * group's shorter sequences (L < P) to be.
  * Supported: num_seqs * num_kv_heads * max_context_len < 2^30 (a GQA group of
- * more than 16 heads counts once per 16) and bounds < 2^30; 16-bit pools; head_dim 64 or 128; block_size 8, 16, 32, 64 or
- * 128; any num_q_heads % num_kv_heads == 0.
+ * more than 16 heads counts once per 16) and bounds < 2^30; 16-bit pools;
+ * head_dim 64 or 128; block_size 8, 16, 32, 64 or 128; any num_q_heads %
+ * num_kv_heads == 0.
  */
 pa_status pa_decode_shared_plan(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
                                 int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
