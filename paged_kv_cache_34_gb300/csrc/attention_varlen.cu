@@ -38,6 +38,7 @@ cudaError_t launch_attention_varlen(const AttentionVarlenArgs &a, cudaStream_t s
   p.wait_ns = flash::wait_limit(a.wait_ns);
   p.out_wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_row_stride % 16 == 0;
   p.kv_bytes = 4 * a.head_dim;
+  p.pair_log2 = a.tiles == 2 ? 1 : 0;
   const int grid = static_cast<int>(a.grid);
   const bool compact = a.max_seqlen <= kCompactLen, bf = a.dtype == PA_BF16;
   auto launch = [&](auto e, auto d) {

@@ -25,9 +25,9 @@
 // Why this shape:
 //  * A work item is a pair of query tiles that share every K/V tile loaded
 //    (A the first tile, B the second), or, where a sequence or group has only
-//    one tile left, that tile on both streams with the keys split between
-//    them by turns (their two states are joined in the epilogue), so neither
-//    stream idles.  A tile's rows are (token, head) pairs of the query heads
+//    one tile left or a launch has few, one tile on both streams with the keys
+//    split between them by turns (their two states are joined in the epilogue),
+//    so neither stream idles.  A tile's rows are (token, head) pairs of the query heads
 //    of one KV head.
 //  * The streams run through the items without a stop: K/V tiles are
 //    numbered through all of a CTA's items ("ring positions") and each stream,
@@ -168,6 +168,7 @@ struct Params {
   int32_t hq, group, pg, tpt;  // heads, per KV head, per tile row group; rows (tokens) per tile
   int32_t hu;               // head units: hq / pg
   bool out_wide;            // packed: output rows are 32-byte aligned
+  int32_t pair_log2;        // packed: log2 of an item's query tiles, 1 or 0
   float scale_log2;         // |scale| * log2 e
   uint32_t negate;          // 1: the scale is negative, Q enters the product negated
   int32_t causal;
@@ -264,7 +265,7 @@ struct PackedSched {
     if (s >= p.num_seqs) return 0;
     const int a = __ldg(p.cu + s), e = __ldg(p.cu + s + 1);
     if (a < 0 || e <= a || e > p.total || e - a > p.max_seqlen) return 0;
-    return (tiles_of(p, e - a) + 1) / 2;
+    return (tiles_of(p, e - a) + p.pair_log2) >> p.pair_log2;
   }
   // The next sequence by length (up to 64).
   __device__ void longest(int lane) {
@@ -320,7 +321,7 @@ struct PackedSched {
       }
     }
     // head units per block: pairs * 2 * tpt tokens of K and V per KV head
-    const int64_t kv = static_cast<int64_t>(pairs) * 2 * p.tpt * p.kv_bytes;
+    const int64_t kv = (static_cast<int64_t>(pairs) << p.pair_log2) * p.tpt * p.kv_bytes;
     const int per_kv = p.group / p.pg;
     const int hb = static_cast<int>(
         min(static_cast<int64_t>(p.hu), max(kBlockBytes / kv, static_cast<int64_t>(1)) * per_kv));
@@ -760,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             it.live = 1;
             it.q0 = __ldg(p.cu + seq);
             it.ntok = __ldg(p.cu + seq + 1) - it.q0;
-            it.tok0 = pair * 2 * p.tpt;
+            it.tok0 = (pair << p.pair_log2) * p.tpt;
             it.head0 = head * p.pg;
             it.key0 = 0;
             it.kend = it.ntok;
@@ -769,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {  // keys up to those of the tile's last token
               const int first = it.tok0 + t * p.tpt;
-              int keys = first < it.ntok ? it.ntok : 0;
+              int keys = first < it.ntok && t <= p.pair_log2 ? it.ntok : 0;
               if (p.causal && keys > 0) keys = min(keys, first + p.tpt);
               it.cnt[t] = (keys + kKeys - 1) / kKeys;
             }

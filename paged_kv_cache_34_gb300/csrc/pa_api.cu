@@ -869,7 +869,12 @@ pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *que
   a.num_kv_heads = num_kv_heads;
   a.head_dim = head_dim;
   a.packed_heads = pa::flash_packed_heads(num_q_heads / num_kv_heads);
-  a.grid = pa::varlen_items(num_seqs, total_tokens, max_seqlen, num_q_heads, a.packed_heads);
+  auto items = [&](int tiles) {
+    return pa::varlen_items(num_seqs, total_tokens, max_seqlen, num_q_heads, a.packed_heads,
+                            tiles);
+  };
+  a.tiles = 2;
+  a.grid = items(2);
   if (a.grid > INT32_MAX) return PA_ERR_UNSUPPORTED;
   flash_scale(scale, &a.scale_log2, &a.negate);
   a.causal = causal ? 1 : 0;
@@ -878,6 +883,18 @@ pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *que
   a.wait_ns = pa::pipeline_wait_ns();
   cudaError_t e = current_num_sms(&a.num_sms);
   if (e != cudaSuccess) return cuda_fail(e);
+  // Few query tiles: one per item, its keys on both streams by turns, while all
+  // items run at once (500 tokens 32/32 heads: 12.0 us, in pairs 14.3; 1000 8/2:
+  // 17.6 and 21.7; 37 tokens 8/2: 7.3 and 8.5).  Beyond that items of few keys
+  // cost more than they split (4 x 200 tokens 32/8: 14.1 and 13.4) and at
+  // head_dim 128 the K ring, two tiles for the streams' two steps, holds long ones
+  // up (4000 tokens 8/2: 70 and 55); with its four at head_dim 64 two rounds
+  // still pay (4000 8/2: 34.7 and 44.6; 700 + 900 12/4: 13.5 and 17.4).
+  const int64_t rounds = head_dim == 64 && max_seqlen >= 640 ? 2 : 1;
+  if (items(1) <= rounds * a.num_sms) {
+    a.tiles = 1;
+    a.grid = items(1);
+  }
   if (!encode_rows_map(&a.tm_q, query, dtype, head_dim, num_q_heads, total_tokens, q_row_stride,
                        128 / a.packed_heads, false, a.packed_heads) ||
       !encode_rows_map(&a.tm_k, key, dtype, head_dim, num_kv_heads, total_tokens, kv_row_stride,

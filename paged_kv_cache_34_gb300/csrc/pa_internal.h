@@ -204,14 +204,15 @@ inline int flash_packed_heads(int group) {
   return 1;
 }
 
-// The most items a batch of packed prompts has (one CTA per item): pairs of
-// query tiles x head units; at most one pair of a sequence is partly filled.
+// The most items a batch of packed prompts has (one CTA per item) of `tiles`
+// query tiles each, times head units; at most one item of a sequence is partly
+// filled.
 inline int64_t varlen_items(int num_seqs, int total, int max_seqlen, int num_q_heads,
-                            int packed_heads) {
-  const int64_t rows = 2 * (128 / packed_heads);
+                            int packed_heads, int tiles) {
+  const int64_t rows = tiles * (128 / packed_heads);
   const int64_t longest = max_seqlen < total ? max_seqlen : total;
-  const int64_t pairs = total / rows + num_seqs, most = num_seqs * ((longest + rows - 1) / rows);
-  return (pairs < most ? pairs : most) * (num_q_heads / packed_heads);
+  const int64_t items = total / rows + num_seqs, most = num_seqs * ((longest + rows - 1) / rows);
+  return (items < most ? items : most) * (num_q_heads / packed_heads);
 }
 
 struct AttentionVarlenArgs {
@@ -222,6 +223,7 @@ struct AttentionVarlenArgs {
   int32_t num_q_heads, num_kv_heads, head_dim;
   int packed_heads;
   int64_t grid;      // varlen_items
+  int tiles;         // query tiles per item, 1 or 2
   float scale_log2;  // |scale| * log2(e), not 0
   bool negate;       // the scale is negative
   int32_t causal;

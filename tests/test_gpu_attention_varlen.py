@@ -96,13 +96,39 @@ def test_heads(hq, hkv, d, dtype, causal, bound):
 @pytest.mark.parametrize("lens", [[900, 1], [1, 900], [640, 640, 640], [1153], [0, 0, 5, 0],
                                   [2000, 40, 1024]])
 @pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (40, 40, 128), (80, 40, 64)])
 @BUILDS
-def test_longer_prompts(lens, causal, bound):
-    # several tile pairs, odd tile counts, a last tile on both streams
+def test_longer_prompts(lens, causal, hq, hkv, d, bound):
+    # query tiles alone (few of them) and in pairs, odd tile counts, a last tile
+    # on both streams
     require_gpu()
-    x = make(lens, 4, 2, 128, BF16, seed=len(lens))
+    x = make(lens, hq, hkv, d, BF16, seed=len(lens))
     run(x, causal, **built(bound))
+    for n, heads in (("q", 4), ("out", 4), ("k", 4 * hkv // hq), ("v", 4 * hkv // hq)):
+        x[n] = x[n][:, :heads]  # the first heads' worth of checking
     verify(x, causal)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_query_tiles_alone_and_in_pairs(d):
+    # the same prompt's heads in a small batch and among many heads give the same
+    # values but for the order of sums
+    require_gpu()
+    x = make([700, 33], 32, 32, d, BF16, seed=d, packed_kv=False)
+    run(x)
+    verify(x)
+    y = dict(x, q=x["q"][:, :4].contiguous(), k=x["k"][:, :4].contiguous(),
+             v=x["v"][:, :4].contiguous(), out=torch.empty_like(x["q"][:, :4]))
+    run(y)
+    torch.cuda.synchronize()
+    got, want = y["out"].double(), x["out"][:, :4].double()
+    # each is within the bound of the exact value, so within twice it of the other
+    for h in range(4):
+        for a, n in ((0, 700), (700, 33)):
+            i = torch.arange(n, device="cuda")
+            _, bound = attend(x["q"][a:a + n, h], x["k"][a:a + n, h], x["v"][a:a + n, h],
+                              x["scale"], i[None] <= i[:, None])
+            assert bool(((got - want)[a:a + n, h].abs() <= 2 * bound).all())
 
 
 def test_long_prompt():
