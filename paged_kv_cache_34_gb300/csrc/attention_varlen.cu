@@ -44,6 +44,9 @@ cudaError_t launch_attention_varlen(const AttentionVarlenArgs &a, cudaStream_t s
   auto launch = [&](auto e, auto d) {
     using E = decltype(e);
     constexpr int D = decltype(d)::value;
+    if (a.tiles == 1)
+      return flash::launch<E, D, flash::kPackedSingle, true>(p, a.tm_q, a.tm_k, a.tm_v, grid,
+                                                             stream);
     return compact ? flash::launch<E, D, flash::kPacked, true>(p, a.tm_q, a.tm_k, a.tm_v, grid,
                                                                stream)
                    : flash::launch<E, D, flash::kPacked, false>(p, a.tm_q, a.tm_k, a.tm_v, grid,

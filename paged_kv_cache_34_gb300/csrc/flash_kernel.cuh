@@ -79,7 +79,12 @@ enum Mode {
   kPacked = 0,       // packed prompts over plain rows
   kPaged = 1,        // prefix pass
   kPagedSingle = 2,  // ... where no group has more rows than one query tile
+  kPackedSingle = 3  // packed prompts, one query tile per item
 };
+template <int MODE>
+constexpr bool kIsPaged = MODE == kPaged || MODE == kPagedSingle;
+template <int MODE>
+constexpr bool kIsSingle = MODE == kPagedSingle || MODE == kPackedSingle;
 
 template <int D, int MODE>
 struct Layout {
@@ -93,9 +98,9 @@ struct Layout {
   static constexpr int kUnit = D == 128 ? 1 : 2;
   // Q buffers of stream A and B; a single-tile launch's streams share theirs.
   static constexpr int kQA = (MODE == kPacked ? 2 : 1) * kUnit;
-  static constexpr int kQB = (MODE == kPagedSingle ? 0 : 1) * kUnit;
+  static constexpr int kQB = (kIsSingle<MODE> ? 0 : 1) * kUnit;
   static constexpr int NQ = kQA + kQB;
-  static constexpr int NK = (MODE == kPagedSingle ? 3 : 2) * kUnit;
+  static constexpr int NK = (kIsSingle<MODE> ? 3 : 2) * kUnit;
   static constexpr int NV = (MODE == kPacked ? 2 : 3) * kUnit;
   static constexpr int kQOff = 0;
   static constexpr int kKOff = NQ * kTile;
@@ -620,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ CUtensorMap tmk,
                  const __grid_constant__ CUtensorMap tmv) {
   using L = Layout<D, MODE>;
-  constexpr bool PAGED = MODE != kPacked;
+  constexpr bool PAGED = kIsPaged<MODE>, SINGLE = kIsSingle<MODE>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
   float *s_m = reinterpret_cast<float *>(smem + L::kMlOff), *s_l = s_m + 256;
@@ -666,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n = 1;
       if ((i >= L::kPFull && i < L::kPFull + 2) || (i >= L::kOFree && i < L::kOFree + 2)) n = 4;
       if (i >= L::kMLFull && i < L::kMLFull + 2) n = 128;
-      if (i >= L::kQEmpty && i < L::kQEmpty + L::NQ) n = MODE == kPagedSingle ? 2 : 1;
+      if (i >= L::kQEmpty && i < L::kQEmpty + L::NQ) n = SINGLE ? 2 : 1;
       if (i >= L::kKEmpty && i < L::kKEmpty + L::NK) n = 2;    // either stream
       if (i >= L::kVEmpty && i < L::kVEmpty + L::NV) n = 2;
       if (i >= L::kVFixed && i < L::kVFixed + L::NV) n = 4;    // the epilogue's warps
@@ -883,8 +888,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(L::kBegun));
         // the streams' query tiles: the first one's before the item's first K
         // (a shared one counts as stream A's)
-        const bool two = MODE != kPagedSingle && it.cnt[0] > 0 && it.cnt[1] > 0;
-        const int t_first = MODE == kPagedSingle || it.cnt[0] > 0 ? 0 : 1;
+        const bool two = !SINGLE && it.cnt[0] > 0 && it.cnt[1] > 0;
+        const int t_first = SINGLE || it.cnt[0] > 0 ? 0 : 1;
         // PAGED: this lane's block ids, the next tile's in flight
         const int32_t *bt = PAGED ? p.block_table + it.kv0 * p.bt_stride : nullptr;
         auto load_id = [&](int i) {
@@ -1007,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         first = true;
         tail = (it.flags & kTail) != 0;
         odd = (it.flags & kTailOdd) != 0;
-        if (left > 0 || MODE == kPagedSingle) ++q;
+        if (left > 0 || SINGLE) ++q;
         unused = left == 0;
       };
       // Accounts for the tiles before ring position m that this stream does
@@ -1065,7 +1070,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Else K is about to land, and waiting for it keeps P V and Q K^T
             // in one block (prefix pass, looking / waiting: 64 / 72 us on 64
             // sequences in 6 groups, 365 / 351 on 256 of one).
-            along = PAGED && step == 2 ? __all_sync(0xffffffffu, mbar_test(bar(kb), kp)) != 0
+            along = MODE != kPacked && step == 2 ? __all_sync(0xffffffffu, mbar_test(bar(kb), kp)) != 0
                                        : ready(kb, kp);
             if (along && first) along = ready(L::kQFull + L::q_slot(t, q), L::q_use(t, q) & 1);
           }
@@ -1108,7 +1113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Otherwise walk to the next tile the stream uses.
         while (ok && !ended && left == 0) {
           skip_to(end);
-          if (MODE == kPagedSingle && unused && ok) {
+          if (SINGLE && unused && ok) {
             ok = wait(L::kQFull + L::q_slot(t, q), L::q_use(t, q) & 1);
             if (lane == 0) mbar_arrive(bar(L::kQEmpty + L::q_slot(t, q)));
           }

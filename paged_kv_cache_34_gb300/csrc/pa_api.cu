@@ -890,7 +890,7 @@ pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *que
   // head_dim 128 the K ring, two tiles for the streams' two steps, holds long ones
   // up (4000 tokens 8/2: 70 and 55); with its four at head_dim 64 two rounds
   // still pay (4000 8/2: 34.7 and 44.6; 700 + 900 12/4: 13.5 and 17.4).
-  const int64_t rounds = head_dim == 64 && max_seqlen >= 640 ? 2 : 1;
+  const int64_t rounds = max_seqlen >= 640 ? 2 : 1;
   if (items(1) <= rounds * a.num_sms) {
     a.tiles = 1;
     a.grid = items(1);
