@@ -92,8 +92,8 @@ struct Layout {
   static constexpr int kTile = kHalves * kHalf;  // one Q, K or V tile
   // Buffers of 32 KB (16 at head_dim 64), in what the 227 KB hold.  Packed
   // prompts run through many items: a third Q buffer lets the next one's first
-  // query tile load early.  The prefix pass has few items and K and V from
-  // memory: they get the room (67 us against 82 with the packed split on 8
+  // query tile load early.  The prefix pass, and items of single tiles, have few
+  // items and wait for K and V: they get the room (67 us against 82 with the packed split on 8
   // sequences behind 16384 tokens, 32/32 heads).
   static constexpr int kUnit = D == 128 ? 1 : 2;
   // Q buffers of stream A and B; a single-tile launch's streams share theirs.
@@ -1070,8 +1070,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Else K is about to land, and waiting for it keeps P V and Q K^T
             // in one block (prefix pass, looking / waiting: 64 / 72 us on 64
             // sequences in 6 groups, 365 / 351 on 256 of one).
-            along = MODE != kPacked && step == 2 ? __all_sync(0xffffffffu, mbar_test(bar(kb), kp)) != 0
-                                       : ready(kb, kp);
+            along = MODE != kPacked && step == 2
+                        ? __all_sync(0xffffffffu, mbar_test(bar(kb), kp)) != 0
+                        : ready(kb, kp);
             if (along && first) along = ready(L::kQFull + L::q_slot(t, q), L::q_use(t, q) & 1);
           }
           if (ok && pfirst) {  // O of the stream's previous item has been read

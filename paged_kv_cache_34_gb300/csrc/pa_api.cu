@@ -884,13 +884,14 @@ pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *que
   cudaError_t e = current_num_sms(&a.num_sms);
   if (e != cudaSuccess) return cuda_fail(e);
   // Few query tiles: one per item, its keys on both streams by turns, while all
-  // items run at once (500 tokens 32/32 heads: 12.0 us, in pairs 14.3; 1000 8/2:
-  // 17.6 and 21.7; 37 tokens 8/2: 7.3 and 8.5).  Beyond that items of few keys
-  // cost more than they split (4 x 200 tokens 32/8: 14.1 and 13.4) and at
-  // head_dim 128 the K ring, two tiles for the streams' two steps, holds long ones
-  // up (4000 tokens 8/2: 70 and 55); with its four at head_dim 64 two rounds
-  // still pay (4000 8/2: 34.7 and 44.6; 700 + 900 12/4: 13.5 and 17.4).
-  const int64_t rounds = max_seqlen >= 640 ? 2 : 1;
+  // items run at once (500 tokens 32/32 heads: 11.2 us, in pairs 14.1; 2000 8/2:
+  // 21.5 and 33.8; 37 tokens 8/2: 7.2 and 8.4), of longer prompts in up to four
+  // rounds (2000 tokens 32/8, 3.4 rounds: 40.4 and 46.8; 1024 32/8, 1.7: 20.1 and
+  // 23.0), which pairs take half of: more items of few keys cost more than they
+  // even out (30 x 100 tokens 8/2, 1.6 rounds: 14.7 and 11.7), and so do more
+  // rounds, that load K and V for every tile (8000 tokens 16/4, 6.6: 210 and 167;
+  // 4 x 1000 32/32, 6.7: 52 and 48).
+  const int64_t rounds = max_seqlen >= 640 ? 4 : 1;
   if (items(1) <= rounds * a.num_sms) {
     a.tiles = 1;
     a.grid = items(1);
