@@ -92,9 +92,10 @@ struct Layout {
   static constexpr int kTile = kHalves * kHalf;  // one Q, K or V tile
   // Buffers of 32 KB (16 at head_dim 64), in what the 227 KB hold.  Packed
   // prompts run through many items: a third Q buffer lets the next one's first
-  // query tile load early.  The prefix pass, and items of single tiles, have few
-  // items and wait for K and V: they get the room (67 us against 82 with the packed split on 8
-  // sequences behind 16384 tokens, 32/32 heads).
+  // query tile load early.  The prefix pass, and a launch of single tiles, have
+  // few items and wait for K and V: these get the room (8 sequences behind 16384
+  // tokens, 32/32 heads: 67 us against 82 with the pairs' split; one prompt of
+  // 2000 tokens 8/2: 21.5 against 30.0).
   static constexpr int kUnit = D == 128 ? 1 : 2;
   // Q buffers of stream A and B; a single-tile launch's streams share theirs.
   static constexpr int kQA = (MODE == kPacked ? 2 : 1) * kUnit;
