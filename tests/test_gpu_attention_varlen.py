@@ -302,11 +302,12 @@ def test_captured_repeated_and_on_two_streams():
     assert int(x["err"]) == 0
 
 
-def test_a_wait_that_runs_out_is_reported():
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (64, 64)])  # tiles alone, in pairs
+def test_a_wait_that_runs_out_is_reported(hq, hkv):
     # a 1 ns bound: the launch gives up somewhere, says so and leaves the
     # device usable; the next launches give the same values as before
     require_gpu()
-    x = make([300, 200], 8, 2, 128, BF16, seed=7)
+    x = make([300, 200], hq, hkv, 128, BF16, seed=7)
     run(x)
     torch.cuda.synchronize()
     want = x["out"].clone()
