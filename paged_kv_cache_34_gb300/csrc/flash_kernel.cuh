@@ -1341,11 +1341,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_ref = -INFINITY, l = 0.f;
       for (int i = 0; i < cnt; ++i, ++n, bound -= bstep) {
         ok = wait_for(bar(L::kSFull + t), n & 1, p.wait_ns);
-        if (!ok) break;
         tc_fence_after();
         // Columns past `bound` are hidden: where a tile has any, its S goes
         // through a loop (not unrolled, for the instruction cache's sake).
-        if (__any_sync(0xffffffffu, bound < kKeys - 1)) {
+        // (A wait that ran out in any lane ends the whole warp here.)
+        if (__any_sync(0xffffffffu, bound < kKeys - 1 || !ok)) {
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
 #pragma unroll 1
           for (int c = 0; c < kKeys; c += 32) {
             if (!__any_sync(0xffffffffu, bound < c + 31)) continue;
