@@ -595,7 +595,7 @@ pa_status pa_build_tables(int32_t *block_table, int64_t block_table_stride,
  * A cu_seqlens that is none, or a sequence longer than max_seqlen, sets
  * PA_DEVERR_CU_SEQLENS; a sequence whose own two entries are bad is skipped.
  * No row of out may overlap query, key or value.  K and V of a sequence must
- * be finite for its rows to be.
+ * be finite for its rows to be; a NaN in a query makes that (row, head) NaN.
  * Supported: fp16 / bf16, head_dim 64 or 128, any num_q_heads % num_kv_heads
  * == 0.
  */
@@ -638,7 +638,8 @@ pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *que
  * same shape; calls that may run at the same time need one each.  Without
  * groups, or with max_prefix_len 0, the call is pa_decode.
  * K and V of all P positions of a prefix must be finite for the outputs of the
- * group's shorter sequences (L < P) to be.
+ * group's shorter sequences (L < P) to be; a NaN in a query makes that
+ * (sequence, head) NaN.
  * Supported: num_seqs * num_kv_heads * max_context_len < 2^30 (a GQA group of
  * more than 16 heads counts once per 16) and bounds < 2^30; 16-bit pools;
  * head_dim 64 or 128; block_size 8, 16, 32, 64 or 128; any num_q_heads %

@@ -146,7 +146,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       float Mn = M;
 #pragma unroll
       for (int k = 0; k < kJoinBatch; ++k) Mn = fmaxf(Mn, st[k].x);
-      if (Mn == -INFINITY) continue;  // nothing visible yet
+      if (Mn == -INFINITY) {  // nothing visible yet: the sums are 0, or NaN of NaN scores
+#pragma unroll
+        for (int k = 0; k < kJoinBatch; ++k) l += st[k].y;
+        continue;
+      }
       const float cr = fast_exp2(M - Mn);  // 0 while M is -inf
       l *= cr;
 #pragma unroll
@@ -178,18 +182,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     l = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    if (Mt != -INFINITY) {
 #pragma unroll
-      for (int k = 0; k < W; ++k) {
-        const float f = fast_exp2(s_m[k] - Mt);  // 0 for a warp that saw nothing
-        l += f * s_l[k];
+    for (int k = 0; k < W; ++k) {
+      // 0 for a warp that saw nothing (its sum is 0, or NaN, which stays)
+      const float f = Mt == -INFINITY ? 1.f : fast_exp2(s_m[k] - Mt);
+      l += f * s_l[k];
 #pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] += f * s_o[k][lane * V + v];
-      }
+      for (int v = 0; v < V; ++v) acc[v] += f * s_o[k][lane * V + v];
     }
   }
-  // a sum that is not positive (no visible key, or only bad blocks) gives zeros
-  const bool good = l > 0.f;
+  // no visible key, or only bad blocks, give zeros; a sum that is NaN gives NaN
+  const bool good = l != 0.f;
   const float inv = good ? 1.f / l : 0.f;
   typename E::T *out =
       static_cast<typename E::T *>(p.out) + b * p.out_row_stride + h * D + lane * V;

@@ -1217,7 +1217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 2; ++t) f[t] = m[t] > -INFINITY && !bad ? fast_exp2(m[t] - mm) : 0.f;
         const float ll = f[0] * l[0] + f[1] * l[1];
         if constexpr (!PAGED) {
-          const float inv = ll > 0.f ? 1.f / ll : 0.f;
+          const float inv = ll == 0.f ? 0.f : 1.f / ll;
           f[0] *= inv;
           f[1] *= inv;
         }
@@ -1238,8 +1238,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool both = use[0] && use[1];
         const uint64_t fa = f2_pack(t0 ? f[1] : f[0], t0 ? f[1] : f[0]);
         const uint64_t fb = f2_pack(f[1], f[1]);
-        // rows that saw no key are 0, whatever O holds
-        const bool none = !(ll > 0.f) || bad;
+        // rows that saw no key are 0, whatever O holds; a sum that is NaN (a query
+        // or a visible key was) is passed on
+        const bool none = ll == 0.f || bad;
         const bool any_none = __any_sync(0xffffffffu, none && row_ok);
         // 32 bytes a lane and store where rows allow it: a store's 32 rows are
         // 32 lines to the load/store unit either way (24 prompts of 2691 tokens
