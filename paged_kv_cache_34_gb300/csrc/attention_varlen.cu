@@ -29,6 +29,7 @@ cudaError_t launch_attention_varlen(const AttentionVarlenArgs &a, cudaStream_t s
   p.hu = p.hq / p.pg;
   p.scale_log2 = a.scale_log2;
   p.negate = a.negate ? 1u : 0u;
+  p.q_off = a.q_off;
   p.causal = a.causal;
   p.cu = a.cu_seqlens;
   p.num_seqs = a.num_seqs;

@@ -259,6 +259,7 @@ cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream)
   f.hu = f.hq / f.pg;
   f.scale_log2 = a.scale_log2;
   f.negate = a.negate ? 1u : 0u;
+  f.q_off = a.q_off;
   f.num_seqs = d.num_seqs;
   f.block_table = d.block_table;
   f.bt_stride = d.block_table_stride;

@@ -175,7 +175,8 @@ struct Params {
   int32_t hu;               // head units: hq / pg
   bool out_wide;            // packed: output rows are 32-byte aligned
   int32_t pair_log2;        // packed: log2 of an item's query tiles, 1 or 0
-  float scale_log2;         // |scale| * log2 e
+  float scale_log2;         // |scale| * log2 e, > 0
+  int32_t q_off;            // 0; at scale 0 the query's rows: its tiles are read as zeros
   uint32_t negate;          // 1: the scale is negative, Q enters the product negated
   int32_t causal;
   // packed prompts
@@ -871,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (use > 0 && !warp_wait(L::kQEmpty + slot, (use - 1) & 1)) return false;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(L::kQFull + slot), q_bytes);
-          const int tok = it.q0 + it.tok0 + ((it.flags & kSingle) ? 0 : t * p.tpt);
+          const int tok = p.q_off + it.q0 + it.tok0 + ((it.flags & kSingle) ? 0 : t * p.tpt);
           const uint32_t dst = smem_u32(smem + L::kQOff + slot * L::kTile);
 #pragma unroll
           for (int h = 0; h < L::kHalves; ++h)

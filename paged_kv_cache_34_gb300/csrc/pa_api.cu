@@ -102,13 +102,15 @@ bool encode_rows_map(CUtensorMap *map, const void *base, pa_dtype dtype, int hea
 
 bool valid_block_size(int bs) { return bs == 8 || bs == 16 || bs == 32 || bs == 64 || bs == 128; }
 
-// The factor of the flash engine's scores: |scale| log2 e, kept away from 0 so
-// that a masked score (-inf) times it stays -inf (1e-37 leaves every finite
-// score's weight at 1), and whether Q enters the product negated.
-void flash_scale(float scale, float *scale_log2, bool *negate) {
+// The factor of the flash engine's scores: |scale| log2 e, and whether Q enters
+// the product negated.  It has to be positive, so that a masked score (-inf)
+// times it stays -inf: at scale 0 the query tiles are taken from behind the last
+// row instead (q_off rows on), where TMA reads zeros, and every score is 0.
+void flash_scale(float scale, int32_t rows, float *scale_log2, bool *negate, int32_t *q_off) {
   const double f = fabs(static_cast<double>(scale)) * 1.4426950408889634;
-  *scale_log2 = f > 1e-37 ? static_cast<float>(f) : 1e-37f;
+  *scale_log2 = scale == 0.0f ? 1.0f : static_cast<float>(f);  // > 0: f rounds up from 2^-149
   *negate = scale < 0.0f;
+  *q_off = scale == 0.0f ? rows : 0;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -876,7 +878,8 @@ pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *que
   a.tiles = 2;
   a.grid = items(2);
   if (a.grid > INT32_MAX) return PA_ERR_UNSUPPORTED;
-  flash_scale(scale, &a.scale_log2, &a.negate);
+  if (scale == 0.0f && total_tokens > (1 << 30)) return PA_ERR_UNSUPPORTED;  // q_off + a row
+  flash_scale(scale, total_tokens, &a.scale_log2, &a.negate, &a.q_off);
   a.causal = causal ? 1 : 0;
   a.d_error = d_error;
   a.dtype = dtype;
@@ -1025,7 +1028,7 @@ pa_status pa_decode_shared(void *out, int64_t out_row_stride, const void *query,
   a.prefix_cost =
       pa::shared_cost(num_seqs, num_groups, num_q_heads, num_kv_heads, max_prefix_len);
   a.packed_heads = pa::flash_packed_heads(num_q_heads / num_kv_heads);
-  flash_scale(scale, &a.scale_log2, &a.negate);
+  flash_scale(scale, num_seqs, &a.scale_log2, &a.negate, &a.q_off);
   char *w = static_cast<char *>(workspace) + s.decode_bytes;
   a.ws_o = reinterpret_cast<float *>(w);
   w += s.o_bytes;

@@ -226,6 +226,7 @@ struct AttentionVarlenArgs {
   int tiles;         // query tiles per item, 1 or 2
   float scale_log2;  // |scale| * log2(e), not 0
   bool negate;       // the scale is negative
+  int32_t q_off;     // scale 0: rows to move the query tiles by, out of the tensor
   int32_t causal;
   int32_t *d_error;
   pa_dtype dtype;
@@ -278,6 +279,7 @@ struct DecodeSharedArgs {
   int packed_heads;
   float scale_log2;    // |scale| * log2(e), not 0
   bool negate;         // the scale is negative
+  int32_t q_off;       // scale 0: rows to move the query tiles by, out of the tensor
   CUtensorMap tm_q;    // box 64 x packed_heads x 128 / packed_heads
   CUtensorMap tm_k, tm_v;  // box 64 x 1 x block_size
   // [rows, D] and [rows, 2] states.  A group of n sequences takes n x packed_heads

@@ -90,3 +90,42 @@ def test_nan_of_a_query_in_a_join_of_four_warps():
     nan = torch.isnan(x["out"])
     assert bool(nan[0, 1].all()) and int(nan.sum()) == 128
     shared.verify(x, seqs=[1])
+
+
+def big(x, power):
+    """Queries and keys whose scores reach 10^38, still finite in fp32."""
+    for n in ("q", "k"):
+        x[n].mul_(2.0 ** power)
+
+
+SCALES = pytest.mark.parametrize("scale,power", [
+    # (scale, power of two on q and k): no preference, whatever the scores; one
+    # that brings the largest scores to a few units; the reverse, nearly one-hot
+    (0.0, 0), (0.0, 58), (2.0 ** -126, 59), (-0.11, 0), (3.0, 0)])
+
+
+@VARLEN
+@SCALES
+def test_scales(build, scale, power, dtype=BF16):
+    require_gpu()
+    x = varlen.make([200, 0, 129, 1], 6, 2, 64, dtype, seed=24, packed_kv=False)
+    big(x, power)
+    x["scale"] = scale
+    varlen.verify(first_copy(call(x, build)))
+
+
+@VARLEN
+@pytest.mark.parametrize("scale", [0.0, -0.11, 3.0])
+def test_scales_in_half_precision(build, scale):
+    test_scales(build, scale, 0, F16)
+
+
+@SHARED
+@SCALES
+def test_scales_over_a_prefix(build, hq, hkv, bound, scale, power):
+    require_gpu()
+    x = shared.make([(260, [5, 17, 0, 70, 1]), (40, [3])], hq, hkv, 64, 16, BF16, seed=25)
+    big(dict(q=x["q"], k=x["k_pool"]), power)
+    x["scale"] = scale
+    decode(x, build, bound)
+    shared.verify(x)
