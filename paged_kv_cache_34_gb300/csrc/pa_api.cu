@@ -923,7 +923,7 @@ struct SharedPlan {
 };
 pa_status shared_plan(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
                       int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
-                      int32_t max_prefix_len, SharedPlan *out) {
+                      int32_t max_prefix_len, int32_t block_size, SharedPlan *out) {
   if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_context_len < 0 ||
       num_groups < 0 || max_prefix_len < 0 || num_q_heads % num_kv_heads != 0)
     return PA_ERR_SHAPE;
@@ -939,6 +939,11 @@ pa_status shared_plan(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
       (max_context_len >= most || max_prefix_len >= most ||
        !use_balanced(num_seqs, units, max_context_len, 0) ||
        pa::shared_cost(num_seqs, num_groups, num_q_heads, num_kv_heads, max_prefix_len) >= most))
+    return PA_ERR_UNSUPPORTED;
+  // The own parts' schedule keeps 12 bytes per sequence in shared memory.
+  if (s.shared && pa::decode_smem_bytes(head_dim, num_seqs, 0, block_size) +
+                          4 * static_cast<size_t>(num_seqs) >
+                      227 * 1024)
     return PA_ERR_UNSUPPORTED;
   const pa_status st = pa_decode_plan(num_seqs, num_q_heads, num_kv_heads, head_dim,
                                       max_context_len, 0, &P, &s.decode_bytes);
@@ -969,8 +974,9 @@ pa_status pa_decode_shared_plan(int32_t num_seqs, int32_t num_groups, int32_t nu
                                 int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
                                 int32_t max_prefix_len, size_t *workspace_bytes_out) {
   SharedPlan s;
+  // (8: what the plan serves, the call serves at any block size)
   const pa_status st = shared_plan(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim,
-                                   max_context_len, max_prefix_len, &s);
+                                   max_context_len, max_prefix_len, 8, &s);
   if (st == PA_OK && workspace_bytes_out) *workspace_bytes_out = s.bytes;
   return st;
 }
@@ -999,7 +1005,7 @@ pa_status pa_decode_shared(void *out, int64_t out_row_stride, const void *query,
   }
   SharedPlan s;
   st = shared_plan(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, max_context_len,
-                   max_prefix_len, &s);
+                   max_prefix_len, block_size, &s);
   if (st != PA_OK) return st;
   if (!s.shared)
     return decode_call(out, out_row_stride, query, q_row_stride, key_cache, value_cache,
@@ -1010,9 +1016,6 @@ pa_status pa_decode_shared(void *out, int64_t out_row_stride, const void *query,
   if (!workspace || workspace_bytes < s.bytes ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return PA_ERR_WORKSPACE;
-  if (pa::decode_smem_bytes(head_dim, num_seqs, 0, block_size) + 4 * static_cast<size_t>(num_seqs) >
-      227 * 1024)
-    return PA_ERR_UNSUPPORTED;
   pa::DecodeSharedArgs a;
   pa::DecodeArgs &d = a.decode;
   d = c.args;

@@ -129,3 +129,13 @@ def test_scales_over_a_prefix(build, hq, hkv, bound, scale, power):
     x["scale"] = scale
     decode(x, build, bound)
     shared.verify(x)
+
+
+def test_the_largest_planned_batch():
+    # as many sequences as the plan serves, at the smallest blocks
+    require_gpu()
+    x = shared.make([(9, [1] * 5000), (17, [0, 3] * 2600), (0, [2] * 11)], 2, 1, 128, 8, F16,
+                    seed=26)
+    assert len(x["ctx_list"]) == 10211
+    shared.run(x)
+    shared.verify(x, seqs=[0, 1, 31, 4999, 5000, 5001, 8192, 10199, 10200, 10210])

@@ -3,6 +3,7 @@ CPU (no pointer here is ever dereferenced; see also the operators' own files).""
 import pytest
 
 import test_attention_varlen_host as varlen
+import test_decode_shared_host as shared
 from test_attention_varlen_host import lib  # noqa: F401  (fixture)
 
 
@@ -12,3 +13,16 @@ from test_attention_varlen_host import lib  # noqa: F401  (fixture)
 ])
 def test_attention_varlen_refusals(lib, kw, status):  # noqa: F811
     assert varlen.call(lib, **kw) == status
+
+
+@pytest.mark.parametrize("d,most", [(64, 14393), (128, 10211)])
+def test_decode_shared_plan_refuses_batches_that_the_call_refuses(lib, d, most):  # noqa: F811
+    # 12 bytes per sequence in shared memory: refused by both, before any CUDA call
+    for s in (most + 1, 3 * most):
+        assert lib.pa_decode_shared_plan(s, 1, 8, 2, d, 16, 16, None) == 3
+        assert shared.call(lib, s=s, d=d, bs=8, qs=8 * d, os=8 * d, mc=16, mp=16) == 3
+    # (PA_ERR_CUDA without a device: not refused)
+    assert lib.pa_decode_shared_plan(most, 1, 8, 2, d, 16, 16, None) != 3
+    assert shared.call(lib, s=most, d=d, bs=8, qs=8 * d, os=8 * d, mc=16, mp=16) != 3
+    # without a prefix it is the plain decode, whose limit is its own
+    assert lib.pa_decode_shared_plan(most + 1, 0, 8, 2, d, 16, 16, None) != 3
