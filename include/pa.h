@@ -592,7 +592,10 @@ pa_status pa_build_tables(int32_t *block_table, int64_t block_table_stride,
  *                their out rows are left as they were; they may hold
  *                anything.
  *   max_seqlen   host upper bound of the sequences' lengths.
- * A cu_seqlens that is none, or a sequence longer than max_seqlen, sets
+ * With num_seqs, total_tokens or max_seqlen 0 the host has said that there is
+ * nothing to attend to: nothing is launched, cu_seqlens is not read (so no
+ * error bit is set for it) and out is left as it was.  Otherwise a cu_seqlens
+ * that is none, or a sequence longer than max_seqlen, sets
  * PA_DEVERR_CU_SEQLENS; a sequence whose own two entries are bad is skipped.
  * No row of out may overlap query, key or value.  K and V of a sequence must
  * be finite for its rows to be; a NaN in a query makes that (row, head) NaN.

@@ -552,7 +552,8 @@ def pa_attention_varlen(out, query, key, value, cu_seqlens, *, scale, max_seqlen
     """Attention of prompts packed one behind the other, over their own rows:
     out/query [T, Hq, D], key/value [T, Hkv, D] (equal row strides, e.g. views
     into one QKV buffer), cu_seqlens int32 [S+1].  ``max_seqlen`` is the host
-    upper bound of the lengths; rows past cu_seqlens[S] are left alone."""
+    upper bound of the lengths (0: nothing to do); rows past cu_seqlens[S] are
+    left alone."""
     lib = lib or _lib or library()
     t, hq, d = query.shape
     shape, dtype, n, dev = key.shape, query.dtype, cu_seqlens.numel(), query.get_device()

@@ -9,7 +9,7 @@ import torch
 import test_gpu_attention_varlen as varlen
 import test_gpu_decode_shared as shared
 from engine_builds import first_copy, reach, shared_build, varlen_build
-from gpu_util import gpu, require_gpu
+from gpu_util import gpu, pa, require_gpu
 
 pytestmark = gpu
 
@@ -139,3 +139,20 @@ def test_the_largest_planned_batch():
     assert len(x["ctx_list"]) == 10211
     shared.run(x)
     shared.verify(x, seqs=[0, 1, 31, 4999, 5000, 5001, 8192, 10199, 10200, 10210])
+
+
+def test_a_bound_of_zero_means_nothing_to_do():
+    # nothing is launched: no row written, cu_seqlens not looked at; any other
+    # bound that is too short is reported
+    require_gpu()
+    x = varlen.make([5, 40], 4, 2, 64, BF16, seed=27)
+    for bound, err in ((0, 0), (1, pa.DEVERR_CU_SEQLENS)):
+        varlen.run(x, max_seqlen=bound)
+        torch.cuda.synchronize()
+        assert int(x["err"]) == err
+        assert bool((x["wide"] == -3.0).all())
+    x["cu"].fill_(-9)
+    x["err"].zero_()
+    varlen.run(x, max_seqlen=0)
+    torch.cuda.synchronize()
+    assert int(x["err"]) == 0
