@@ -637,6 +637,8 @@ def pa_decode_shared(out, query, key_cache, value_cache, block_table, context_le
             and value_cache.get_device() == dev and block_table.get_device() == dev
             and (workspace is None or workspace.get_device() == dev)):
         _bad_device("out, caches, block_table or workspace", dev)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     if d_error is not None:
         _check_error(d_error, dev)
     _current(dev)

@@ -1,7 +1,9 @@
 """Refusals of the serving-step operators that are decided on the host, on the
 CPU (no pointer here is ever dereferenced; see also the operators' own files)."""
 import pytest
+import torch
 
+import paged_kv_cache_34_gb300 as pa
 import test_attention_varlen_host as varlen
 import test_decode_shared_host as shared
 from test_attention_varlen_host import lib  # noqa: F401  (fixture)
@@ -26,3 +28,15 @@ def test_decode_shared_plan_refuses_batches_that_the_call_refuses(lib, d, most):
     assert shared.call(lib, s=most, d=d, bs=8, qs=8 * d, os=8 * d, mc=16, mp=16) != 3
     # without a prefix it is the plain decode, whose limit is its own
     assert lib.pa_decode_shared_plan(most + 1, 0, 8, 2, d, 16, 16, None) != 3
+
+
+@pytest.mark.parametrize("workspace", [torch.zeros(1, dtype=torch.uint8).expand(1 << 20),
+                                       torch.zeros(1 << 12, dtype=torch.uint8)[::2]])
+def test_decode_shared_refuses_a_workspace_that_is_not_its_bytes(workspace):
+    # its size counts elements: an expanded or strided one has other bytes behind it
+    i = lambda *n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+    q, pool = torch.zeros(3, 8, 64), torch.zeros(9, 16, 2, 64)
+    q, pool = q.bfloat16(), pool.bfloat16()
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        pa.pa_decode_shared(q, q, pool, pool, i(3, 4), i(3), i(3), i(2), scale=1.0,
+                            max_context_len=8, max_prefix_len=4, workspace=workspace)
