@@ -277,6 +277,15 @@ def _current(dev):
         raise ValueError("the tensors must be on the current CUDA device")
 
 
+def _bound(v, name):
+    """A host bound as the C int32 it is passed as (ctypes would wrap a larger
+    one: 2**32 to 0, nothing to do)."""
+    v = int(v)
+    if not 0 <= v <= 0x7fffffff:
+        raise ValueError(f"{name} must be between 0 and 2**31 - 1")
+    return v
+
+
 def _raw_stream(stream, dev):
     """The cudaStream_t of `stream`, or of the current stream (without building
     a stream object, which takes 3 us)."""
@@ -570,12 +579,13 @@ def pa_attention_varlen(out, query, key, value, cu_seqlens, *, scale, max_seqlen
     if not (out.get_device() == dev and key.get_device() == dev and value.get_device() == dev
             and cu_seqlens.get_device() == dev):
         _bad_device("out, key, value or cu_seqlens", dev)
+    max_seqlen = _bound(max_seqlen, "max_seqlen")
     if d_error is not None:
         _check_error(d_error, dev)
     _current(dev)
     st = lib.pa_attention_varlen(out.data_ptr(), os, query.data_ptr(), qs, key.data_ptr(),
                                  value.data_ptr(), ks, cu_seqlens.data_ptr(), n - 1, t,
-                                 int(max_seqlen), hq, shape[1], d, float(scale),
+                                 max_seqlen, hq, shape[1], d, float(scale),
                                  1 if causal else 0, _DTYPE[dtype],
                                  None if d_error is None else d_error.data_ptr(),
                                  _raw_stream(stream, dev))
@@ -590,7 +600,8 @@ def pa_decode_shared_plan(num_seqs, num_groups, num_q_heads, num_kv_heads, head_
     lib = lib or library()
     ws = ctypes.c_size_t(0)
     st = lib.pa_decode_shared_plan(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim,
-                                   int(max_context_len), int(max_prefix_len), ctypes.byref(ws))
+                                   _bound(max_context_len, "max_context_len"),
+                                   _bound(max_prefix_len, "max_prefix_len"), ctypes.byref(ws))
     _check(lib, st, "pa_decode_shared_plan")
     return ws.value
 
@@ -637,6 +648,8 @@ def pa_decode_shared(out, query, key_cache, value_cache, block_table, context_le
             and value_cache.get_device() == dev and block_table.get_device() == dev
             and (workspace is None or workspace.get_device() == dev)):
         _bad_device("out, caches, block_table or workspace", dev)
+    max_context_len = _bound(max_context_len, "max_context_len")
+    max_prefix_len = _bound(max_prefix_len, "max_prefix_len")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     if d_error is not None:
@@ -651,7 +664,7 @@ def pa_decode_shared(out, query, key_cache, value_cache, block_table, context_le
         out.data_ptr(), os, query.data_ptr(), qs, key_cache.data_ptr(), value_cache.data_ptr(),
         block_table.data_ptr(), stride if s > 1 else width, width, context_lens.data_ptr(),
         group_starts.data_ptr(), prefix_lens.data_ptr(), g, s, hq, hkv, d, bs, nb, float(scale),
-        int(max_context_len), int(max_prefix_len), workspace.data_ptr(),
+        max_context_len, max_prefix_len, workspace.data_ptr(),
         workspace.nbytes, _DTYPE[dtype], None if d_error is None else d_error.data_ptr(),
         _raw_stream(stream, dev))
     if st:

@@ -40,3 +40,21 @@ def test_decode_shared_refuses_a_workspace_that_is_not_its_bytes(workspace):
     with pytest.raises(ValueError, match="workspace must be contiguous"):
         pa.pa_decode_shared(q, q, pool, pool, i(3, 4), i(3), i(3), i(2), scale=1.0,
                             max_context_len=8, max_prefix_len=4, workspace=workspace)
+
+
+@pytest.mark.parametrize("bound", [-1, 1 << 31, 1 << 32, (1 << 32) + 64, (1 << 63) - 1])
+def test_host_bounds_beyond_32_bits_are_refused(bound):
+    # passed on as they are, 2**32 would be 0: nothing to do, without a word
+    i = lambda *n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+    q, pool = torch.zeros(3, 8, 64).bfloat16(), torch.zeros(9, 16, 2, 64).bfloat16()
+    kv = torch.zeros(3, 2, 64).bfloat16()
+    with pytest.raises(ValueError, match="max_seqlen must be"):
+        pa.pa_attention_varlen(q, q, kv, kv, i(2), scale=1.0, max_seqlen=bound)
+    for name in ("max_context_len", "max_prefix_len"):
+        bounds = dict(max_context_len=8, max_prefix_len=4)
+        bounds[name] = bound
+        with pytest.raises(ValueError, match=name + " must be"):
+            pa.pa_decode_shared(q, q, pool, pool, i(3, 4), i(3), i(3), i(2), scale=1.0, **bounds)
+        with pytest.raises(ValueError, match=name + " must be"):
+            pa.pa_decode_shared_plan(3, 2, 8, 2, 64, bounds["max_context_len"],
+                                     bounds["max_prefix_len"])
