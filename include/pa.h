@@ -591,7 +591,11 @@ pa_status pa_build_tables(int32_t *block_table, int64_t block_table_stride,
  *                cu_seqlens[num_seqs] on (padding) are not read as keys and
  *                their out rows are left as they were; they may hold
  *                anything.
- *   max_seqlen   host upper bound of the sequences' lengths.
+ *   max_seqlen   host upper bound of the sequences' lengths.  It also chooses
+ *                the kernel's build, so a tighter bound can be faster (30
+ *                prompts of 100 tokens, 8/2 heads: 11.9 us with 100, 14.7 with
+ *                131072; 16 of 1000, 32/32: 143 and 155); total_tokens sizes
+ *                the launch.
  * With num_seqs, total_tokens or max_seqlen 0 the host has said that there is
  * nothing to attend to: nothing is launched, cu_seqlens is not read (so no
  * error bit is set for it) and out is left as it was.  Otherwise a cu_seqlens

@@ -893,7 +893,12 @@ pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *que
   // 23.0), which pairs take half of: more items of few keys cost more than they
   // even out (30 x 100 tokens 8/2, 1.6 rounds: 14.7 and 11.7), and so do more
   // rounds, that load K and V for every tile (8000 tokens 16/4, 6.6: 210 and 167;
-  // 4 x 1000 32/32, 6.7: 52 and 48).
+  // 4 x 1000 32/32, 6.7: 52 and 48).  "Longer" goes by the bound, the host's only
+  // sign of a batch's longest prompt: by twice the mean length, loose bounds cost
+  // nothing (30 x 100 8/2 with a bound of 131072: 12.2 us, by the bound 14.7), but
+  // batches of one long prompt and many short ones do (2000 + 20 x 30 tokens 8/2:
+  // 37.4 against 25.7; 8000 + 20 x 200 32/8, with the compact softmax: 394 against
+  // 352).
   const int64_t rounds = max_seqlen >= 640 ? 4 : 1;
   if (items(1) <= rounds * a.num_sms) {
     a.tiles = 1;
