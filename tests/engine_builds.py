@@ -32,13 +32,35 @@ def varlen_build(num_seqs, total, max_seqlen, hq, hkv):
 
 def shared_build(num_seqs, num_groups, max_prefix, hq, hkv):
     pg = packed_heads(hq // hkv)
-    tpt = 128 // pg
-    if num_seqs <= tpt:
+    if num_seqs <= 128 // pg:
         return "single"
-    cost = (num_seqs // tpt + num_groups) * (hq // pg) * -(-max_prefix // 128)
-    most = sms() // 2 if cost <= 6 * sms() else sms()
-    runs = max(1, min((cost + 1) // 2, most))
+    cost, runs = shared_runs(num_seqs, num_groups, max_prefix, hq, hkv)
     return "compact" if cost <= 64 * runs else "pairs"
+
+
+def shared_runs(num_seqs, num_groups, max_prefix, hq, hkv):
+    """(the most the prefix pass can cost, its runs) of a batch of tile pairs."""
+    pg = packed_heads(hq // hkv)
+    cost = (num_seqs // (128 // pg) + num_groups) * (hq // pg) * -(-max_prefix // 128)
+    most = sms() // 2 if cost <= 6 * sms() else sms()
+    return cost, max(1, min((cost + 1) // 2, most))
+
+
+def runs_with_two_rows_of_a_pair(start, tiles, line, run):
+    """How many of the prefix pass's runs (of `run` cost) hold tiles of one pair of
+    query tiles from two blocks of a line of `line` K/V tiles, in a group of
+    `tiles` query tiles that starts at cost position `start`."""
+    ks = min(line, run if tiles == 3 else (run + 1) // 2)
+    held = {}
+    for blk in range(-(-line // ks)):
+        n = min(ks, line - blk * ks)
+        at = start + blk * ks * tiles
+        for q in range((tiles + 1) // 2):
+            w = 2 if 2 * q + 1 < tiles else 1
+            for i in range(n):
+                held.setdefault(((at + w * i) // run, q), set()).add(blk)
+            at += w * n
+    return sum(len(b) > 1 for b in held.values())
 
 
 def reach(x, build):
