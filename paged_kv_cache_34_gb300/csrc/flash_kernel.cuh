@@ -392,12 +392,14 @@ __device__ inline bool check_cu(const Params &p, int lane) {
 // are then a block's pairs over the same K and V, which come from memory once
 // (256 sequences over 32768 tokens, 64/8 heads, 8 pairs: 142 MB read where whole
 // lines one after the other read 850, the pass 170 us against 198).  Two query
-// tiles or less are one pair, whose line is one block.  A run holds no two rows of
-// one pair: three tiles' other row is a run long with blocks of C.
+// tiles or less are one pair, whose line is one block.  Of full blocks a run holds
+// no two rows of one pair (three tiles' other row is a run long with blocks of C);
+// where a line's last block is shorter, a run may.
 //
 // A work item is a row's tiles of one head unit in one run; its states start at
-// a workspace row that grows along the line by at least its rows (item_row) plus
-// 256 per run, so no two items share one.  Warp-collective.
+// a workspace row that grows along the line by at least its rows (item_row, which
+// counts every block) plus 256 per run, so no two items share one, nor do a
+// pair's rows of two blocks in one run.  Warp-collective.
 struct GroupGeom {
   int first, n, nkt, prefix, cost;
 };
