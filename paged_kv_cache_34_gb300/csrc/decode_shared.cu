@@ -31,15 +31,16 @@ namespace {
 // kJoinBatch at a time with every load in flight, and the warps' results are
 // folded in shared memory.  Little code, it starts from a cold instruction
 // cache: one loop over both parts' states took 62 us where this takes 58 on
-// 64 sequences in 6 groups, and the block search for every group 30.0 where the
-// build without it takes @@ on 32 sequences over 4000 tokens.
+// 64 sequences in 6 groups, and with the block search, where no group needs it,
+// 4 sequences over 500 tokens take 18.7 against 15.8 (32 over 4000: 37.5 and 37.3).
 constexpr int kJoinWarps = 4;
 constexpr int kJoinBatch = 4;
 // Four warps to a row where the own parts' workers are this many to a unit (a
 // sequence and KV head), so that a row can have a batch of states for each warp
-// (4 sequences of 8000 own tokens, 8/2 heads: 19.4 us for the call, with one
-// warp 35.4); else one (8 sequences behind 16384 tokens, 32/32 heads: 64.2 us,
-// with four 65.2; 256 behind 32768, 64/8: 296 and 345).
+// (4 sequences of 8000 own tokens, 8/2 heads, 152 workers a unit: 19.8 us for the
+// call, with one warp 36.1; 32 of up to 3000, 8/1, 38: 21.0 and 32.6; 8 of 500,
+// 32/8, 19: 20.1 and 21.7); else one (32 of up to 1000, 32/8, 4.8: 37.3, with four
+// 36.8; 64 of 500, 64/8, 2.4: 55.6 and 69.6; 256 of them, 0.6: 173 and 225).
 constexpr int kJoinWideStates = 16;
 
 // BLOCKS: a group may have more than two query tiles.
@@ -205,9 +206,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 }
 
 // Up to this cost per run (of what the batch may cost at most) the prefix pass
-// takes the compact softmax: it starts and ends items more than it runs (64
-// sequences in 6 groups: 54.7 us against 56.3; 256 over 32768 tokens: 311
-// against 295).
+// takes the compact softmax: it starts and ends items more than it runs (64/8
+// heads, compact and unrolled: 64 sequences in 6 groups over 5000 tokens, cost 21 a
+// run: 58.2 and 59.6 us; 64 over 10000, 21: 61.9 and 63.1; 64 over 20000, 41: 71.7
+// and 72.4; 256 over 10000, 71: 158.0 and 156.6; 64 over 40000, 82: 96.0 and 95.3;
+// 256 over 40000, 280: 299 and 287; of many groups or heads the compact one stays
+// ahead by 1 %: 200 in 10 over 20000, 32/8, 132: 190.7 and 192.1).
 constexpr int64_t kCompactCost = 64;
 
 template <class E, int D>

@@ -248,15 +248,21 @@ inline int64_t shared_cost(int num_seqs, int num_groups, int num_q_heads, int nu
 }
 
 // The own parts start on the SMs that the prefix pass leaves free, so a pass of
-// a few tiles per SM, which is mostly start-up, takes half of the SMs (32
-// sequences over 4000 tokens: 27.5 us against 29.8 with all of them).  Of longer
-// passes, one of single query tiles waits for memory, which fewer SMs keep as
-// busy: it takes the largest power of two, 128 of 152, whose runs also end
-// where heads do when tiles and heads are powers of two (8 sequences over 16384
-// tokens, 32/32 heads: 57.6 us, with 152 / 136 / 116 SMs 64.9 / 63.4 / 63.4;
-// 16 over 32768, 32/8: 53.1, with 152 54.4).  One of tile pairs waits for the
-// tensor cores and takes them all (256 sequences over 32768 tokens: 296 us,
-// with 16 fewer 306, with half 386).
+// a few tiles per SM, which is mostly start-up, takes half of the SMs (32/8 heads,
+// with half and with all: 32 sequences over 2000 tokens 35.4 and 35.9 us, over 4000
+// 37.4 and 42.3, over 6000 39.0 and 43.4; 16 over 9000 30.7 and 36.6; 64 over 1000,
+// 64/8: 55.7 and 59.9; but 40 over 4000, 16/16, with many own parts for few tiles:
+// 64.5 and 60.7).  Of longer passes, one of single query tiles waits for memory,
+// which fewer SMs keep as busy while the own parts start on the rest: it takes the
+// largest power of two, 128 of 152 (with 128 and with 152: 8 sequences, 32/8 heads,
+// over 9000 / 20000 / 32768 / 50000 tokens 20.9, 24.3 / 26.4, 30.3 / 38.7, 44.4 /
+// 52.3, 54.8; 16, 40/8, over 9000 / 20000 / 50000 27.0, 28.3 / 34.9, 36.7 / 58.3,
+// 59.6; 8, 40/40, over 9000 / 20000 / 50000 50.0, 53.6 / 83.7, 84.5 / 172.2, 171.4;
+// 32/32 over 9000 / 20000 / 50000 46.9, 46.8 / 71.1, 71.8 / 143.5, 140.6; 112 and 140
+// SMs lie in between).  Where tiles and heads are powers of two its runs also end
+// where heads do (8 over 16384, 32/32: 57.5 and 63.0; over 16400: 61.8 and 63.9).
+// One of tile pairs waits for the tensor cores and takes them all (256 sequences
+// over 32768 tokens: 296 us, with 16 fewer 306, with half 386).
 inline int shared_runs(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
                        int max_prefix, int num_sms) {
   const int64_t cost =
