@@ -661,8 +661,9 @@ pa_status pa_attention_varlen(void *out, int64_t out_row_stride, const void *que
  * Supported: num_seqs * num_kv_heads * max_context_len < 2^30 (a GQA group of
  * more than 16 heads counts once per 16) and bounds < 2^30; up to 10211
  * sequences at head_dim 128, 14393 at 64 (12 bytes each in shared memory; the
- * plan refuses what the call would refuse for it); 16-bit pools; head_dim 64 or 128; block_size 8, 16, 32, 64 or 128; any num_q_heads %
- * num_kv_heads == 0.
+ * plan refuses what the call would refuse for it); 16-bit pools; head_dim 64
+ * or 128; block_size 8, 16, 32, 64 or 128; any num_q_heads % num_kv_heads ==
+ * 0.
  */
 pa_status pa_decode_shared_plan(int32_t num_seqs, int32_t num_groups, int32_t num_q_heads,
                                 int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
