@@ -22,7 +22,7 @@
 //
 // Bound by latency, not by bytes: launch, lengths, sums, search, block ids,
 // stores follow one another.  Measured (graph replay, GB300): 3.0 us for one
-// token of one request, 4.7 us for 1024 requests of 16 tokens, 11.0 us for
+// token of one request, 4.7 us for 1024 requests of 16 tokens, 11.2 us for
 // 1024 prompts of up to 2000 tokens (a million in all, 12.6 MB written).  Two
 // CTAs per SM at most, in several steps: a third repeats the sums more often
 // and takes registers from the token loop (1024 x 1000 tokens: 12.4 us against

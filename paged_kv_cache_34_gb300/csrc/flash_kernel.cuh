@@ -12,8 +12,10 @@
 // result exact up to rounding.  Scores, sums and O are fp32; the weights are
 // rounded to the input's 16-bit type for the tensor core, and the sum takes
 // them in fp32 before that.  (Summing the rounded values, which makes o_i an
-// exact mean under them, costs two instructions a weight instead of a half:
-// 16384 tokens 32/8 heads 1680 against 1770 TFLOP/s.)
+// exact mean under them, costs one or two instructions a weight instead of a half:
+// 16384 tokens 32/8 heads 1390 us against 1285, 16 x 1000 32/32 146 against 144.  On
+// values far from 0, with a mean of 4, the error is by 0.5 % smaller then as a root
+// mean square, by 20 % at its largest; on centred ones by 1 % and 0.)
 //
 // What bounds it.  Per 128 x 128 tile step at head_dim 128 the tensor core
 // needs 1024 cycles (16 MMAs of 64), the softmax of one warpgroup about as
@@ -40,9 +42,10 @@
 //    shared between launches.
 //
 // Measured (causal, head_dim 128, rates of the visible pairs; a 16-bit library
-// product reaches 1945 TFLOP/s): 16384 tokens 32/8 heads 1800 TFLOP/s, 4 x 4096
-// 32/8 1540, 24 prompts of up to 2700 tokens 40/8 1170, 16 of up to 2000 32/32
-// 1000, 16 x 1000 32/32 910; head_dim 64, 8192 tokens 1010.  Prefix pass: 256
+// product reaches 1945 TFLOP/s): 16384 tokens 32/8 heads 1650 to 1790 TFLOP/s (by
+// the card's power), 4 x 4096 32/8 1540, 24 prompts of up to 2700 tokens 40/8 1170, 16 of up to 2000 32/32
+// 1000, 16 x 1000 32/32 910; not causal 1730, 1670, -, 1240, 1210; head_dim 64, 8192
+// tokens 1020, where the softmax bounds it.  Prefix pass: 256
 // sequences x 64/8 heads over 32768 tokens 1640 (170 us).  In the long run a
 // step's length is one stream's chain (softmax and its own MMAs, 2400 cycles,
 // 2048 of them with the tensor core busy); around items, where both streams'
