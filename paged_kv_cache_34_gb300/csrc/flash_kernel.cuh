@@ -43,9 +43,9 @@
 //
 // Measured (causal, head_dim 128, rates of the visible pairs; a 16-bit library
 // product reaches 1945 TFLOP/s): 16384 tokens 32/8 heads 1650 to 1790 TFLOP/s (by
-// the card's power), 4 x 4096 32/8 1540, 24 prompts of up to 2700 tokens 40/8 1170, 16 of up to 2000 32/32
-// 1000, 16 x 1000 32/32 910; not causal 1730, 1670, -, 1240, 1210; head_dim 64, 8192
-// tokens 1020, where the softmax bounds it.  Prefix pass: 256
+// the card's power), 4 x 4096 32/8 1540, 24 prompts of up to 2700 tokens 40/8 1170,
+// 16 of up to 2000 32/32 1000, 16 x 1000 32/32 910; not causal 1730, 1670, -, 1240,
+// 1210; head_dim 64, 8192 tokens 1020, where the softmax bounds it.  Prefix pass: 256
 // sequences x 64/8 heads over 32768 tokens 1640 (170 us).  In the long run a
 // step's length is one stream's chain (softmax and its own MMAs, 2400 cycles,
 // 2048 of them with the tensor core busy); around items, where both streams'
