@@ -103,6 +103,7 @@ typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1 } pa_dtype;
 #define PA_DEVERR_TIMEOUT 16   /* a bounded pipeline wait gave up             */
 #define PA_DEVERR_SCALE 32     /* an 8-bit pool's scale not positive finite   */
 #define PA_DEVERR_NO_BLOCKS 64 /* the free list is too short for the step     */
+#define PA_DEVERR_POSITION 128 /* a position outside the rotation's table      */
 
 /* ABI version the library was built with (PA_ABI_VERSION). */
 int32_t pa_abi_version(void);
@@ -142,6 +143,58 @@ pa_status pa_reshape_and_cache(const void *key, const void *value,
                                int32_t head_dim, int32_t block_size,
                                int64_t num_blocks, pa_dtype dtype,
                                int32_t *d_error, void *stream);
+
+/*
+ * pa_rope_and_cache -- norm and position rotation of a step's query and key
+ * heads, and the write of its keys and values into the pools, in one pass.
+ *
+ * Defines: for token t at position p = positions[t], a query or key head's row
+ * x of D = head_dim values becomes, in fp32 and rounded once at the end,
+ *     y = x * w / sqrt(mean(x^2) + eps)   where its weight w is given, else x;
+ *     y_a, y_b -> y_a c_i - y_b s_i, y_b c_i + y_a s_i     for i < R/2,
+ *         (a, b) = (i, i + R/2), or (2i, 2i + 1) when interleaved,
+ *         c_i = cos_sin[p][i], s_i = cos_sin[p][R/2 + i], R = rot_dim;
+ * elements from R on keep y.  The query rows go to query_out; the key rows go to
+ * pool row slot_mapping[t] ([SKILL] §3.1, §3.3) and, where it is given, to
+ * key_out; the value rows go to the pool as they are.  It is
+ * pa_reshape_and_cache with what comes before it: the same slots (a negative one
+ * writes nothing to the pools; one past them sets PA_DEVERR_SLOT), and the row
+ * written is the row pa_reshape_and_cache would write from key_out.
+ *
+ *   query_out    [num_tokens, num_q_heads, head_dim] at q_out_row_stride; may be
+ *                query itself (the same rows at the same stride).
+ *   key_out      [num_tokens, num_kv_heads, head_dim] at k_out_row_stride;
+ *                nullable; may be key itself.
+ *   query        [num_tokens, num_q_heads, head_dim] at q_row_stride.
+ *   key, value   [num_tokens, num_kv_heads, head_dim], both at kv_row_stride
+ *                (all three may be views into one QKV buffer).
+ *   positions    int32 [num_tokens] (pa_build_tables writes them).
+ *   cos_sin      fp32 [max_position, rot_dim]: rot_dim/2 cosines, then as many
+ *                sines.  A position outside it sets PA_DEVERR_POSITION, and that
+ *                token is skipped: its output rows and its pool row stay.
+ *   rot_dim      a multiple of 16 up to head_dim; 0: no rotation (positions and
+ *                cos_sin are not read).
+ *   q_weight,
+ *   k_weight     [head_dim] of dtype, each nullable: no norm of those heads.
+ *   eps          finite, not negative; of the norms.
+ *   key_cache,
+ *   value_cache,
+ *   slot_mapping all NULL: nothing is written to a cache (then key_out is
+ *                required, and value, block_size and num_blocks are not used).
+ * Outputs may not overlap inputs or each other otherwise (PA_ERR_SHAPE); columns
+ * of one buffer's rows side by side are no overlap.
+ * Supported: fp16 / bf16, head_dim 64 or 128, any numbers of heads and any
+ * block_size.
+ */
+pa_status pa_rope_and_cache(void *query_out, int64_t q_out_row_stride, void *key_out,
+                            int64_t k_out_row_stride, const void *query, int64_t q_row_stride,
+                            const void *key, const void *value, int64_t kv_row_stride,
+                            const int32_t *positions, const float *cos_sin, int64_t max_position,
+                            int32_t rot_dim, int32_t interleaved, const void *q_weight,
+                            const void *k_weight, float eps, void *key_cache, void *value_cache,
+                            const int64_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                            int64_t num_blocks, pa_dtype dtype, int32_t *d_error, void *stream);
 
 /*
  * pa_decode_plan -- the split-KV plan pa_decode will use.

@@ -8,6 +8,8 @@ library's kernels.  There is no CPU fallback: without the built library the
 first call raises.
 
     pa_reshape_and_cache  new K/V rows -> pool rows given by slot_mapping
+    pa_rope_and_cache     norm and rotation of query and key heads, and the cache write
+    pa_qk_norm_rope       the same without a cache
     pa_decode             one query per sequence, split-KV + LSE combine
     pa_prefill_varlen     causal attention for cu_seqlens-packed queries
     pa_reshape_and_cache_int8, pa_decode_int8, pa_decode_write_int8 (and _fp8)
@@ -28,14 +30,14 @@ import threading
 
 import torch
 
-__all__ = ["pa_reshape_and_cache", "pa_decode", "pa_decode_plan", "pa_decode_write",
+__all__ = ["pa_reshape_and_cache", "pa_rope_and_cache", "pa_qk_norm_rope", "pa_decode", "pa_decode_plan", "pa_decode_write",
            "pa_prefill_varlen", "pa_reshape_and_cache_int8", "pa_decode_int8",
            "pa_decode_write_int8", "pa_reshape_and_cache_fp8", "pa_decode_fp8",
            "pa_decode_write_fp8", "pa_copy_blocks", "pa_build_tables",
            "pa_attention_varlen", "pa_decode_shared", "pa_decode_shared_plan", "PaError",
            "library", "DEVERR_SLOT", "DEVERR_BLOCK_ID", "DEVERR_CU_SEQLENS",
            "DEVERR_CONTEXT", "DEVERR_TIMEOUT", "DEVERR_SCALE", "DEVERR_NO_BLOCKS",
-           "LIB_PATH"]
+           "DEVERR_POSITION", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpa.so")
 
@@ -43,6 +45,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpa.so")
 DEVERR_SLOT, DEVERR_BLOCK_ID, DEVERR_CU_SEQLENS, DEVERR_CONTEXT, DEVERR_TIMEOUT = 1, 2, 4, 8, 16
 DEVERR_SCALE = 32
 DEVERR_NO_BLOCKS = 64
+DEVERR_POSITION = 128
 
 _STATUS = {0: "PA_OK", 1: "PA_ERR_NULL", 2: "PA_ERR_SHAPE", 3: "PA_ERR_UNSUPPORTED",
            4: "PA_ERR_ALIGN", 5: "PA_ERR_WORKSPACE", 6: "PA_ERR_CUDA"}
@@ -81,6 +84,10 @@ def library(path: str | None = None):
         lib.pa_reshape_and_cache.argtypes = [V, V, I64, V, V, V, I32, I32, I32, I32, I64,
                                              c.c_int, V, V]
         lib.pa_reshape_and_cache.restype = c.c_int
+        lib.pa_rope_and_cache.argtypes = [V, I64, V, I64, V, I64, V, V, I64, V, V, I64, I32, I32, V,
+                                          V, F, V, V, V, I32, I32, I32, I32, I32, I64, c.c_int, V,
+                                          V]
+        lib.pa_rope_and_cache.restype = c.c_int
         lib.pa_decode_plan.argtypes = [I32, I32, I32, I32, I32, I32,
                                        c.POINTER(I32), c.POINTER(SZ)]
         lib.pa_decode_plan.restype = c.c_int
@@ -174,6 +181,95 @@ def pa_reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, *,
                                   _ptr(value_cache), _ptr(slot_mapping), key.shape[0], hkv, d,
                                   bs, nb, _DTYPE[key.dtype], _ptr(d_error), _stream(stream))
     _check(lib, st, "pa_reshape_and_cache")
+
+
+def _rope(what, query_out, key_out, query, key, value, key_cache, value_cache, slot_mapping,
+          positions, cos_sin, interleaved, q_weight, k_weight, eps, d_error, stream, lib):
+    lib = lib or _lib or library()
+    t, hq, d = query.shape
+    tk, hkv, dk = key.shape
+    dtype, dev = query.dtype, query.get_device()
+    if query_out.shape != query.shape or tk != t or dk != d:
+        raise ValueError("query_out/query must be [T, Hq, D] and key [T, Hkv, D]")
+    if dtype not in _DTYPE or query_out.dtype is not dtype or key.dtype is not dtype:
+        raise ValueError("query_out, query and key must share a dtype, float16 or bfloat16")
+    if query_out.get_device() != dev or key.get_device() != dev:
+        _bad_device("query_out or key", dev)
+    os, qs, ks = _rows(query_out, "query_out"), _rows(query, "query"), _rows(key, "key")
+    kos = ko = v = kc = vc = sm = pos = cs = qw = kw = None
+    rot = most = bs = nb = 0
+    if key_out is not None:
+        if key_out.shape != key.shape or key_out.dtype is not dtype:
+            raise ValueError("key_out must be like key")
+        if key_out.get_device() != dev:
+            _bad_device("key_out", dev)
+        kos, ko = _rows(key_out, "key_out"), key_out.data_ptr()
+    if key_cache is not None:
+        nb, bs, hc, dc = key_cache.shape
+        if value.shape != key.shape or value.dtype is not dtype or _rows(value, "value") != ks:
+            raise ValueError("value must be like key, with its row stride")
+        if hc != hkv or dc != d or value_cache.shape != key_cache.shape \
+                or key_cache.dtype is not dtype or value_cache.dtype is not dtype \
+                or not key_cache.is_contiguous() or not value_cache.is_contiguous():
+            raise ValueError("caches must be contiguous [num_blocks, block_size, Hkv, D] of key's "
+                             "dtype")
+        if not (value.get_device() == dev and key_cache.get_device() == dev
+                and value_cache.get_device() == dev):
+            _bad_device("value or caches", dev)
+        if slot_mapping.dtype is not torch.int64 or slot_mapping.numel() != t \
+                or slot_mapping.get_device() != dev or not slot_mapping.is_contiguous():
+            _bad_vector(slot_mapping, t, torch.int64, "slot_mapping", dev)
+        v, kc, vc = value.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr()
+        sm = slot_mapping.data_ptr()
+    if cos_sin is not None:
+        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous float32 tensor [max_position, rot_dim]")
+        if cos_sin.get_device() != dev:
+            _bad_device("cos_sin", dev)
+        if positions.dtype is not torch.int32 or positions.numel() != t \
+                or positions.get_device() != dev or not positions.is_contiguous():
+            _bad_vector(positions, t, torch.int32, "positions", dev)
+        most, rot = cos_sin.shape
+        pos, cs = positions.data_ptr(), cos_sin.data_ptr()
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.dtype is not dtype or w.numel() != d or not w.is_contiguous()
+                              or w.get_device() != dev):
+            _bad_vector(w, d, dtype, name, dev)
+    if d_error is not None:
+        _check_error(d_error, dev)
+    _current(dev)
+    st = lib.pa_rope_and_cache(
+        query_out.data_ptr(), os, ko, kos or 0, query.data_ptr(), qs, key.data_ptr(), v, ks, pos,
+        cs, most, rot, 1 if interleaved else 0, None if q_weight is None else q_weight.data_ptr(),
+        None if k_weight is None else k_weight.data_ptr(), eps, kc, vc, sm, t, hq, hkv, d, bs, nb,
+        _DTYPE[dtype], None if d_error is None else d_error.data_ptr(), _raw_stream(stream, dev))
+    if st:
+        _check(lib, st, what)
+
+
+def pa_rope_and_cache(query_out, query, key, value, key_cache, value_cache, slot_mapping, positions,
+                      cos_sin, *, key_out=None, interleaved=False, q_weight=None, k_weight=None,
+                      eps=1e-6, d_error=None, stream=None, lib=None):
+    """Norms (where weights [D] are given) and rotation of a step's query and
+    key heads, and its cache write, in one pass: query_out/query [T, Hq, D],
+    key/value [T, Hkv, D] (equal row strides), caches [NB, bs, Hkv, D],
+    slot_mapping int64 [T] (negative: no cache write), positions int32 [T],
+    cos_sin float32 [max_position, rot_dim] (cosines, then sines; None: no
+    rotation).  The pairs rotated are (i, i + rot_dim/2), or (2i, 2i + 1) when
+    ``interleaved``.  ``key_out`` also takes the key rows; query_out and
+    key_out may be query and key themselves."""
+    _rope("pa_rope_and_cache", query_out, key_out, query, key, value, key_cache, value_cache,
+          slot_mapping, positions, cos_sin, interleaved, q_weight, k_weight, eps, d_error, stream,
+          lib)
+
+
+def pa_qk_norm_rope(query_out, key_out, query, key, positions, cos_sin, *, interleaved=False,
+                    q_weight=None, k_weight=None, eps=1e-6, d_error=None, stream=None, lib=None):
+    """pa_rope_and_cache without a cache: norms and rotation of the query and
+    key heads into query_out [T, Hq, D] and key_out [T, Hkv, D] (query and key
+    themselves, for example)."""
+    _rope("pa_qk_norm_rope", query_out, key_out, query, key, None, None, None, None, positions,
+          cos_sin, interleaved, q_weight, k_weight, eps, d_error, stream, lib)
 
 
 def _scales(t, hkv, what):

@@ -269,6 +269,109 @@ pa_status pa_reshape_and_cache(const void *key, const void *value, int64_t kv_ro
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
+pa_status pa_rope_and_cache(void *query_out, int64_t q_out_row_stride, void *key_out,
+                            int64_t k_out_row_stride, const void *query, int64_t q_row_stride,
+                            const void *key, const void *value, int64_t kv_row_stride,
+                            const int32_t *positions, const float *cos_sin, int64_t max_position,
+                            int32_t rot_dim, int32_t interleaved, const void *q_weight,
+                            const void *k_weight, float eps, void *key_cache, void *value_cache,
+                            const int64_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                            int64_t num_blocks, pa_dtype dtype, int32_t *d_error, void *stream) {
+  const bool cache = key_cache || value_cache || slot_mapping;
+  if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || rot_dim < 0 ||
+      rot_dim > head_dim || max_position < 0 || !(eps >= 0.0f) || !isfinite(eps))
+    return PA_ERR_SHAPE;
+  if (cache && (block_size <= 0 || num_blocks < 0 || num_blocks > INT64_MAX / block_size))
+    return PA_ERR_SHAPE;
+  if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PA_OK;
+  if (!query_out || !query || !key || (!cache && !key_out)) return PA_ERR_NULL;
+  if (cache && (!key_cache || !value_cache || !slot_mapping || !value)) return PA_ERR_NULL;
+  if (rot_dim > 0 && (!positions || !cos_sin)) return PA_ERR_NULL;
+  const int64_t qrow = static_cast<int64_t>(num_q_heads) * head_dim;
+  const int64_t krow = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (q_row_stride < qrow || q_out_row_stride < qrow || kv_row_stride < krow ||
+      (key_out && k_out_row_stride < krow))
+    return PA_ERR_SHAPE;
+  // byte offsets of every row fit in 64 bits
+  const int64_t most = INT64_MAX / 4 / num_tokens;
+  if (q_row_stride > most || q_out_row_stride > most || kv_row_stride > most ||
+      (key_out && k_out_row_stride > most))
+    return PA_ERR_SHAPE;
+  if (q_row_stride % 8 || q_out_row_stride % 8 || kv_row_stride % 8 ||
+      (key_out && k_out_row_stride % 8))
+    return PA_ERR_ALIGN;
+  if (!aligned16(query_out) || !aligned16(key_out) || !aligned16(query) || !aligned16(key) ||
+      (cache && (!aligned16(value) || !aligned16(key_cache) || !aligned16(value_cache))) ||
+      !aligned16(q_weight) || !aligned16(k_weight) || (rot_dim && !aligned16(cos_sin)))
+    return PA_ERR_ALIGN;
+  if ((rot_dim && (reinterpret_cast<uintptr_t>(positions) & 3u)) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+    return PA_ERR_ALIGN;
+  // A row may be rewritten in place (same rows, same stride); other overlaps of
+  // rows that are read and rows that are written are refused.
+  struct Rows {
+    const void *p;
+    int64_t stride, row;
+  };
+  const int64_t last = num_tokens - 1;
+  auto apart = [&](const Rows &x, const Rows &y, bool in_place) {
+    if (!x.p || !y.p) return true;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    const uintptr_t ae = a + 2 * (last * x.stride + x.row), be = b + 2 * (last * y.stride + y.row);
+    if (a >= be || b >= ae) return true;
+    if (x.stride != y.stride && num_tokens > 1) return false;
+    if (in_place && a == b) return true;
+    // views side by side in the rows of one buffer
+    const uintptr_t s = 2 * static_cast<uintptr_t>(x.stride);
+    if (num_tokens == 1) return false;
+    const uintptr_t d = a < b ? (b - a) % s : s - (a - b) % s;  // y's columns behind x's
+    return d >= 2 * static_cast<uintptr_t>(x.row) && d + 2 * static_cast<uintptr_t>(y.row) <= s;
+  };
+  const Rows q_in = {query, q_row_stride, qrow}, k_in = {key, kv_row_stride, krow};
+  const Rows v_in = {cache ? value : nullptr, kv_row_stride, krow};
+  const Rows q_o = {query_out, q_out_row_stride, qrow}, k_o = {key_out, k_out_row_stride, krow};
+  if (!apart(q_in, q_o, true) || !apart(k_in, k_o, true) || !apart(q_in, k_o, false) ||
+      !apart(k_in, q_o, false) || !apart(v_in, q_o, false) || !apart(v_in, k_o, false) ||
+      !apart(q_o, k_o, false))
+    return PA_ERR_SHAPE;
+  pa::RopeArgs a;
+  a.query_out = query_out;
+  a.key_out = key_out;
+  a.q_out_row_stride = q_out_row_stride;
+  a.k_out_row_stride = k_out_row_stride;
+  a.query = query;
+  a.key = key;
+  a.value = value;
+  a.q_row_stride = q_row_stride;
+  a.kv_row_stride = kv_row_stride;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.max_position = max_position;
+  a.rot = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.key_cache = key_cache;
+  a.value_cache = value_cache;
+  a.slot_mapping = slot_mapping;
+  a.num_slots = cache ? num_blocks * block_size : 0;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.dtype = dtype;
+  a.d_error = d_error;
+  cudaError_t e = current_num_sms(&a.num_sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  e = pa::launch_rope_and_cache(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
 pa_status pa_copy_blocks(void *key_cache, void *value_cache, int64_t block_bytes,
                          int64_t num_blocks, const int64_t *block_mapping, int32_t num_pairs,
                          int32_t *d_error, void *stream) {

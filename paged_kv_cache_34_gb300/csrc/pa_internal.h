@@ -33,6 +33,29 @@ struct ReshapeArgs {
 };
 cudaError_t launch_reshape_and_cache(const ReshapeArgs &a, cudaStream_t stream);
 
+// pa_rope_and_cache; strides in elements.
+struct RopeArgs {
+  void *query_out, *key_out;  // key_out nullable with a cache
+  int64_t q_out_row_stride, k_out_row_stride;
+  const void *query, *key, *value;
+  int64_t q_row_stride, kv_row_stride;
+  const int32_t *positions;
+  const float *cos_sin;  // [max_position, rot]
+  int64_t max_position;
+  int32_t rot;  // rotated elements of a head, 0 for none
+  bool interleaved;
+  const void *q_weight, *k_weight;  // [head_dim], nullable: no norm
+  float eps;
+  void *key_cache, *value_cache;  // null: no write
+  const int64_t *slot_mapping;
+  int64_t num_slots;
+  int32_t num_tokens, num_q_heads, num_kv_heads, head_dim;
+  pa_dtype dtype;
+  int32_t *d_error;
+  int num_sms;
+};
+cudaError_t launch_rope_and_cache(const RopeArgs &a, cudaStream_t stream);
+
 struct CopyBlocksArgs {
   void *key_cache;
   void *value_cache;
