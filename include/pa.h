@@ -15,7 +15,10 @@
  * pa_decode_static_ws is pa_decode without a caller-supplied workspace.
  * pa_reshape_and_cache_int8 / pa_decode_int8 / pa_decode_write_int8 are the
  * write, the decode and the step over INT8 pools, the _fp8 calls the same
- * over FP8 (E4M3) pools; pa_copy_blocks copies whole blocks (copy-on-write).
+ * over FP8 (E4M3) pools, and the _fp4 calls over 4-bit pools, which
+ * pa_gather_cache_fp4 reads back as 16-bit rows; pa_copy_blocks copies whole
+ * blocks (copy-on-write).  pa_rope_and_cache is the write with what comes before
+ * it: the norms and the rotation of the step's query and key heads.
  * pa_build_tables forms a step's block tables, slots and cumulative lengths
  * from request lengths; pa_attention_varlen is the attention of packed
  * prompts straight from their K/V rows, without a cache; pa_decode_shared is
@@ -538,6 +541,125 @@ pa_status pa_decode_write_fp8(void *out, int64_t out_row_stride, const void *que
                               int32_t max_context_len, int32_t partition_size,
                               void *workspace, size_t workspace_bytes, pa_dtype dtype,
                               int32_t *d_error, void *stream);
+
+/*
+ * FP4 KV pools: 4.5 bits a value.
+ *
+ * The pages name no 4-bit format; this library's reading of their quantised
+ * cache takes the one the GPU converts natively.  A value is
+ *     code * scale * S,
+ * code an OCP E2M1 number (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives, 4
+ * bits), scale an E4M3 number (not negative) shared by a group of 16 consecutive
+ * elements of a head's row, and S the KV head's fp32 scale (k_scale[g],
+ * v_scale[g]; absmax / 2688 puts the largest value at the largest code and
+ * scale).  The write takes, in fp32 and rounded to nearest, for each group x
+ *     c = E4M3(max |x| / (6 S)) (at most 448),  w = value(c) S,
+ *     codes E2M1(x / w) (ties to the even code, at most 6),
+ * codes 0 where c is 0; NaN counts as 0.  S must be between 2^-64 and 2^64: one
+ * that is not sets PA_DEVERR_SCALE, its head's groups are written and read as
+ * zeros, and the decode gives that head's queries a zero output.
+ *
+ * A pool is uint8 [num_blocks, num_kv_heads, block_size / 8, 9 head_dim / 2]: the
+ * last dimension is a tile of eight tokens, first their codes, head_dim / 2
+ * bytes a token (element 2i in the low half of byte i, 2i + 1 in the high half),
+ * then their scales, head_dim / 16 bytes a token.  Token s % block_size of block
+ * s / block_size is slot s, as in the other pools, and pa_copy_blocks copies
+ * blocks of num_kv_heads * block_size * 9 / 16 * head_dim bytes.
+ * All calls: head_dim 64 or 128, block_size 8, 16, 32, 64 or 128, pools 16-byte
+ * aligned, k_scale and v_scale device fp32 [num_kv_heads].
+ */
+
+/*
+ * pa_reshape_and_cache_fp4 -- pa_reshape_and_cache into FP4 pools.
+ * Arguments and errors as for pa_reshape_and_cache_fp8.  Two tokens of one call may
+ * share a tile (not a slot).
+ */
+pa_status pa_reshape_and_cache_fp4(const void *key, const void *value, int64_t kv_row_stride,
+                                   void *key_cache, void *value_cache,
+                                   const int64_t *slot_mapping, int32_t num_tokens,
+                                   int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                   int64_t num_blocks, const float *k_scale, const float *v_scale,
+                                   pa_dtype dtype, int32_t *d_error, void *stream);
+
+/*
+ * pa_gather_cache_fp4 -- FP4 pools read back as 16-bit rows.
+ *
+ * Position j of sequence b, j < context_lens[b], goes to row row_starts[b] + j of
+ * key_out and value_out, all heads, rounded once from its value.  A chunk of a
+ * prompt over what an FP4 cache holds: write the chunk, gather, and attend with
+ * pa_prefill_varlen, whose 16-bit pools the rows are where each start is a
+ * multiple of its block size (block r of sequence b then starts at row
+ * row_starts[b] + r * block_size).
+ *
+ *   key_out,
+ *   value_out       [num_rows, num_kv_heads, head_dim] of dtype at their row
+ *                   strides; rows of no position are left as they were.  The rows
+ *                   of two sequences should not meet (one of them is kept).
+ *   context_lens,
+ *   row_starts      int32 [num_seqs].  A length that is negative, beyond the table
+ *                   or beyond max_context_len sets PA_DEVERR_CONTEXT, rows outside
+ *                   [0, num_rows) set PA_DEVERR_CU_SEQLENS: that sequence is
+ *                   skipped.  A bad block id sets PA_DEVERR_BLOCK_ID and its
+ *                   positions are skipped.
+ * Supported: up to 65535 sequences.  Nothing is launched where num_seqs or
+ * max_context_len is 0.
+ */
+pa_status pa_gather_cache_fp4(void *key_out, int64_t k_out_row_stride, void *value_out,
+                              int64_t v_out_row_stride, int32_t num_rows, const void *key_cache,
+                              const void *value_cache, const int32_t *block_table,
+                              int64_t block_table_stride, int32_t max_blocks_per_seq,
+                              const int32_t *context_lens, const int32_t *row_starts,
+                              int32_t num_seqs, int32_t max_context_len, int32_t num_kv_heads,
+                              int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                              const float *k_scale, const float *v_scale, pa_dtype dtype,
+                              int32_t *d_error, void *stream);
+
+/*
+ * pa_decode_fp4 -- pa_decode over FP4 pools.
+ *
+ * Scores and weighted sums are accumulated in fp32 from the products of codes and
+ * group scales, which fp16 holds exactly, and the query rounded to fp16 after a
+ * power of two that depends on its head (bf16 queries keep their range, as over
+ * the one-byte pools); the softmax weights are rounded to fp16.  A NaN in a query
+ * makes that (sequence, head) NaN.  Arguments and errors as for pa_decode_fp8,
+ * without its partition size.  The workspace (256-byte aligned) is of
+ * pa_decode_fp4_plan's size for the same shape; calls that may run at the same
+ * time need one each.
+ * Supported: any num_q_heads % num_kv_heads == 0; up to 16384 sequences;
+ * num_seqs * num_kv_heads * max_context_len < 2^30 (lengths rounded up to 16; a
+ * GQA group of more than 16 heads counts once per 16).  The plan refuses what
+ * the call would refuse for it.
+ */
+pa_status pa_decode_fp4_plan(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                             int32_t head_dim, int32_t max_context_len,
+                             size_t *workspace_bytes_out);
+
+pa_status pa_decode_fp4(void *out, int64_t out_row_stride, const void *query, int64_t q_row_stride,
+                        const void *key_cache, const void *value_cache, const int32_t *block_table,
+                        int64_t block_table_stride, int32_t max_blocks_per_seq,
+                        const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                        int64_t num_blocks, const float *k_scale, const float *v_scale, float scale,
+                        int32_t max_context_len, void *workspace, size_t workspace_bytes,
+                        pa_dtype dtype, int32_t *d_error, void *stream);
+
+/*
+ * pa_decode_write_fp4 -- one decode step over FP4 pools in one call:
+ * pa_reshape_and_cache_fp4(key, value, ..., slot_mapping, num_new_tokens, ...), then
+ * pa_decode_fp4 over the updated pools.  Every argument is checked before anything
+ * is enqueued.
+ */
+pa_status pa_decode_write_fp4(void *out, int64_t out_row_stride, const void *query,
+                              int64_t q_row_stride, const void *key, const void *value,
+                              int64_t kv_row_stride, void *key_cache, void *value_cache,
+                              const int64_t *slot_mapping, int32_t num_new_tokens,
+                              const int32_t *block_table, int64_t block_table_stride,
+                              int32_t max_blocks_per_seq, const int32_t *context_lens,
+                              int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                              int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                              const float *k_scale, const float *v_scale, float scale,
+                              int32_t max_context_len, void *workspace, size_t workspace_bytes,
+                              pa_dtype dtype, int32_t *d_error, void *stream);
 
 /*
  * pa_copy_blocks -- copy whole blocks of both pools (copy-on-write).

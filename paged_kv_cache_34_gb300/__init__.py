@@ -14,6 +14,9 @@ first call raises.
     pa_prefill_varlen     causal attention for cu_seqlens-packed queries
     pa_reshape_and_cache_int8, pa_decode_int8, pa_decode_write_int8 (and _fp8)
                           the write, decode and step over INT8 (FP8 E4M3) pools
+    pa_reshape_and_cache_fp4, pa_decode_fp4, pa_decode_write_fp4
+                          the same over 4-bit pools (E2M1 codes, E4M3 group scales)
+    pa_gather_cache_fp4   4-bit pools read back as 16-bit rows
     pa_copy_blocks        copy whole blocks of both pools (copy-on-write)
     pa_build_tables       a step's block tables, slots, positions and cumulative
                           lengths from request lengths
@@ -33,7 +36,8 @@ import torch
 __all__ = ["pa_reshape_and_cache", "pa_rope_and_cache", "pa_qk_norm_rope", "pa_decode", "pa_decode_plan", "pa_decode_write",
            "pa_prefill_varlen", "pa_reshape_and_cache_int8", "pa_decode_int8",
            "pa_decode_write_int8", "pa_reshape_and_cache_fp8", "pa_decode_fp8",
-           "pa_decode_write_fp8", "pa_copy_blocks", "pa_build_tables",
+           "pa_decode_write_fp8", "pa_reshape_and_cache_fp4", "pa_gather_cache_fp4",
+           "pa_decode_fp4", "pa_decode_fp4_plan", "pa_decode_write_fp4", "pa_copy_blocks", "pa_build_tables",
            "pa_attention_varlen", "pa_decode_shared", "pa_decode_shared_plan", "PaError",
            "library", "DEVERR_SLOT", "DEVERR_BLOCK_ID", "DEVERR_CU_SEQLENS",
            "DEVERR_CONTEXT", "DEVERR_TIMEOUT", "DEVERR_SCALE", "DEVERR_NO_BLOCKS",
@@ -130,6 +134,20 @@ def library(path: str | None = None):
         lib.pa_reshape_and_cache_fp8.restype = c.c_int
         lib.pa_decode_fp8.argtypes = lib.pa_decode_int8.argtypes
         lib.pa_decode_fp8.restype = c.c_int
+        lib.pa_reshape_and_cache_fp4.argtypes = lib.pa_reshape_and_cache_int8.argtypes
+        lib.pa_reshape_and_cache_fp4.restype = c.c_int
+        lib.pa_gather_cache_fp4.argtypes = [V, I64, V, I64, I32, V, V, V, I64, I32, V, V, I32, I32,
+                                            I32, I32, I32, I64, V, V, c.c_int, V, V]
+        lib.pa_gather_cache_fp4.restype = c.c_int
+        lib.pa_decode_fp4_plan.argtypes = [I32] * 5 + [c.POINTER(SZ)]
+        lib.pa_decode_fp4_plan.restype = c.c_int
+        lib.pa_decode_fp4.argtypes = [V, I64, V, I64, V, V, V, I64, I32, V, I32, I32, I32, I32, I32,
+                                      I64, V, V, F, I32, V, SZ, c.c_int, V, V]
+        lib.pa_decode_fp4.restype = c.c_int
+        lib.pa_decode_write_fp4.argtypes = [V, I64, V, I64, V, V, I64, V, V, V, I32, V, I64, I32, V,
+                                            I32, I32, I32, I32, I32, I64, V, V, F, I32, V, SZ,
+                                            c.c_int, V, V]
+        lib.pa_decode_write_fp4.restype = c.c_int
         lib.pa_decode_write_fp8.argtypes = lib.pa_decode_write_int8.argtypes
         lib.pa_decode_write_fp8.restype = c.c_int
         if path is None:
@@ -321,6 +339,116 @@ def pa_reshape_and_cache_fp8(key, value, key_cache, value_cache, slot_mapping, k
     float8_e4m3fn) [NB, bs, Hkv, D]; k_scale / v_scale float32 [Hkv]."""
     _write8("fp8", key, value, key_cache, value_cache, slot_mapping, k_scale, v_scale,
             d_error, stream, lib)
+
+
+def _pools4(key_cache, value_cache, dev):
+    """(num_blocks, num_kv_heads, block_size, head_dim) of a pair of FP4 pools."""
+    if key_cache.dtype is not torch.uint8 or value_cache.dtype is not torch.uint8 \
+            or key_cache.dim() != 4 or value_cache.shape != key_cache.shape \
+            or not key_cache.is_contiguous() or not value_cache.is_contiguous():
+        raise ValueError("FP4 caches must be contiguous uint8 [num_blocks, Hkv, block_size / 8, "
+                         "9 * head_dim / 2]")
+    if key_cache.get_device() != dev or value_cache.get_device() != dev:
+        _bad_device("caches", dev)
+    nb, hkv, tiles, width = key_cache.shape
+    if width % 9:
+        raise ValueError("an FP4 cache's tiles are 9 * head_dim / 2 bytes")
+    return nb, hkv, 8 * tiles, width // 9 * 2
+
+
+def _scales4(t, hkv, dev, what):
+    if t.dtype is not torch.float32 or t.numel() != hkv or not t.is_contiguous() \
+            or t.get_device() != dev:
+        _bad_vector(t, hkv, torch.float32, what, dev)
+    return t.data_ptr()
+
+
+def _new_rows4(key, value, slot_mapping, hkv, d, dev):
+    """(row stride, token count) of the rows that a write into FP4 pools takes."""
+    ks = _rows(key, "key")
+    if key.dtype not in _DTYPE or value.dtype is not key.dtype or value.shape != key.shape \
+            or key.shape[1] != hkv or key.shape[2] != d:
+        raise ValueError("key and value must be [N, Hkv, D] of one dtype, float16 or bfloat16")
+    if _rows(value, "value") != ks:
+        raise ValueError("key and value must share a row stride")
+    n = key.shape[0]
+    if key.get_device() != dev or value.get_device() != dev:
+        _bad_device("key or value", dev)
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.numel() != n \
+            or slot_mapping.get_device() != dev or not slot_mapping.is_contiguous():
+        _bad_vector(slot_mapping, n, torch.int64, "slot_mapping", dev)
+    return ks, n
+
+
+def pa_reshape_and_cache_fp4(key, value, key_cache, value_cache, slot_mapping, k_scale, v_scale,
+                             *, d_error=None, stream=None, lib=None):
+    """pa_reshape_and_cache into FP4 pools: caches uint8 [NB, Hkv, bs / 8, 9 D / 2]
+    (tiles of eight tokens: E2M1 codes, then E4M3 group scales); k_scale / v_scale
+    float32 [Hkv], between 2**-64 and 2**64 (absmax / 2688, for example)."""
+    lib = lib or _lib or library()
+    dev = key.get_device()
+    nb, hkv, bs, d = _pools4(key_cache, value_cache, dev)
+    ks, n = _new_rows4(key, value, slot_mapping, hkv, d, dev)
+    k_sc, v_sc = _scales4(k_scale, hkv, dev, "k_scale"), _scales4(v_scale, hkv, dev, "v_scale")
+    if d_error is not None:
+        _check_error(d_error, dev)
+    _current(dev)
+    st = lib.pa_reshape_and_cache_fp4(
+        key.data_ptr(), value.data_ptr(), ks, key_cache.data_ptr(), value_cache.data_ptr(),
+        slot_mapping.data_ptr(), n, hkv, d, bs, nb, k_sc, v_sc, _DTYPE[key.dtype],
+        None if d_error is None else d_error.data_ptr(), _raw_stream(stream, dev))
+    if st:
+        _check(lib, st, "pa_reshape_and_cache_fp4")
+
+
+def _table4(block_table, s, dev):
+    """(row stride, width) of a block table int32 [s, max_blocks]."""
+    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.shape[0] != s:
+        raise ValueError("block_table must be int32 [num_seqs, max_blocks]")
+    stride, inner = block_table.stride()
+    width = block_table.shape[1]
+    if width > 1 and inner != 1:
+        raise ValueError("block_table must have contiguous rows")
+    if block_table.get_device() != dev:
+        _bad_device("block_table", dev)
+    return (stride if s > 1 else width), width
+
+
+def pa_gather_cache_fp4(key_out, value_out, key_cache, value_cache, block_table, context_lens,
+                        row_starts, k_scale, v_scale, *, max_context_len, d_error=None, stream=None,
+                        lib=None):
+    """The rows that FP4 pools hold, in 16 bits: position j < context_lens[b] of
+    sequence b goes to row row_starts[b] + j (both int32 [S]) of key_out and
+    value_out [R, Hkv, D]; other rows are left as they were."""
+    lib = lib or _lib or library()
+    dev, s = key_out.get_device(), context_lens.numel()
+    nb, hkv, bs, d = _pools4(key_cache, value_cache, dev)
+    r = key_out.shape[0]
+    if key_out.dtype not in _DTYPE or value_out.dtype is not key_out.dtype \
+            or key_out.shape != (r, hkv, d) or value_out.shape != (r, hkv, d):
+        raise ValueError("key_out and value_out must be [R, Hkv, D] of one dtype, float16 or "
+                         "bfloat16")
+    if value_out.get_device() != dev:
+        _bad_device("value_out", dev)
+    ks, vs = _rows(key_out, "key_out"), _rows(value_out, "value_out")
+    stride, width = _table4(block_table, s, dev)
+    for t, name in ((context_lens, "context_lens"), (row_starts, "row_starts")):
+        if t.dtype is not torch.int32 or t.numel() != s or t.get_device() != dev \
+                or not t.is_contiguous():
+            _bad_vector(t, s, torch.int32, name, dev)
+    k_sc, v_sc = _scales4(k_scale, hkv, dev, "k_scale"), _scales4(v_scale, hkv, dev, "v_scale")
+    max_context_len = _bound(max_context_len, "max_context_len")
+    if d_error is not None:
+        _check_error(d_error, dev)
+    _current(dev)
+    st = lib.pa_gather_cache_fp4(
+        key_out.data_ptr(), ks, value_out.data_ptr(), vs, r, key_cache.data_ptr(),
+        value_cache.data_ptr(), block_table.data_ptr(), stride, width, context_lens.data_ptr(),
+        row_starts.data_ptr(), s, max_context_len, hkv, d, bs, nb, k_sc, v_sc,
+        _DTYPE[key_out.dtype], None if d_error is None else d_error.data_ptr(),
+        _raw_stream(stream, dev))
+    if st:
+        _check(lib, st, "pa_gather_cache_fp4")
 
 
 def pa_copy_blocks(key_cache, value_cache, block_mapping, *, d_error=None, stream=None,
@@ -626,6 +754,82 @@ def pa_decode_write_fp8(out, query, key, value, key_cache, value_cache, slot_map
     return _decode_write8("fp8", out, query, key, value, key_cache, value_cache, slot_mapping,
                           block_table, context_lens, k_scale, v_scale, scale, max_context_len,
                           partition_size, workspace, d_error, stream, lib)
+
+
+def pa_decode_fp4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, lib=None):
+    """The workspace bytes pa_decode_fp4 needs for this shape."""
+    lib = lib or _lib or library()
+    ws = ctypes.c_size_t(0)
+    st = lib.pa_decode_fp4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                _bound(max_context_len, "max_context_len"), ctypes.byref(ws))
+    if st:
+        _check(lib, st, "pa_decode_fp4_plan")
+    return ws.value
+
+
+def _decode4(what, out, query, new, key_cache, value_cache, block_table, context_lens, k_scale,
+             v_scale, scale, max_context_len, workspace, d_error, stream, lib):
+    lib = lib or _lib or library()
+    s, hq, dq = query.shape
+    dtype, dev = query.dtype, query.get_device()
+    nb, hkv, bs, d = _pools4(key_cache, value_cache, dev)
+    if out.shape != query.shape or dq != d or dtype not in _DTYPE or out.dtype is not dtype:
+        raise ValueError("out/query must be [S, Hq, D] of one dtype, float16 or bfloat16")
+    os, qs = _rows(out, "out"), _rows(query, "query")
+    stride, width = _table4(block_table, s, dev)
+    if context_lens.dtype is not torch.int32 or context_lens.numel() != s \
+            or context_lens.get_device() != dev or not context_lens.is_contiguous():
+        _bad_vector(context_lens, s, torch.int32, "context_lens", dev)
+    k_sc, v_sc = _scales4(k_scale, hkv, dev, "k_scale"), _scales4(v_scale, hkv, dev, "v_scale")
+    if out.get_device() != dev or workspace is not None and workspace.get_device() != dev:
+        _bad_device("out or workspace", dev)
+    max_context_len = _bound(max_context_len, "max_context_len")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    rows = ()
+    if new is not None:
+        key, value, slot_mapping = new
+        ks, n = _new_rows4(key, value, slot_mapping, hkv, d, dev)
+        if key.dtype is not dtype:
+            raise ValueError("key and value must share query's dtype")
+        rows = (key.data_ptr(), value.data_ptr(), ks, key_cache.data_ptr(), value_cache.data_ptr(),
+                slot_mapping.data_ptr(), n)
+    if d_error is not None:
+        _check_error(d_error, dev)
+    _current(dev)
+    if workspace is None:
+        need = pa_decode_fp4_plan(s, hq, hkv, d, max_context_len, lib=lib)
+        # on the call's stream: a later allocation of another one must not get it
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+    st = getattr(lib, what)(
+        out.data_ptr(), os, query.data_ptr(), qs,
+        *(rows or (key_cache.data_ptr(), value_cache.data_ptr())), block_table.data_ptr(), stride,
+        width, context_lens.data_ptr(), s, hq, hkv, d, bs, nb, k_sc, v_sc, scale, max_context_len,
+        workspace.data_ptr(), workspace.nbytes, _DTYPE[dtype],
+        None if d_error is None else d_error.data_ptr(), _raw_stream(stream, dev))
+    if st:
+        _check(lib, st, what)
+    return out
+
+
+def pa_decode_fp4(out, query, key_cache, value_cache, block_table, context_lens, k_scale, v_scale,
+                  *, scale, max_context_len, workspace=None, d_error=None, stream=None, lib=None):
+    """pa_decode over FP4 pools (see pa_reshape_and_cache_fp4) with per-KV-head
+    float32 scales.  A workspace is allocated with torch when none is given."""
+    return _decode4("pa_decode_fp4", out, query, None, key_cache, value_cache, block_table,
+                    context_lens, k_scale, v_scale, scale, max_context_len, workspace, d_error,
+                    stream, lib)
+
+
+def pa_decode_write_fp4(out, query, key, value, key_cache, value_cache, slot_mapping, block_table,
+                        context_lens, k_scale, v_scale, *, scale, max_context_len, workspace=None,
+                        d_error=None, stream=None, lib=None):
+    """One decode step over FP4 pools in one call: pa_reshape_and_cache_fp4, then
+    pa_decode_fp4.  Arguments as for those two functions."""
+    return _decode4("pa_decode_write_fp4", out, query, (key, value, slot_mapping), key_cache,
+                    value_cache, block_table, context_lens, k_scale, v_scale, scale,
+                    max_context_len, workspace, d_error, stream, lib)
 
 
 def pa_prefill_varlen(out, query, key_cache, value_cache, block_table, cu_seqlens_q,

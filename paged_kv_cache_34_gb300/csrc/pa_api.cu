@@ -1164,3 +1164,259 @@ pa_status pa_decode_shared(void *out, int64_t out_row_stride, const void *query,
 }
 
 }  // extern "C"
+
+namespace {
+
+// The write into 4-bit pools; *empty as for prepare_write.
+pa_status prepare_write_fp4(const void *key, const void *value, int64_t kv_row_stride,
+                            void *key_cache, void *value_cache, const int64_t *slot_mapping,
+                            int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                            int32_t block_size, int64_t num_blocks, const float *k_scale,
+                            const float *v_scale, pa_dtype dtype, int32_t *d_error,
+                            pa::ReshapeArgs *out, bool *empty) {
+  if (block_size > 0 && (num_blocks < 0 || num_blocks > INT64_MAX / block_size))
+    return PA_ERR_SHAPE;
+  const pa_status st = prepare_write(key, value, kv_row_stride, key_cache, value_cache,
+                                     slot_mapping, num_tokens, num_kv_heads, head_dim, block_size,
+                                     num_blocks, dtype, d_error, out, empty);
+  if (st != PA_OK) return st;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (!valid_block_size(block_size)) return PA_ERR_UNSUPPORTED;
+  if (!k_scale || !v_scale) return PA_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u)
+    return PA_ERR_ALIGN;
+  if (*empty) return PA_OK;
+  if (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) return PA_ERR_ALIGN;
+  out->dtype = dtype;
+  out->head_dim = head_dim;
+  out->k_scale = k_scale;
+  out->v_scale = v_scale;
+  out->num_kv_heads = num_kv_heads;
+  out->block_size = block_size;
+  return PA_OK;
+}
+
+// The workspace of a decode over 4-bit pools: pieces x (heads per slice) partial states,
+// then the prefix sums for the join.
+size_t fp4_workspace(const pa::DecodeBalance &d, int hs, int head_dim, int num_seqs) {
+  const size_t rows = static_cast<size_t>(d.pieces) * hs;
+  return align256(rows * head_dim * sizeof(float)) + align256(rows * 2 * sizeof(float)) +
+         align256((static_cast<size_t>(num_seqs) + 1) * sizeof(int32_t));
+}
+
+pa_status fp4_plan(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                   int32_t max_context_len, int *sms, pa::DecodeBalance *d, size_t *bytes) {
+  if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      max_context_len < 0 || num_q_heads % num_kv_heads != 0)
+    return PA_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  const pa::DecodeSlices sl = pa::decode_slices(num_q_heads / num_kv_heads);
+  // the schedule's positions are 32-bit, its prefix sums in shared memory
+  const int64_t units = static_cast<int64_t>(num_kv_heads) * sl.nc;
+  if (static_cast<int64_t>(max_context_len) > (1 << 30) ||
+      (num_seqs > 0 &&
+       units * ((max_context_len + 15) / 16) * 16 > ((1LL << 30) - 1) / num_seqs) ||
+      num_seqs > pa::kFp4MostSeqs)
+    return PA_ERR_UNSUPPORTED;
+  const cudaError_t e = current_num_sms(sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  *d = pa::fp4_balance(num_seqs, static_cast<int>(units), sl.ng, max_context_len, *sms);
+  *bytes = fp4_workspace(*d, sl.hs, head_dim, num_seqs);
+  return PA_OK;
+}
+
+// pa_decode_fp4, optionally after the step's cache write (launched once every check has
+// passed, so an error enqueues nothing).
+pa_status decode_fp4(void *out, int64_t out_row_stride, const void *query, int64_t q_row_stride,
+                     const void *key_cache, const void *value_cache, const int32_t *block_table,
+                     int64_t block_table_stride, int32_t max_blocks_per_seq,
+                     const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads,
+                     int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                     int64_t num_blocks, const float *k_scale, const float *v_scale, float scale,
+                     int32_t max_context_len, void *workspace, size_t workspace_bytes,
+                     pa_dtype dtype, int32_t *d_error, void *stream, const pa::ReshapeArgs *write) {
+  DecodeSetup setup;
+  pa_status st = check_decode(out, out_row_stride, query, q_row_stride, key_cache, value_cache,
+                              block_table, block_table_stride, max_blocks_per_seq, context_lens,
+                              num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                              num_blocks, scale, max_context_len, 0, dtype, &setup);
+  if (st != PA_OK) return st;
+  pa::DecodeArgs &a = setup.args;
+  if (!setup.empty) {
+    if (!k_scale || !v_scale) return PA_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale) |
+         reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(context_lens)) & 3u)
+      return PA_ERR_ALIGN;
+    pa::DecodeBalance d;
+    size_t need = 0;
+    st = fp4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, &a.num_sms, &d,
+                  &need);
+    if (st != PA_OK) return st;
+    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+      return PA_ERR_WORKSPACE;
+    a.grid = d.grid;
+    const size_t rows = static_cast<size_t>(d.pieces) * a.slices.hs;
+    char *w = static_cast<char *>(workspace);
+    a.ws_o = reinterpret_cast<float *>(w);
+    w += align256(rows * head_dim * sizeof(float));
+    a.ws_ml = reinterpret_cast<float *>(w);
+    w += align256(rows * 2 * sizeof(float));
+    a.ws_pref = reinterpret_cast<int32_t *>(w);
+    a.partition_size = 0;
+    a.num_partitions = 0;
+    a.k_pool = const_cast<void *>(key_cache);
+    a.v_pool = const_cast<void *>(value_cache);
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.d_error = d_error;
+    a.wait_ns = pa::pipeline_wait_ns();
+  }
+  if (write) {
+    pa::ReshapeArgs w = *write;
+    cudaError_t e = current_num_sms(&w.num_sms);
+    if (e == cudaSuccess) e = pa::launch_reshape_and_cache_fp4(w, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  if (setup.empty) return PA_OK;
+  const cudaError_t e = pa::launch_decode_fp4(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_reshape_and_cache_fp4(const void *key, const void *value, int64_t kv_row_stride,
+                                   void *key_cache, void *value_cache,
+                                   const int64_t *slot_mapping, int32_t num_tokens,
+                                   int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                   int64_t num_blocks, const float *k_scale, const float *v_scale,
+                                   pa_dtype dtype, int32_t *d_error, void *stream) {
+  pa::ReshapeArgs w;
+  bool empty = true;
+  const pa_status st = prepare_write_fp4(key, value, kv_row_stride, key_cache, value_cache,
+                                         slot_mapping, num_tokens, num_kv_heads, head_dim,
+                                         block_size, num_blocks, k_scale, v_scale, dtype, d_error,
+                                         &w, &empty);
+  if (st != PA_OK || empty) return st;
+  cudaError_t e = current_num_sms(&w.num_sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  e = pa::launch_reshape_and_cache_fp4(w, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+pa_status pa_gather_cache_fp4(void *key_out, int64_t k_out_row_stride, void *value_out,
+                              int64_t v_out_row_stride, int32_t num_rows, const void *key_cache,
+                              const void *value_cache, const int32_t *block_table,
+                              int64_t block_table_stride, int32_t max_blocks_per_seq,
+                              const int32_t *context_lens, const int32_t *row_starts,
+                              int32_t num_seqs, int32_t max_context_len, int32_t num_kv_heads,
+                              int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                              const float *k_scale, const float *v_scale, pa_dtype dtype,
+                              int32_t *d_error, void *stream) {
+  if (num_rows < 0 || max_blocks_per_seq < 0 || num_seqs < 0 || max_context_len < 0 ||
+      num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks < 0 ||
+      block_table_stride < max_blocks_per_seq)
+    return PA_ERR_SHAPE;
+  if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (!valid_block_size(block_size) || num_seqs > 65535) return PA_ERR_UNSUPPORTED;
+  const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (k_out_row_stride < row || v_out_row_stride < row) return PA_ERR_SHAPE;
+  if (num_rows > 0 && (k_out_row_stride > INT64_MAX / 4 / num_rows ||
+                       v_out_row_stride > INT64_MAX / 4 / num_rows))
+    return PA_ERR_SHAPE;
+  if (k_out_row_stride % 8 || v_out_row_stride % 8) return PA_ERR_ALIGN;
+  if (num_seqs == 0 || max_context_len == 0) return PA_OK;
+  if (!key_cache || !value_cache || !block_table || !context_lens || !row_starts || !k_scale ||
+      !v_scale || (num_rows > 0 && (!key_out || !value_out)))
+    return PA_ERR_NULL;
+  if (!aligned16(key_out) || !aligned16(value_out) || !aligned16(key_cache) ||
+      !aligned16(value_cache))
+    return PA_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(context_lens) |
+       reinterpret_cast<uintptr_t>(row_starts) | reinterpret_cast<uintptr_t>(k_scale) |
+       reinterpret_cast<uintptr_t>(v_scale)) & 3u)
+    return PA_ERR_ALIGN;
+  pa::GatherArgs a;
+  a.key_out = key_out;
+  a.value_out = value_out;
+  a.k_stride_bytes = k_out_row_stride * 2;
+  a.v_stride_bytes = v_out_row_stride * 2;
+  a.num_rows = num_rows;
+  a.key_cache = key_cache;
+  a.value_cache = value_cache;
+  a.block_table = block_table;
+  a.block_table_stride = block_table_stride;
+  const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * block_size;
+  a.capacity = static_cast<int32_t>(cap > INT32_MAX ? INT32_MAX : cap);
+  a.context_lens = context_lens;
+  a.row_starts = row_starts;
+  a.num_seqs = num_seqs;
+  a.max_context_len = max_context_len;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.dtype = dtype;
+  a.d_error = d_error;
+  cudaError_t e = current_num_sms(&a.num_sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  e = pa::launch_gather_cache_fp4(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+pa_status pa_decode_fp4_plan(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                             int32_t head_dim, int32_t max_context_len,
+                             size_t *workspace_bytes_out) {
+  int sms = 0;
+  pa::DecodeBalance d;
+  size_t bytes = 0;
+  const pa_status st = fp4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
+                                &sms, &d, &bytes);
+  if (st == PA_OK && workspace_bytes_out) *workspace_bytes_out = bytes;
+  return st;
+}
+
+pa_status pa_decode_fp4(void *out, int64_t out_row_stride, const void *query, int64_t q_row_stride,
+                        const void *key_cache, const void *value_cache, const int32_t *block_table,
+                        int64_t block_table_stride, int32_t max_blocks_per_seq,
+                        const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                        int64_t num_blocks, const float *k_scale, const float *v_scale, float scale,
+                        int32_t max_context_len, void *workspace, size_t workspace_bytes,
+                        pa_dtype dtype, int32_t *d_error, void *stream) {
+  return decode_fp4(out, out_row_stride, query, q_row_stride, key_cache, value_cache, block_table,
+                    block_table_stride, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
+                    num_kv_heads, head_dim, block_size, num_blocks, k_scale, v_scale, scale,
+                    max_context_len, workspace, workspace_bytes, dtype, d_error, stream, nullptr);
+}
+
+pa_status pa_decode_write_fp4(void *out, int64_t out_row_stride, const void *query,
+                              int64_t q_row_stride, const void *key, const void *value,
+                              int64_t kv_row_stride, void *key_cache, void *value_cache,
+                              const int64_t *slot_mapping, int32_t num_new_tokens,
+                              const int32_t *block_table, int64_t block_table_stride,
+                              int32_t max_blocks_per_seq, const int32_t *context_lens,
+                              int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                              int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                              const float *k_scale, const float *v_scale, float scale,
+                              int32_t max_context_len, void *workspace, size_t workspace_bytes,
+                              pa_dtype dtype, int32_t *d_error, void *stream) {
+  pa::ReshapeArgs w;
+  bool empty = true;
+  const pa_status st = prepare_write_fp4(key, value, kv_row_stride, key_cache, value_cache,
+                                         slot_mapping, num_new_tokens, num_kv_heads, head_dim,
+                                         block_size, num_blocks, k_scale, v_scale, dtype, d_error,
+                                         &w, &empty);
+  if (st != PA_OK) return st;
+  return decode_fp4(out, out_row_stride, query, q_row_stride, key_cache, value_cache, block_table,
+                    block_table_stride, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
+                    num_kv_heads, head_dim, block_size, num_blocks, k_scale, v_scale, scale,
+                    max_context_len, workspace, workspace_bytes, dtype, d_error, stream,
+                    empty ? nullptr : &w);
+}
+
+}  // extern "C"

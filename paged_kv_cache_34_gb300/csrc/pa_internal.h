@@ -30,8 +30,29 @@ struct ReshapeArgs {
   pa_dtype dtype = PA_F16;
   int32_t head_dim = 0;
   const float *k_scale = nullptr, *v_scale = nullptr;
+  int32_t num_kv_heads = 0, block_size = 0;  // 4-bit pools
 };
 cudaError_t launch_reshape_and_cache(const ReshapeArgs &a, cudaStream_t stream);
+cudaError_t launch_reshape_and_cache_fp4(const ReshapeArgs &a, cudaStream_t stream);
+
+// pa_gather_cache_fp4
+struct GatherArgs {
+  void *key_out, *value_out;
+  int64_t k_stride_bytes, v_stride_bytes;  // between rows
+  int32_t num_rows;
+  const void *key_cache, *value_cache;
+  const int32_t *block_table;
+  int64_t block_table_stride;
+  int32_t capacity;
+  const int32_t *context_lens, *row_starts;
+  int32_t num_seqs, max_context_len, num_kv_heads, head_dim, block_size;
+  int64_t num_blocks;
+  const float *k_scale, *v_scale;
+  pa_dtype dtype;
+  int32_t *d_error;
+  int num_sms;
+};
+cudaError_t launch_gather_cache_fp4(const GatherArgs &a, cudaStream_t stream);
 
 // pa_rope_and_cache; strides in elements.
 struct RopeArgs {
@@ -177,6 +198,27 @@ struct DecodeArgs {
   uint64_t wait_ns = 0;  // bound of a pipeline wait (see pipeline_wait_ns)
 };
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream);
+
+// The decode over 4-bit pools: CTAs of four warps, each a worker; the balanced split
+// over all of them, chunks of 16 tokens or more.
+constexpr int kFp4Warps = 4;
+constexpr int kFp4ChunkCap = 1 << 18;  // most tokens per chunk (workers x cap < 2^31)
+constexpr int fp4_ctas_per_sm(int ng) { return ng == 2 ? 3 : 4; }
+inline DecodeBalance fp4_balance(int num_seqs, int units, int ng, int max_ctx, int num_sms) {
+  DecodeBalance d;
+  const int64_t t_max = static_cast<int64_t>(num_seqs) * units * ((max_ctx + 15) / 16) * 16;
+  const int64_t most = static_cast<int64_t>(fp4_ctas_per_sm(ng)) * num_sms;
+  int64_t grid = (t_max / 16 + kFp4Warps - 1) / kFp4Warps;
+  grid = grid < 1 ? 1 : (grid > most ? most : grid);
+  d.grid = static_cast<int>(grid);
+  d.workers = d.grid * kFp4Warps;
+  const int64_t per = static_cast<int64_t>(d.workers) * kFp4ChunkCap;
+  d.pieces = static_cast<int64_t>(num_seqs) * units + (t_max + per) / per * d.workers;
+  return d;
+}
+constexpr int kFp4MostSeqs = 16384;  // prefix sums and lengths, 8 bytes each in shared memory
+inline int fp4_decode_smem(int num_seqs) { return 4 * (2 * num_seqs + 1); }
+cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t stream);
 // Records a failed CUDA call for pa_last_cuda_error() (this thread).
 void record_cuda_error(cudaError_t e);
 // Bound of the kernels' pipeline waits for the next launches: 2 s, unless a
