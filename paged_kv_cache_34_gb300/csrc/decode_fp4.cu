@@ -37,19 +37,68 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+__device__ __forceinline__ uint4 lds_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds_v2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+// Untiled copy of `bytes` (a multiple of 16) into shared memory, both ends 16-byte aligned.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 template <class E, int D, int NG>
 __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
     decode_fp4_kernel(const DecodeParams p, const uint8_t *__restrict__ kpool,
                       const uint8_t *__restrict__ vpool) {
   using TL = Tile<D>;
-  constexpr int KSTEPS = D / 16, KW = D / 32, VW = D / 64;
+  constexpr int KSTEPS = D / 16, KW = D / 32, VW = D / 64, NS = kFp4Stages;
+  constexpr int kHalf = kFp4StageTokens / 8 * TL::kBytes;  // a stage's keys, or its values
   constexpr bool QS = E::kBF16;
-  extern __shared__ int s_pref[];  // [S + 1] prefix sums, then [S] lengths
-  int *s_len = s_pref + p.num_seqs + 1;
+  // each warp's stages; barriers; [S + 1] prefix sums, [S] lengths
+  extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * NS * 2 * kHalf;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kWarps * NS * 2 * kHalf);
+  const uint32_t full = smem_u32(bars + warp * NS);
+  int *s_pref = reinterpret_cast<int *>(bars + kWarps * NS);
+  int *s_len = s_pref + p.num_seqs + 1;
   const int nseq = p.num_seqs;
-  griddep_wait();
+  // Inputs come from earlier kernels; right after the step's write, only the pools'
+  // rows come from the kernel just before this one.
+  if (!p.after_write) griddep_wait();
   griddep_launch_dependents();
+  if (lane == 0) {
+    for (int s = 0; s < NS; ++s) mbar_init(full + 8 * s, 1);
+    fence_barrier_init();
+  }
   if (warp == 0) {
     int carry = 0;
     for (int base = 0; base < nseq; base += 32) {
@@ -99,12 +148,68 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
                                             b * p.out_row_stride);
     for (int e = lane; e < p.hq * D / 8; e += 32) orow[e] = make_uint4(0, 0, 0, 0);
   }
-  const int bs_shift = 31 - __clz(p.block_size);
-  const int tiles_shift = bs_shift - 3;  // tiles of a (block, head)
+  const int bs = p.block_size, bs_shift = 31 - __clz(bs);
+
+  // Feeding the ring.  A stage is kFp4StageTokens of a piece; lane l < 2 n copies the
+  // l % n-th of its n runs of 8 or 16 tokens (pieces start at multiples of 16, so a
+  // run lies in one block), keys with l < n and values above.  The block ids of the
+  // stage after are loaded as one is issued.
+  const int run = bs < 16 ? 8 : 16, runs = kFp4StageTokens / run;
+  const uint32_t run_bytes = run / 8 * TL::kBytes;
+  const bool mover = lane < 2 * runs, is_v = lane >= runs;
+  const int my = (lane - (is_v ? runs : 0)) * run;  // this lane's first token in the stage
+  const uint32_t my_dst = ring + (is_v ? kHalf : 0) + my / 8 * TL::kBytes;
+  const uint8_t *pool = is_v ? vpool : kpool;
+  Cursor pc = dec::first_cursor(sc, gw);
+  int f_cur = 0, f_end = 0, f_kvh = 0;  // the stage to issue next (f_end 0: none)
+  const int32_t *f_row = nullptr;
+  int f_id = 0;
+  uint32_t bad_stages = 0;
+  auto look = [&]() {  // the next stage's place and this lane's block id
+    if (f_cur >= f_end) {
+      Item m;
+      f_end = 0;
+      if (!dec::next_piece(sc, pc, m)) return;
+      f_cur = m.start;
+      f_end = m.end;
+      f_kvh = p.nc == 1 ? m.g : m.g / p.nc;
+      f_row = p.block_table + static_cast<int64_t>(m.b) * p.bt_stride;
+    }
+    if (mover && f_cur + my < f_end) f_id = __ldg(f_row + ((f_cur + my) >> bs_shift));
+  };
+  auto issue = [&](int s) {
+    if (f_end == 0) return;
+    const int j = f_cur + my;
+    const bool want = mover && j < f_end;
+    const bool ok = want && f_id >= 0 && f_id < p.num_blocks;
+    const unsigned copies = __ballot_sync(0xffffffffu, ok);
+    const unsigned wrong = __ballot_sync(0xffffffffu, want && !ok);
+    bad_stages = wrong ? bad_stages | (1u << s) : bad_stages & ~(1u << s);
+    if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, __popc(copies) * run_bytes);
+    __syncwarp();
+    if (ok)
+      bulk_load(my_dst + s * 2 * kHalf,
+                pool + (((static_cast<int64_t>(f_id) * p.hkv + f_kvh) << (bs_shift - 3)) +
+                        ((j & (bs - 1)) >> 3)) * TL::kBytes,
+                run_bytes, full + 8 * s);
+    f_cur += kFp4StageTokens;
+    look();
+  };
+  look();
+  if (p.after_write) griddep_wait();
+  int issued = 0;
+#pragma unroll 1
+  for (int s = 0; s < NS; ++s) {
+    if (f_end) ++issued;
+    issue(s);
+  }
 
   Cursor cu = dec::first_cursor(sc, gw);
   Item m;
-  while (dec::next_piece(sc, cu, m)) {
+  int s = 0;  // the stage to read next and its phase
+  uint32_t phase = 0;
+  bool alive = true;
+  while (alive && dec::next_piece(sc, cu, m)) {
     int nh;
     const int h0 = dec::slice_head0(sc, m.g, nh);
     const int kvh = p.nc == 1 ? m.g : m.g / p.nc;
@@ -132,23 +237,19 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
       mst[n][0] = mst[n][1] = -INFINITY;
       lst[n][0] = lst[n][1] = 0.f;
     }
-    const int32_t *row = p.block_table + static_cast<int64_t>(m.b) * p.bt_stride;
-    for (int j0 = m.start; j0 < m.end; j0 += 32) {
-      int64_t at[4];  // byte offsets of the four tiles, -1 past the end or in a bad block
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int j = j0 + 8 * q;
-        at[q] = -1;
-        if (j < m.end) {
-          const int id = __ldg(row + (j >> bs_shift));
-          if (id >= 0 && id < p.num_blocks)
-            at[q] = (((static_cast<int64_t>(id) * p.hkv + kvh) << tiles_shift) +
-                     ((j & (p.block_size - 1)) >> 3)) * TL::kBytes;
-          else {
-            bad = true;
-            if (lane == 0) raise_error(p.err, PA_DEVERR_BLOCK_ID);
-          }
-        }
+#pragma unroll 1
+    for (int j0 = m.start; j0 < m.end; j0 += kFp4StageTokens) {
+      // (one lane's wait running out ends the warp's)
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(full + 8 * s, phase, p.wait_ns))) {
+        if (lane == 0) raise_error(p.err, PA_DEVERR_TIMEOUT);
+        alive = false;
+        break;
+      }
+      const uint32_t kst = ring + s * 2 * kHalf, vst = kst + kHalf;
+      const int left = m.end - j0;  // tokens of the stage (the last one may hold fewer)
+      if (bad_stages >> s & 1) {
+        bad = true;
+        if (lane == 0) raise_error(p.err, PA_DEVERR_BLOCK_ID);
       }
       float s2[NG][2][4];
 #pragma unroll
@@ -160,26 +261,22 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
         uint32_t kw[2][KW], sc2[2][2];  // [row g of tile 2u | 2u + 1]
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-#pragma unroll
-          for (int w = 0; w < KW; ++w) kw[r][w] = 0;
-          uint32_t sb = 0;
-          if (at[2 * u + r] >= 0) {
-            const uint8_t *tile = kpool + at[2 * u + r];
-            const uint8_t *src = tile + g8 * TL::kRowBytes + t4 * (D / 8);
-            const uint8_t *ss = tile + TL::kScales + g8 * TL::kScaleBytes;
-            if constexpr (D == 128) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src));
-              kw[r][0] = v.x, kw[r][1] = v.y, kw[r][2] = v.z, kw[r][3] = v.w;
-              sb = __ldg(reinterpret_cast<const uint16_t *>(ss) + t4);
-            } else {
-              const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
-              kw[r][0] = v.x, kw[r][1] = v.y;
-              sb = __ldg(ss + t4) * 0x101u;
-            }
+          const uint32_t tile = kst + (2 * u + r) * TL::kBytes;
+          const uint32_t src = tile + g8 * TL::kRowBytes + t4 * (D / 8);
+          const uint32_t ss = tile + TL::kScales + g8 * TL::kScaleBytes;
+          uint32_t sb;
+          if constexpr (D == 128) {
+            const uint4 v = lds_v4(src);
+            kw[r][0] = v.x, kw[r][1] = v.y, kw[r][2] = v.z, kw[r][3] = v.w;
+            sb = lds_u16(ss + 2 * t4);
+          } else {
+            const uint2 v = lds_v2(src);
+            kw[r][0] = v.x, kw[r][1] = v.y;
+            sb = lds_u8(ss + t4);
           }
-          const uint32_t s = e4m3_to_f16x2(sb);
-          sc2[r][0] = __byte_perm(s, s, 0x1010);
-          sc2[r][1] = __byte_perm(s, s, 0x3232);
+          const uint32_t sf = e4m3_to_f16x2(sb);
+          sc2[r][0] = __byte_perm(sf, sf, 0x1010);
+          sc2[r][1] = __byte_perm(sf, sf, 0x3232);
         }
 #pragma unroll
         for (int w = 0; w < KW; ++w) {  // k-steps 2w, 2w + 1
@@ -208,8 +305,7 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
         float sv[2][4], mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int t0 = j0 + 16 * u + g8;
-          const bool in0 = t0 < m.end, in1 = t0 + 8 < m.end;
+          const bool in0 = 16 * u + g8 < left, in1 = 16 * u + g8 + 8 < left;
           sv[u][0] = in0 ? s2[n][u][0] * slA : -INFINITY;
           sv[u][1] = in0 ? s2[n][u][1] * slB : -INFINITY;
           sv[u][2] = in1 ? s2[n][u][2] * slA : -INFINITY;
@@ -222,31 +318,34 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
           mx0 = fmaxf(mx0, dec::shfl_xor(mx0, x));
           mx1 = fmaxf(mx1, dec::shfl_xor(mx1, x));
         }
-        const float mn0 = fmaxf(mst[n][0], mx0), mn1 = fmaxf(mst[n][1], mx1);
-        const float cr0 = mn0 == -INFINITY ? 0.f : exp2f(mst[n][0] - mn0);
-        const float cr1 = mn1 == -INFINITY ? 0.f : exp2f(mst[n][1] - mn1);
-        mst[n][0] = mn0;
-        mst[n][1] = mn1;
+        if (__any_sync(0xffffffffu, mx0 > mst[n][0] || mx1 > mst[n][1])) {
+          const float mn0 = fmaxf(mst[n][0], mx0), mn1 = fmaxf(mst[n][1], mx1);
+          const float cr0 = mn0 == -INFINITY ? 0.f : fast_exp2(mst[n][0] - mn0);
+          const float cr1 = mn1 == -INFINITY ? 0.f : fast_exp2(mst[n][1] - mn1);
+          mst[n][0] = mn0;
+          mst[n][1] = mn1;
+          lst[n][0] *= cr0;
+          lst[n][1] *= cr1;
+#pragma unroll
+          for (int mt = 0; mt < KSTEPS; ++mt) {
+            o[n][mt][0] *= cr0;
+            o[n][mt][1] *= cr1;
+            o[n][mt][2] *= cr0;
+            o[n][mt][3] *= cr1;
+          }
+        }
         // P is rounded to fp16 for the tensor core; the sums take the same rounded
         // values, so the output is a weighted mean of V under the rounded weights.
-        float ls0 = 0.f, ls1 = 0.f;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint32_t w0 = F16::pack2(exp2f(sv[u][0] - mn0), exp2f(sv[u][1] - mn1));
-          const uint32_t w1 = F16::pack2(exp2f(sv[u][2] - mn0), exp2f(sv[u][3] - mn1));
-          ls0 += F16::lo(w0) + F16::lo(w1);
-          ls1 += F16::hi(w0) + F16::hi(w1);
+          const uint32_t w0 = F16::pack2(fast_exp2(sv[u][0] - mst[n][0]),
+                                         fast_exp2(sv[u][1] - mst[n][1]));
+          const uint32_t w1 = F16::pack2(fast_exp2(sv[u][2] - mst[n][0]),
+                                         fast_exp2(sv[u][3] - mst[n][1]));
+          F16::add_halves(w0, lst[n][0], lst[n][1]);
+          F16::add_halves(w1, lst[n][0], lst[n][1]);
           pb[n][u][0] = movmatrix_trans(w0);
           pb[n][u][1] = movmatrix_trans(w1);
-        }
-        lst[n][0] = lst[n][0] * cr0 + ls0;
-        lst[n][1] = lst[n][1] * cr1 + ls1;
-#pragma unroll
-        for (int mt = 0; mt < KSTEPS; ++mt) {
-          o[n][mt][0] *= cr0;
-          o[n][mt][1] *= cr1;
-          o[n][mt][2] *= cr0;
-          o[n][mt][3] *= cr1;
         }
       }
 #pragma unroll
@@ -254,28 +353,25 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
         uint32_t vx[2][VW], vy[2][VW], sv[2];  // tokens 2t and 2t + 1 of tile 2u | 2u + 1
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-#pragma unroll
-          for (int w = 0; w < VW; ++w) vx[r][w] = vy[r][w] = 0;
-          uint32_t sb = 0;
-          if (at[2 * u + r] >= 0) {
-            const uint8_t *tile = vpool + at[2 * u + r];
-            const uint8_t *src = tile + 2 * t4 * TL::kRowBytes + g8 * (D / 16);
-            const uint8_t *ss = tile + TL::kScales + 2 * t4 * TL::kScaleBytes +
-                                (D == 128 ? g8 : g8 >> 1);
-            if constexpr (D == 128) {
-              const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src));
-              const uint2 y = __ldg(reinterpret_cast<const uint2 *>(src + TL::kRowBytes));
-              vx[r][0] = x.x, vx[r][1] = x.y, vy[r][0] = y.x, vy[r][1] = y.y;
-            } else {
-              vx[r][0] = __ldg(reinterpret_cast<const uint32_t *>(src));
-              vy[r][0] = __ldg(reinterpret_cast<const uint32_t *>(src + TL::kRowBytes));
-            }
-            // rows past the context hold anything: their scale, and so their value, is 0
-            const int t0 = j0 + 8 * (2 * u + r) + 2 * t4;
-            if (t0 < m.end) sb = __ldg(ss);
-            if (t0 + 1 < m.end) sb |= static_cast<uint32_t>(__ldg(ss + TL::kScaleBytes)) << 8;
+          const uint32_t tile = vst + (2 * u + r) * TL::kBytes;
+          const uint32_t src = tile + 2 * t4 * TL::kRowBytes + g8 * (D / 16);
+          const uint32_t ss = tile + TL::kScales + 2 * t4 * TL::kScaleBytes +
+                              (D == 128 ? g8 : g8 >> 1);
+          if constexpr (D == 128) {
+            const uint2 x = lds_v2(src), y = lds_v2(src + TL::kRowBytes);
+            vx[r][0] = x.x, vx[r][1] = x.y, vy[r][0] = y.x, vy[r][1] = y.y;
+          } else {
+            vx[r][0] = lds_u32(src);
+            vy[r][0] = lds_u32(src + TL::kRowBytes);
           }
-          sv[r] = e4m3_to_f16x2(sb);
+          uint32_t sx = lds_u8(ss), sy = lds_u8(ss + TL::kScaleBytes);
+          if (left < kFp4StageTokens) {
+            // rows past the context hold anything: their scale, and so their value, is 0
+            const int t0 = 8 * (2 * u + r) + 2 * t4;
+            if (t0 >= left) sx = 0;
+            if (t0 + 1 >= left) sy = 0;
+          }
+          sv[r] = e4m3_to_f16x2(sx | sy << 8);
         }
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
@@ -301,7 +397,16 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
                                pb[n][u][0], pb[n][u][1]);
         }
       }
+      __syncwarp();  // every lane has read the stage
+      if (f_end) ++issued;
+      issue(s);
+      --issued;
+      if (++s == NS) {
+        s = 0;
+        phase ^= 1;
+      }
     }
+    if (!alive) break;
     bad = __any_sync(0xffffffffu, bad);
     // The piece's result: lane (g, t) holds elements (D / 8) g + i of head 2t in
     // o[i / 2][i % 2 ? 2 : 0] and of head 2t + 1 in o[i / 2][i % 2 ? 3 : 1].
@@ -344,6 +449,14 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
                 make_float2(bad ? -INFINITY : mst[n][hh], bad ? 0.f : l);
         }
       }
+    }
+  }
+  // A wait ran out: leave once the copies in flight are in.
+  for (; issued > 0; --issued) {
+    mbar_wait_bounded(full + 8 * s, phase);
+    if (++s == NS) {
+      s = 0;
+      phase ^= 1;
     }
   }
 }
@@ -431,7 +544,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_fp4_join_kernel(const 
 
 template <class E, int D, int NG>
 cudaError_t launch(const DecodeArgs &a, const DecodeParams &p, cudaStream_t stream) {
-  const int smem = fp4_decode_smem(a.num_seqs);
+  const int smem = fp4_decode_smem(D, a.num_seqs);
   cudaError_t e = allow_dynamic_smem<decode_fp4_kernel<E, D, NG>>();
   if (e != cudaSuccess) return e;
   e = launch_pdl(decode_fp4_kernel<E, D, NG>, dim3(static_cast<unsigned>(a.grid)),
@@ -455,7 +568,7 @@ cudaError_t launch_type(const DecodeArgs &a, const DecodeParams &p, cudaStream_t
 cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t stream) {
   dec::DecodeParams p = decode_params(a);
   const DecodeBalance d = fp4_balance(a.num_seqs, a.num_kv_heads * a.slices.nc, a.slices.ng,
-                                      a.max_context_len, a.num_sms);
+                                      a.head_dim, a.max_context_len, a.num_sms);
   p.num_workers = d.workers;
   p.chunk_cap = kFp4ChunkCap;
   return a.dtype == PA_BF16 ? fp4::launch_type<BF16>(a, p, stream)

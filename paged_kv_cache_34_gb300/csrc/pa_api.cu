@@ -1220,7 +1220,7 @@ pa_status fp4_plan(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, 
     return PA_ERR_UNSUPPORTED;
   const cudaError_t e = current_num_sms(sms);
   if (e != cudaSuccess) return cuda_fail(e);
-  *d = pa::fp4_balance(num_seqs, static_cast<int>(units), sl.ng, max_context_len, *sms);
+  *d = pa::fp4_balance(num_seqs, static_cast<int>(units), sl.ng, head_dim, max_context_len, *sms);
   *bytes = fp4_workspace(*d, sl.hs, head_dim, num_seqs);
   return PA_OK;
 }
@@ -1276,6 +1276,7 @@ pa_status decode_fp4(void *out, int64_t out_row_stride, const void *query, int64
     cudaError_t e = current_num_sms(&w.num_sms);
     if (e == cudaSuccess) e = pa::launch_reshape_and_cache_fp4(w, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e);
+    a.after_write = true;
   }
   if (setup.empty) return PA_OK;
   const cudaError_t e = pa::launch_decode_fp4(a, static_cast<cudaStream_t>(stream));

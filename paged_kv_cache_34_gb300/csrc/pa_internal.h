@@ -203,11 +203,29 @@ cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream);
 // over all of them, chunks of 16 tokens or more.
 constexpr int kFp4Warps = 4;
 constexpr int kFp4ChunkCap = 1 << 18;  // most tokens per chunk (workers x cap < 2^31)
-constexpr int fp4_ctas_per_sm(int ng) { return ng == 2 ? 3 : 4; }
-inline DecodeBalance fp4_balance(int num_seqs, int units, int ng, int max_ctx, int num_sms) {
+#ifndef FP4_CTAS
+#define FP4_CTAS 4
+#endif
+constexpr int fp4_ctas_per_sm(int ng) { return ng == 2 ? 3 : FP4_CTAS; }
+#ifndef FP4_STAGES
+#define FP4_STAGES 3
+#endif
+constexpr int kFp4StageTokens = 32;  // of a warp's stage
+constexpr int kFp4Stages = FP4_STAGES;
+constexpr int kFp4MostSeqs = 16384;  // prefix sums and lengths, 8 bytes each in shared memory
+// Shared memory: the stages (keys and values, 4.5 bits an element), a barrier each, then
+// prefix sums and lengths.
+inline int fp4_decode_smem(int head_dim, int num_seqs) {
+  return kFp4Warps * kFp4Stages * (kFp4StageTokens * head_dim * 9 / 8 + 8) +
+         4 * (2 * num_seqs + 1);
+}
+inline DecodeBalance fp4_balance(int num_seqs, int units, int ng, int head_dim, int max_ctx,
+                                 int num_sms) {
   DecodeBalance d;
   const int64_t t_max = static_cast<int64_t>(num_seqs) * units * ((max_ctx + 15) / 16) * 16;
-  const int64_t most = static_cast<int64_t>(fp4_ctas_per_sm(ng)) * num_sms;
+  // CTAs that are resident at once: 1 KB of an SM's 228 is taken for each
+  int64_t most = 228 * 1024 / (fp4_decode_smem(head_dim, num_seqs) + 1024);
+  most = (most < fp4_ctas_per_sm(ng) ? most : fp4_ctas_per_sm(ng)) * num_sms;
   int64_t grid = (t_max / 16 + kFp4Warps - 1) / kFp4Warps;
   grid = grid < 1 ? 1 : (grid > most ? most : grid);
   d.grid = static_cast<int>(grid);
@@ -216,8 +234,6 @@ inline DecodeBalance fp4_balance(int num_seqs, int units, int ng, int max_ctx, i
   d.pieces = static_cast<int64_t>(num_seqs) * units + (t_max + per) / per * d.workers;
   return d;
 }
-constexpr int kFp4MostSeqs = 16384;  // prefix sums and lengths, 8 bytes each in shared memory
-inline int fp4_decode_smem(int num_seqs) { return 4 * (2 * num_seqs + 1); }
 cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t stream);
 // Records a failed CUDA call for pa_last_cuda_error() (this thread).
 void record_cuda_error(cudaError_t e);

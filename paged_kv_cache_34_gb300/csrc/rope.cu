@@ -13,8 +13,13 @@
 // Design: HBM bound; every byte is moved once.  D / 16 lanes hold a head's row, 16
 // values each: chunk j and its partner R / 16 chunks on, so that both halves of a
 // rotated pair sit in one lane and a norm takes log2(D / 16) shuffles.  A CTA takes
-// a token at a time, a lane group per head, so that a token's cosines and sines are
-// read once per lane whatever the number of heads.
+// a token at a time, a lane group per head in as many rounds as it needs, so that a
+// token's cosines and sines are read once per lane whatever the number of heads.  A
+// lane's next row, the next token's among them, is on its way while the current one
+// is worked on, and the next token's position and slot before that (16 prompts up to
+// 2000 tokens, 32/8 heads, with norms: 76 us, 5.7 TB/s of the 6.75 of a copy; without
+// the next row on its way 82).  64 registers, 1024 threads an SM (with 94 and one CTA
+// of 384 threads 149).
 #include "pa_device.cuh"
 #include "pa_internal.h"
 
@@ -47,7 +52,7 @@ __device__ __forceinline__ uint4 pack8(const float *f) {
 
 // NORM: some weight is given.  PAIRS: neighbouring elements are rotated.
 template <class E, int D, bool NORM, bool PAIRS>
-__global__ void rope_and_cache_kernel(const RopeArgs p) {
+__global__ void __launch_bounds__(512, 2) rope_and_cache_kernel(const RopeArgs p) {
   constexpr int L = D / 16;  // lanes per head
   using T = typename E::T;
   const int grp = threadIdx.x / L, ln = threadIdx.x % L, groups = blockDim.x / L;
@@ -59,18 +64,42 @@ __global__ void rope_and_cache_kernel(const RopeArgs p) {
   const int rows = p.num_q_heads + p.num_kv_heads * (cache ? 2 : 1);
   griddep_wait();  // inputs may come from the kernel just before this one
   griddep_launch_dependents();
-  for (int64_t t = blockIdx.x; t < p.num_tokens; t += gridDim.x) {
-    const int64_t slot = cache ? __ldg(p.slot_mapping + t) : -1;
-    const int64_t pos = p.rot ? __ldg(p.positions + t) : 0;
-    if (p.rot && (pos < 0 || pos >= p.max_position)) {
-      if (threadIdx.x == 0) raise_error(p.d_error, PA_DEVERR_POSITION);
-      continue;
+  int64_t slot = -1;
+  int pos = 0;
+  auto ahead = [&](int64_t t) {
+    if (t >= p.num_tokens) return;
+    if (p.rot) pos = __ldg(p.positions + t);
+    if (cache) slot = __ldg(p.slot_mapping + t);
+  };
+  // A lane's chunks of row r of token t: query heads, then key heads, then value heads.
+  auto fetch = [&](int64_t t, int r, uint4 &va, uint4 &vb) {
+    if (t >= p.num_tokens || r >= rows) return;
+    int h = r - p.num_q_heads;
+    const T *src = static_cast<const T *>(p.query) + t * p.q_row_stride + r * D;
+    if (h >= 0) {
+      const bool value = h >= p.num_kv_heads;
+      if (value) h -= p.num_kv_heads;
+      src = static_cast<const T *>(value ? p.value : p.key) + t * p.kv_row_stride + h * D;
     }
-    if (slot >= p.num_slots && threadIdx.x == 0) raise_error(p.d_error, PA_DEVERR_SLOT);
-    const bool store = slot >= 0 && slot < p.num_slots;
+    va = load_row(src + 8 * ca);
+    vb = load_row(src + 8 * cb);
+  };
+  uint4 na, nb;  // the chunks of the row after the current one
+  ahead(blockIdx.x);
+  fetch(blockIdx.x, grp, na, nb);
+  for (int64_t t = blockIdx.x; t < p.num_tokens; t += gridDim.x) {
+    const int64_t at = slot;
+    const int row = pos;
+    ahead(t + gridDim.x);  // the next token's, while this one's rows are on their way
+    const bool known = !p.rot || (row >= 0 && row < p.max_position);
+    if (threadIdx.x == 0) {
+      if (!known) raise_error(p.d_error, PA_DEVERR_POSITION);
+      else if (at >= p.num_slots) raise_error(p.d_error, PA_DEVERR_SLOT);
+    }
+    const bool store = known && at >= 0 && at < p.num_slots;
     float c[8], s[8];
-    if (turn) {  // half-split: the pair's eight angles; neighbours: four for each chunk
-      const float *cs = p.cos_sin + pos * p.rot;
+    if (turn && known) {  // half-split: the pair's eight angles; neighbours: four for each chunk
+      const float *cs = p.cos_sin + static_cast<int64_t>(row) * p.rot;
       const float4 *x0 = reinterpret_cast<const float4 *>(cs + (PAIRS ? 4 * ca : 8 * ca));
       const float4 *x1 = PAIRS ? reinterpret_cast<const float4 *>(cs + 4 * cb) : x0 + 1;
       const int h4 = p.rot / 8;  // float4s of half a row
@@ -83,31 +112,17 @@ __global__ void rope_and_cache_kernel(const RopeArgs p) {
     // every lane takes every round: the norm's shuffles need whole warps
     for (int r0 = 0; r0 < rows; r0 += groups) {
       const int r = r0 + grp;
-      const bool live = r < rows, q = r < p.num_q_heads;
+      uint4 va = na, vb = nb;
+      if (r0 + groups < rows) fetch(t, r + groups, na, nb);
+      else fetch(t + gridDim.x, grp, na, nb);
+      const bool live = known && r < rows, q = r < p.num_q_heads;
       const int kh = r - p.num_q_heads;  // the key head, or num_kv_heads + the value head
       const bool value = kh >= p.num_kv_heads;
-      const T *src = static_cast<const T *>(p.query) + t * p.q_row_stride + r * D;
-      if (!q) src = static_cast<const T *>(p.key) + t * p.kv_row_stride + kh * D;
-      if (value)
-        src = static_cast<const T *>(p.value) + t * p.kv_row_stride + (kh - p.num_kv_heads) * D;
-      uint4 va = make_uint4(0, 0, 0, 0), vb = va;
-      if (live && (!value || store)) {
-        va = load_row(src + 8 * ca);
-        vb = load_row(src + 8 * cb);
-      }
-      if (live && value) {
-        if (store) {
-          T *dst = static_cast<T *>(p.value_cache) +
-                   (slot * p.num_kv_heads + kh - p.num_kv_heads) * D;
-          *reinterpret_cast<uint4 *>(dst + 8 * ca) = va;
-          *reinterpret_cast<uint4 *>(dst + 8 * cb) = vb;
-        }
-      }
-      const void *w = q ? p.q_weight : p.k_weight;
       float a[8], b[8];
       unpack8<E>(va, a);
       unpack8<E>(vb, b);
       if constexpr (NORM) {
+        const void *w = q ? p.q_weight : p.k_weight;
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss += a[i] * a[i] + b[i] * b[i];
@@ -115,44 +130,46 @@ __global__ void rope_and_cache_kernel(const RopeArgs p) {
         for (int m = 1; m < L; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
         if (w && live && !value) {
           const float f = rsqrtf(ss * (1.f / D) + p.eps);
-          float wa[8], wb[8];
+          float wa[8];
           unpack8<E>(__ldg(reinterpret_cast<const uint4 *>(w) + ca), wa);
-          unpack8<E>(__ldg(reinterpret_cast<const uint4 *>(w) + cb), wb);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) a[i] *= f * wa[i];
+          unpack8<E>(__ldg(reinterpret_cast<const uint4 *>(w) + cb), wa);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) b[i] *= f * wa[i];
+        }
+      }
+      if (!live) continue;
+      if (!value) {
+        if (turn) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            a[i] *= f * wa[i];
-            b[i] *= f * wb[i];
+            if constexpr (PAIRS) {
+              if (i & 1) continue;
+              const float a0 = a[i], b0 = b[i];
+              a[i] = a0 * c[i / 2] - a[i + 1] * s[i / 2];
+              a[i + 1] = a[i + 1] * c[i / 2] + a0 * s[i / 2];
+              b[i] = b0 * c[4 + i / 2] - b[i + 1] * s[4 + i / 2];
+              b[i + 1] = b[i + 1] * c[4 + i / 2] + b0 * s[4 + i / 2];
+            } else {
+              const float a0 = a[i];
+              a[i] = a0 * c[i] - b[i] * s[i];
+              b[i] = b[i] * c[i] + a0 * s[i];
+            }
           }
         }
-      }
-      if (!live || value) continue;
-      if (turn) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if constexpr (PAIRS) {
-            if (i & 1) continue;
-            const float a0 = a[i], b0 = b[i];
-            a[i] = a0 * c[i / 2] - a[i + 1] * s[i / 2];
-            a[i + 1] = a[i + 1] * c[i / 2] + a0 * s[i / 2];
-            b[i] = b0 * c[4 + i / 2] - b[i + 1] * s[4 + i / 2];
-            b[i + 1] = b[i + 1] * c[4 + i / 2] + b0 * s[4 + i / 2];
-          } else {
-            const float a0 = a[i];
-            a[i] = a0 * c[i] - b[i] * s[i];
-            b[i] = b[i] * c[i] + a0 * s[i];
-          }
+        va = pack8<E>(a);
+        vb = pack8<E>(b);
+        if (q || p.key_out) {
+          T *dst = q ? static_cast<T *>(p.query_out) + t * p.q_out_row_stride + r * D
+                     : static_cast<T *>(p.key_out) + t * p.k_out_row_stride + kh * D;
+          *reinterpret_cast<uint4 *>(dst + 8 * ca) = va;
+          *reinterpret_cast<uint4 *>(dst + 8 * cb) = vb;
         }
-      }
-      va = pack8<E>(a);
-      vb = pack8<E>(b);
-      if (q || p.key_out) {
-        T *dst = q ? static_cast<T *>(p.query_out) + t * p.q_out_row_stride + r * D
-                   : static_cast<T *>(p.key_out) + t * p.k_out_row_stride + kh * D;
-        *reinterpret_cast<uint4 *>(dst + 8 * ca) = va;
-        *reinterpret_cast<uint4 *>(dst + 8 * cb) = vb;
       }
       if (!q && store) {
-        T *dst = static_cast<T *>(p.key_cache) + (slot * p.num_kv_heads + kh) * D;
+        T *dst = static_cast<T *>(value ? p.value_cache : p.key_cache) +
+                 (at * p.num_kv_heads + kh - (value ? p.num_kv_heads : 0)) * D;
         *reinterpret_cast<uint4 *>(dst + 8 * ca) = va;
         *reinterpret_cast<uint4 *>(dst + 8 * cb) = vb;
       }
@@ -163,10 +180,16 @@ __global__ void rope_and_cache_kernel(const RopeArgs p) {
 template <class E, int D>
 cudaError_t launch(const RopeArgs &a, cudaStream_t stream) {
   constexpr int L = D / 16;
+  // Where every token has a CTA at once, wide CTAs take its rows in one round; beyond
+  // that, narrow ones keep more rounds' loads in flight (32/8 heads, norms, up to 512
+  // and up to 128 threads: 32 tokens 2.4 and 3.6 us, 304 3.1 and 4.0, 456 5.1 and 4.2,
+  // 2432 21.2 and 13.9, 16700 122 and 76.5; up to 64 threads 76.1 and 13.3, but 456
+  // 6.4).
   const int rows = a.num_q_heads + a.num_kv_heads * (a.key_cache ? 2 : 1);
-  int threads = (rows * L + 31) / 32 * 32;
-  if (threads > 512) threads = 512;
-  const int64_t most = static_cast<int64_t>(a.num_sms) * (2048 / threads);
+  const int widest = a.num_tokens <= 2 * a.num_sms ? 512 : 128;
+  const int rounds = (rows * L + widest - 1) / widest;
+  const int threads = ((rows + rounds - 1) / rounds * L + 31) / 32 * 32;
+  const int64_t most = static_cast<int64_t>(a.num_sms) * (1024 / threads);
   const int grid = static_cast<int>(a.num_tokens < most ? a.num_tokens : most);
   const bool norm = a.q_weight || a.k_weight;
   auto kernel = norm ? (a.interleaved ? rope_and_cache_kernel<E, D, true, true>
