@@ -25,18 +25,92 @@
 namespace pa {
 namespace fp4 {
 
-using dec::Cursor;
 using dec::DecodeParams;
-using dec::Item;
-using dec::Sched;
 
 constexpr int kWarps = kFp4Warps;
+constexpr int kTokens = kFp4StageTokens;
+template <int D>
+constexpr int kStages = fp4_stages(D);
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+__host__ __device__ __forceinline__ int ceil32(int x) { return (x + 31) & ~31; }
+
+// The balanced split: the units' contexts, each rounded up to 32 tokens, end to end, cut
+// into chunks of a multiple of 32, at most one or two per worker (32-bit arithmetic is
+// exact while total < 2^30 and workers * cap < 2^31).  So a piece starts at a multiple of
+// 32 of its sequence, and a stage of 32 tokens lies in one block of 32 or more.
+__device__ __forceinline__ int chunk_tokens(int total, int workers, int cap) {
+  const uint32_t t = total, per = static_cast<uint32_t>(workers) * cap;
+  const uint32_t n = (t > per ? (t + per - 1) / per : 1u) * workers;
+  const int c = ceil32(static_cast<int>((t + n - 1) / n));
+  return c > 0 ? c : 32;
+}
+
+// A piece of work: tokens start .. end - 1 of unit g (a slice of a KV head's query heads)
+// of sequence b; `whole`: the unit's whole context.  Its partial state goes to the
+// workspace rows (b vh + g + chunk) hs + head.
+struct Piece {
+  int b, g, start, end, chunk;
+  bool whole;
+};
+struct Cursor {
+  int chunk, at;  // a worker's chunk and its place in it
+};
+// The next piece of a worker's chunks; false at the end.
+__device__ inline bool next_piece(const DecodeParams &p, const int *pref, const int *len, int C,
+                                  int chunks, Cursor &cu, Piece &m) {
+  const int total = pref[p.num_seqs];
+  while (cu.chunk < chunks) {
+    const int end = min((cu.chunk + 1) * C, total);
+    if (cu.at >= end) {
+      cu.chunk += p.num_workers;
+      cu.at = cu.chunk * C;
+      continue;
+    }
+    int lo = 0, hi = p.num_seqs;  // pref[lo] <= at < pref[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pref[mid] <= cu.at) lo = mid;
+      else hi = mid;
+    }
+    const int L = len[lo], W = ceil32(L), rel = cu.at - pref[lo];
+    m.b = lo;
+    m.g = rel / W;
+    m.start = rel - m.g * W;
+    const int stop = min(W, m.start + (end - cu.at));
+    cu.at += stop - m.start;
+    m.end = min(stop, L);
+    m.chunk = cu.chunk;
+    m.whole = m.start == 0 && stop == W;
+    return true;
+  }
+  return false;
+}
+// The first query head of unit g and the number of heads in it.
+__device__ __forceinline__ int first_head(const DecodeParams &p, int g, int &n) {
+  const int kvh = p.nc == 1 ? g : g / p.nc, sl = g - kvh * p.nc;
+  n = min(p.hs, p.group - sl * p.hs);
+  return kvh * p.group + sl * p.hs;
+}
+
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, __half2 b) {
+  const __half2 r = __hmul2(as_half2(a), b);
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+// (not volatile, unlike the shared forms: nothing but their operands orders them)
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, const uint32_t (&b)[2]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ uint32_t transpose(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 __device__ __forceinline__ uint4 lds_v4(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -75,12 +149,12 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 }
 
 template <class E, int D, int NG>
-__global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
+__global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
     decode_fp4_kernel(const DecodeParams p, const uint8_t *__restrict__ kpool,
                       const uint8_t *__restrict__ vpool) {
   using TL = Tile<D>;
-  constexpr int KSTEPS = D / 16, KW = D / 32, VW = D / 64, NS = kFp4Stages;
-  constexpr int kHalf = kFp4StageTokens / 8 * TL::kBytes;  // a stage's keys, or its values
+  constexpr int KSTEPS = D / 16, KW = D / 32, VW = D / 64, NS = kStages<D>;
+  constexpr int kHalf = kTokens / 8 * TL::kBytes, kSub = 32;  // a stage's keys, or its values
   constexpr bool QS = E::kBF16;
   // each warp's stages; barriers; [S + 1] prefix sums, [S] lengths
   extern __shared__ __align__(128) uint8_t smem[];
@@ -108,7 +182,7 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
         const int L = checked_context_len(__ldg(p.context_lens + b), p.capacity, p.max_ctx, p.err,
                                           blockIdx.x == 0);
         s_len[b] = L;
-        items = dec::ceil16(L) * p.vh;
+        items = ceil32(L) * p.vh;
       }
       int incl = items;
 #pragma unroll
@@ -122,27 +196,13 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
     if (lane == 0) s_pref[0] = 0;
   }
   __syncthreads();
-  Sched sc;
-  sc.pref = s_pref;
-  sc.len = s_len;
-  sc.S = nseq;
-  sc.vh = p.vh;
-  sc.hq = p.hq;
-  sc.G = p.group;
-  sc.nc = p.nc;
-  sc.hs = p.hs;
-  sc.P = 0;
-  sc.NP = 0;
-  sc.NW = p.num_workers;
-  sc.balanced = true;
-  sc.total = s_pref[nseq];
-  sc.C = dec::balanced_chunk(sc.total, sc.NW, p.chunk_cap);
-  sc.chunks = (sc.total + sc.C - 1) / sc.C;
+  const int total = s_pref[nseq];
+  const int C = chunk_tokens(total, p.num_workers, p.chunk_cap), chunks = (total + C - 1) / C;
   const int gw = blockIdx.x * kWarps + warp;
   if (blockIdx.x == 0)
     for (int i = tid; i <= nseq; i += blockDim.x) p.ws_pref[i] = s_pref[i];
   // empty sequences have no pieces: their zeros
-  for (int b = gw; b < nseq; b += sc.NW) {
+  for (int b = gw; b < nseq; b += p.num_workers) {
     if (s_len[b] != 0) continue;
     uint4 *orow = reinterpret_cast<uint4 *>(static_cast<typename E::T *>(p.out) +
                                             b * p.out_row_stride);
@@ -150,49 +210,56 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
   }
   const int bs = p.block_size, bs_shift = 31 - __clz(bs);
 
-  // Feeding the ring.  A stage is kFp4StageTokens of a piece; lane l < 2 n copies the
-  // l % n-th of its n runs of 8 or 16 tokens (pieces start at multiples of 16, so a
-  // run lies in one block), keys with l < n and values above.  The block ids of the
-  // stage after are loaded as one is issued.
-  const int run = bs < 16 ? 8 : 16, runs = kFp4StageTokens / run;
-  const uint32_t run_bytes = run / 8 * TL::kBytes;
-  const bool mover = lane < 2 * runs, is_v = lane >= runs;
-  const int my = (lane - (is_v ? runs : 0)) * run;  // this lane's first token in the stage
-  const uint32_t my_dst = ring + (is_v ? kHalf : 0) + my / 8 * TL::kBytes;
-  const uint8_t *pool = is_v ? vpool : kpool;
-  Cursor pc = dec::first_cursor(sc, gw);
-  int f_cur = 0, f_end = 0, f_kvh = 0;  // the stage to issue next (f_end 0: none)
+  // Feeding the ring.  A stage is kTokens of a piece: a run of tiles per block, keys and
+  // values.  Lane 0 copies; lane q loads the id of the stage's q-th block, for the stage
+  // after as one is issued.
+  Cursor pc = {gw, gw * C};
+  int f_cur = 0, f_end = 0, f_kvh = 0, f_id = -1;  // the stage to issue next (f_end 0: none)
   const int32_t *f_row = nullptr;
-  int f_id = 0;
   uint32_t bad_stages = 0;
-  auto look = [&]() {  // the next stage's place and this lane's block id
+  auto look = [&]() {  // the next stage's place and its block ids
     if (f_cur >= f_end) {
-      Item m;
+      Piece m;
       f_end = 0;
-      if (!dec::next_piece(sc, pc, m)) return;
+      if (!next_piece(p, s_pref, s_len, C, chunks, pc, m)) return;
       f_cur = m.start;
       f_end = m.end;
       f_kvh = p.nc == 1 ? m.g : m.g / p.nc;
       f_row = p.block_table + static_cast<int64_t>(m.b) * p.bt_stride;
     }
-    if (mover && f_cur + my < f_end) f_id = __ldg(f_row + ((f_cur + my) >> bs_shift));
+    const int blk = (f_cur >> bs_shift) + lane;
+    if (blk << bs_shift < min(f_end, f_cur + kTokens)) f_id = __ldg(f_row + blk);
   };
+  const uint32_t block_bytes = static_cast<uint32_t>(p.hkv << (bs_shift - 3)) * TL::kBytes;
   auto issue = [&](int s) {
     if (f_end == 0) return;
-    const int j = f_cur + my;
-    const bool want = mover && j < f_end;
-    const bool ok = want && f_id >= 0 && f_id < p.num_blocks;
-    const unsigned copies = __ballot_sync(0xffffffffu, ok);
-    const unsigned wrong = __ballot_sync(0xffffffffu, want && !ok);
+    const uint32_t bar = full + 8 * s;
+    uint32_t dst = ring + s * 2 * kHalf, sum = 0;
+    bool wrong = false;
+    const int stop = min(f_end, f_cur + kTokens);
+    int j = f_cur;
+#pragma unroll 1
+    for (int q = 0; j < stop; ++q) {
+      const int id = __shfl_sync(0xffffffffu, f_id, q);
+      const int n = min(bs - (j & (bs - 1)), stop - j);  // tokens in this block
+      const uint32_t bytes = (n + 7) / 8 * TL::kBytes;
+      if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(p.num_blocks)) {
+        wrong = true;
+      } else {
+        const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(id)) * block_bytes +
+                            ((f_kvh << (bs_shift - 3)) + ((j & (bs - 1)) >> 3)) * TL::kBytes;
+        sum += 2 * bytes;
+        if (lane == 0) {
+          bulk_load(dst, kpool + at, bytes, bar);
+          bulk_load(dst + kHalf, vpool + at, bytes, bar);
+        }
+      }
+      dst += bytes;
+      j += n;
+    }
+    if (lane == 0) mbar_arrive_expect_tx(bar, sum);
     bad_stages = wrong ? bad_stages | (1u << s) : bad_stages & ~(1u << s);
-    if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, __popc(copies) * run_bytes);
-    __syncwarp();
-    if (ok)
-      bulk_load(my_dst + s * 2 * kHalf,
-                pool + (((static_cast<int64_t>(f_id) * p.hkv + f_kvh) << (bs_shift - 3)) +
-                        ((j & (bs - 1)) >> 3)) * TL::kBytes,
-                run_bytes, full + 8 * s);
-    f_cur += kFp4StageTokens;
+    f_cur += kTokens;
     look();
   };
   look();
@@ -204,14 +271,14 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
     issue(s);
   }
 
-  Cursor cu = dec::first_cursor(sc, gw);
-  Item m;
+  Cursor cu = {gw, gw * C};
+  Piece m;
   int s = 0;  // the stage to read next and its phase
   uint32_t phase = 0;
   bool alive = true;
-  while (alive && dec::next_piece(sc, cu, m)) {
+  while (alive && next_piece(p, s_pref, s_len, C, chunks, cu, m)) {
     int nh;
-    const int h0 = dec::slice_head0(sc, m.g, nh);
+    const int h0 = first_head(p, m.g, nh);
     const int kvh = p.nc == 1 ? m.g : m.g / p.nc;
     uint32_t qf[NG][KSTEPS][2];
     dec::load_q<E, D, true, NG>(qf, p, m.b, h0, nh, lane);
@@ -229,101 +296,156 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
         slh[n][1] = sl * __shfl_sync(0xffffffffu, qsc[n], 8 * t4 + 4);
       }
     }
-    float o[NG][KSTEPS][4], mst[NG][2], lst[NG][2];
+    float o[NG][KSTEPS][4], ref[NG][2], lst[NG][2];
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
 #pragma unroll
       for (int mt = 0; mt < KSTEPS; ++mt) o[n][mt][0] = o[n][mt][1] = o[n][mt][2] = o[n][mt][3] = 0;
-      mst[n][0] = mst[n][1] = -INFINITY;
+      ref[n][0] = ref[n][1] = -INFINITY;
       lst[n][0] = lst[n][1] = 0.f;
     }
 #pragma unroll 1
-    for (int j0 = m.start; j0 < m.end; j0 += kFp4StageTokens) {
+    for (int j0 = m.start; j0 < m.end; j0 += kTokens) {
       // (one lane's wait running out ends the warp's)
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(full + 8 * s, phase, p.wait_ns))) {
         if (lane == 0) raise_error(p.err, PA_DEVERR_TIMEOUT);
         alive = false;
         break;
       }
-      const uint32_t kst = ring + s * 2 * kHalf, vst = kst + kHalf;
-      const int left = m.end - j0;  // tokens of the stage (the last one may hold fewer)
       if (bad_stages >> s & 1) {
         bad = true;
         if (lane == 0) raise_error(p.err, PA_DEVERR_BLOCK_ID);
       }
+#pragma unroll 1
+      for (int sub = 0; sub < kTokens && j0 + sub < m.end; sub += kSub) {
+      const uint32_t kst = ring + s * 2 * kHalf + sub / 8 * TL::kBytes, vst = kst + kHalf;
+      const int left = m.end - j0 - sub;  // tokens from here on
       float s2[NG][2][4];
 #pragma unroll
       for (int n = 0; n < NG; ++n)
 #pragma unroll
         for (int u = 0; u < 2; ++u) s2[n][u][0] = s2[n][u][1] = s2[n][u][2] = s2[n][u][3] = 0.f;
+      uint32_t kw[4][KW];  // row g of each tile
+      __half2 kf[4][2];    // its groups' scales
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t kw[2][KW], sc2[2][2];  // [row g of tile 2u | 2u + 1]
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint32_t tile = kst + (2 * u + r) * TL::kBytes;
-          const uint32_t src = tile + g8 * TL::kRowBytes + t4 * (D / 8);
-          const uint32_t ss = tile + TL::kScales + g8 * TL::kScaleBytes;
-          uint32_t sb;
-          if constexpr (D == 128) {
-            const uint4 v = lds_v4(src);
-            kw[r][0] = v.x, kw[r][1] = v.y, kw[r][2] = v.z, kw[r][3] = v.w;
-            sb = lds_u16(ss + 2 * t4);
-          } else {
-            const uint2 v = lds_v2(src);
-            kw[r][0] = v.x, kw[r][1] = v.y;
-            sb = lds_u8(ss + t4);
-          }
-          const uint32_t sf = e4m3_to_f16x2(sb);
-          sc2[r][0] = __byte_perm(sf, sf, 0x1010);
-          sc2[r][1] = __byte_perm(sf, sf, 0x3232);
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t tile = kst + i * TL::kBytes;
+        const uint32_t src = tile + g8 * TL::kRowBytes + t4 * (D / 8);
+        const uint32_t ss = tile + TL::kScales + g8 * TL::kScaleBytes;
+        uint32_t sb;
+        if constexpr (D == 128) {
+          const uint4 v = lds_v4(src);
+          kw[i][0] = v.x, kw[i][1] = v.y, kw[i][2] = v.z, kw[i][3] = v.w;
+          sb = lds_u16(ss + 2 * t4);
+        } else {
+          const uint2 v = lds_v2(src);
+          kw[i][0] = v.x, kw[i][1] = v.y;
+          sb = lds_u8(ss + t4);
         }
+        const __half2 f = as_half2(e4m3_to_f16x2(sb));
+        kf[i][0] = __low2half2(f);
+        kf[i][1] = __high2half2(f);
+      }
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {  // k-steps 2w, 2w + 1
+      for (int w = 0; w < KW; ++w) {  // k-steps 2w, 2w + 1
+        const int hf = D == 128 ? w >> 1 : 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
           uint32_t a[4], b[4];
-          widen8(kw[0][w], a[0], a[1], a[2], a[3]);
-          widen8(kw[1][w], b[0], b[1], b[2], b[3]);
-          const int hf = D == 128 ? w >> 1 : 0;
+          widen8(kw[2 * u][w], a[0], a[1], a[2], a[3]);
+          widen8(kw[2 * u + 1][w], b[0], b[1], b[2], b[3]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            a[i] = hmul2(a[i], sc2[0][hf]);
-            b[i] = hmul2(b[i], sc2[1][hf]);
+            a[i] = hmul2(a[i], kf[2 * u][hf]);
+            b[i] = hmul2(b[i], kf[2 * u + 1][hf]);
           }
 #pragma unroll
           for (int n = 0; n < NG; ++n) {
-            mma_16816<false>(s2[n][u], a[0], b[0], a[1], b[1], qf[n][2 * w][0], qf[n][2 * w][1]);
-            mma_16816<false>(s2[n][u], a[2], b[2], a[3], b[3], qf[n][2 * w + 1][0],
-                             qf[n][2 * w + 1][1]);
+            mma(s2[n][u], a[0], b[0], a[1], b[1], qf[n][2 * w]);
+            mma(s2[n][u], a[2], b[2], a[3], b[3], qf[n][2 * w + 1]);
           }
         }
       }
+      uint32_t vx[4][VW], vy[4][VW];  // tokens 2t and 2t + 1 of each tile
+      __half2 vf[4];                  // their scales
+      auto load_v = [&](int i) {
+        const uint32_t tile = vst + i * TL::kBytes;
+        const uint32_t src = tile + 2 * t4 * TL::kRowBytes + g8 * (D / 16);
+        const uint32_t ss = tile + TL::kScales + 2 * t4 * TL::kScaleBytes +
+                            (D == 128 ? g8 : g8 >> 1);
+        if constexpr (D == 128) {
+          const uint2 x = lds_v2(src), y = lds_v2(src + TL::kRowBytes);
+          vx[i][0] = x.x, vx[i][1] = x.y, vy[i][0] = y.x, vy[i][1] = y.y;
+        } else {
+          vx[i][0] = lds_u32(src);
+          vy[i][0] = lds_u32(src + TL::kRowBytes);
+        }
+        uint32_t sx = lds_u8(ss), sy = lds_u8(ss + TL::kScaleBytes);
+        if (left < kSub) {
+          // rows past the context hold anything: their scale, and so their value, is 0
+          const int t0 = 8 * i + 2 * t4;
+          if (t0 >= left) sx = 0;
+          if (t0 + 1 >= left) sy = 0;
+        }
+        vf[i] = as_half2(e4m3_to_f16x2(sx | sy << 8));
+      };
+      // (their loads run under the softmax, where the registers allow it)
+      if constexpr (NG == 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_v(i);
       // Scores of tokens j0 + 16u + g (s2[n][u][0..1], heads 8n + 2t, +1) and + 8 (2..3).
       uint32_t pb[NG][2][2];
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         const float slA = QS ? slh[QS ? n : 0][0] : sl, slB = QS ? slh[QS ? n : 0][1] : sl;
-        float sv[2][4], mx0 = -INFINITY, mx1 = -INFINITY;
+        // Exponents against a reference that only follows the largest score once that
+        // is more than 8 above it: weights up to 256, which fp16 holds as well, and a
+        // stage whose scores stay below needs one vote and no maximum over lanes.
+        float a[2][4];
+        auto exponents = [&]() {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const bool in0 = 16 * u + g8 < left, in1 = 16 * u + g8 + 8 < left;
-          sv[u][0] = in0 ? s2[n][u][0] * slA : -INFINITY;
-          sv[u][1] = in0 ? s2[n][u][1] * slB : -INFINITY;
-          sv[u][2] = in1 ? s2[n][u][2] * slA : -INFINITY;
-          sv[u][3] = in1 ? s2[n][u][3] * slB : -INFINITY;
-          mx0 = fmaxf(mx0, fmaxf(sv[u][0], sv[u][2]));
-          mx1 = fmaxf(mx1, fmaxf(sv[u][1], sv[u][3]));
-        }
+          for (int u = 0; u < 2; ++u) {
+            a[u][0] = s2[n][u][0] * slA - ref[n][0];
+            a[u][1] = s2[n][u][1] * slB - ref[n][1];
+            a[u][2] = s2[n][u][2] * slA - ref[n][0];
+            a[u][3] = s2[n][u][3] * slB - ref[n][1];
+          }
+          if (left < kSub) {
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) {
-          mx0 = fmaxf(mx0, dec::shfl_xor(mx0, x));
-          mx1 = fmaxf(mx1, dec::shfl_xor(mx1, x));
-        }
-        if (__any_sync(0xffffffffu, mx0 > mst[n][0] || mx1 > mst[n][1])) {
-          const float mn0 = fmaxf(mst[n][0], mx0), mn1 = fmaxf(mst[n][1], mx1);
-          const float cr0 = mn0 == -INFINITY ? 0.f : fast_exp2(mst[n][0] - mn0);
-          const float cr1 = mn1 == -INFINITY ? 0.f : fast_exp2(mst[n][1] - mn1);
-          mst[n][0] = mn0;
-          mst[n][1] = mn1;
+            for (int u = 0; u < 2; ++u) {
+              if (16 * u + g8 >= left) a[u][0] = a[u][1] = -INFINITY;
+              if (16 * u + g8 + 8 >= left) a[u][2] = a[u][3] = -INFINITY;
+            }
+          }
+        };
+        exponents();
+        float mx0 = fmaxf(fmaxf(a[0][0], a[0][2]), fmaxf(a[1][0], a[1][2]));
+        float mx1 = fmaxf(fmaxf(a[0][1], a[0][3]), fmaxf(a[1][1], a[1][3]));
+        if (__any_sync(0xffffffffu, fmaxf(mx0, mx1) > 8.f)) {
+          // (the first stage always: the reference is -inf)
+          mx0 = mx1 = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (16 * u + g8 < left) {
+              mx0 = fmaxf(mx0, s2[n][u][0] * slA);
+              mx1 = fmaxf(mx1, s2[n][u][1] * slB);
+            }
+            if (16 * u + g8 + 8 < left) {
+              mx0 = fmaxf(mx0, s2[n][u][2] * slA);
+              mx1 = fmaxf(mx1, s2[n][u][3] * slB);
+            }
+          }
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) {
+            mx0 = fmaxf(mx0, dec::shfl_xor(mx0, x));
+            mx1 = fmaxf(mx1, dec::shfl_xor(mx1, x));
+          }
+          mx0 = fmaxf(mx0, ref[n][0]);
+          mx1 = fmaxf(mx1, ref[n][1]);
+          const float cr0 = mx0 == -INFINITY ? 0.f : fast_exp2(ref[n][0] - mx0);
+          const float cr1 = mx1 == -INFINITY ? 0.f : fast_exp2(ref[n][1] - mx1);
+          ref[n][0] = mx0;
+          ref[n][1] = mx1;
           lst[n][0] *= cr0;
           lst[n][1] *= cr1;
 #pragma unroll
@@ -333,69 +455,49 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
             o[n][mt][2] *= cr0;
             o[n][mt][3] *= cr1;
           }
+          exponents();
         }
         // P is rounded to fp16 for the tensor core; the sums take the same rounded
         // values, so the output is a weighted mean of V under the rounded weights.
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint32_t w0 = F16::pack2(fast_exp2(sv[u][0] - mst[n][0]),
-                                         fast_exp2(sv[u][1] - mst[n][1]));
-          const uint32_t w1 = F16::pack2(fast_exp2(sv[u][2] - mst[n][0]),
-                                         fast_exp2(sv[u][3] - mst[n][1]));
+          const uint32_t w0 = F16::pack2(fast_exp2(a[u][0]), fast_exp2(a[u][1]));
+          const uint32_t w1 = F16::pack2(fast_exp2(a[u][2]), fast_exp2(a[u][3]));
           F16::add_halves(w0, lst[n][0], lst[n][1]);
           F16::add_halves(w1, lst[n][0], lst[n][1]);
-          pb[n][u][0] = movmatrix_trans(w0);
-          pb[n][u][1] = movmatrix_trans(w1);
+          pb[n][u][0] = transpose(w0);
+          pb[n][u][1] = transpose(w1);
         }
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        uint32_t vx[2][VW], vy[2][VW], sv[2];  // tokens 2t and 2t + 1 of tile 2u | 2u + 1
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint32_t tile = vst + (2 * u + r) * TL::kBytes;
-          const uint32_t src = tile + 2 * t4 * TL::kRowBytes + g8 * (D / 16);
-          const uint32_t ss = tile + TL::kScales + 2 * t4 * TL::kScaleBytes +
-                              (D == 128 ? g8 : g8 >> 1);
-          if constexpr (D == 128) {
-            const uint2 x = lds_v2(src), y = lds_v2(src + TL::kRowBytes);
-            vx[r][0] = x.x, vx[r][1] = x.y, vy[r][0] = y.x, vy[r][1] = y.y;
-          } else {
-            vx[r][0] = lds_u32(src);
-            vy[r][0] = lds_u32(src + TL::kRowBytes);
-          }
-          uint32_t sx = lds_u8(ss), sy = lds_u8(ss + TL::kScaleBytes);
-          if (left < kFp4StageTokens) {
-            // rows past the context hold anything: their scale, and so their value, is 0
-            const int t0 = 8 * (2 * u + r) + 2 * t4;
-            if (t0 >= left) sx = 0;
-            if (t0 + 1 >= left) sy = 0;
-          }
-          sv[r] = e4m3_to_f16x2(sx | sy << 8);
+        if constexpr (NG != 1) {
+          load_v(2 * u);
+          load_v(2 * u + 1);
         }
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
           uint32_t ev[2][4], od[2][4];  // elements 2b and 2b + 1 of the lane's words, both tokens
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const uint32_t x = vx[r][w], y = vy[r][w];
+            const uint32_t x = vx[2 * u + r][w], y = vy[2 * u + r][w];
             const uint32_t e = (x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u);
             const uint32_t d = ((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
             widen8(e, ev[r][0], ev[r][1], ev[r][2], ev[r][3]);
             widen8(d, od[r][0], od[r][1], od[r][2], od[r][3]);
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-              ev[r][b] = hmul2(ev[r][b], sv[r]);
-              od[r][b] = hmul2(od[r][b], sv[r]);
+              ev[r][b] = hmul2(ev[r][b], vf[2 * u + r]);
+              od[r][b] = hmul2(od[r][b], vf[2 * u + r]);
             }
           }
 #pragma unroll
           for (int b = 0; b < 4; ++b)
 #pragma unroll
             for (int n = 0; n < NG; ++n)
-              mma_16816<false>(o[n][4 * w + b], ev[0][b], od[0][b], ev[1][b], od[1][b],
-                               pb[n][u][0], pb[n][u][1]);
+              mma(o[n][4 * w + b], ev[0][b], od[0][b], ev[1][b], od[1][b], pb[n][u]);
         }
+      }
       }
       __syncwarp();  // every lane has read the stage
       if (f_end) ++issued;
@@ -422,7 +524,7 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
         const int h = 8 * n + 2 * t4 + hh;
         if (h >= nh) continue;
         const float l = lst[n][hh];
-        if (m.direct) {
+        if (m.whole) {
           // (a NaN sum, from a NaN query, stays)
           const float f = bad || l == 0.f ? 0.f : vs / l;
           uint32_t w[KSTEPS];
@@ -436,7 +538,7 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
           for (int i = 0; i < KSTEPS / 4; ++i)
             dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         } else {
-          const int64_t r = m.prow + h;
+          const int64_t r = (static_cast<int64_t>(m.b) * p.vh + m.g + m.chunk) * p.hs + h;
           const float f = bad ? 0.f : vs;
           float4 *dst = reinterpret_cast<float4 *>(p.ws_o + r * D + (D / 8) * g8);
 #pragma unroll
@@ -446,7 +548,7 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
                                        o[n][2 * i + 1][hh] * f, o[n][2 * i + 1][hh + 2] * f);
           if (g8 == 0)
             reinterpret_cast<float2 *>(p.ws_ml)[r] =
-                make_float2(bad ? -INFINITY : mst[n][hh], bad ? 0.f : l);
+                make_float2(bad ? -INFINITY : ref[n][hh], bad ? 0.f : l);
         }
       }
     }
@@ -461,8 +563,8 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NG))
   }
 }
 
-// Joins the pieces of each (sequence, query head) by log-sum-exp:
-//   M = max m_i, w_i = 2^(m_i - M), out = sum w_i o_i / sum w_i l_i.
+// Joins the pieces of each (sequence, query head), their references m_i, sums l_i and
+// unnormalised outputs o_i: M = max m_i, w_i = 2^(m_i - M), out = sum w_i o_i / sum w_i l_i.
 // One CTA of four warps per (sequence, query head); a lane holds D / 32 elements, warp w
 // takes pieces w, w + 4, ..., eight at a time.
 constexpr int kJoinWarps = 4, kJoinBatch = 8;
@@ -481,9 +583,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_fp4_join_kernel(const 
   const int total = p.ws_pref[p.num_seqs], pref = p.ws_pref[b];
   const int kvh = h / p.group, hg = h - kvh * p.group, slc = hg / p.hs;
   const int g = kvh * p.nc + slc;
-  const int C = dec::balanced_chunk(total, p.num_workers, p.chunk_cap);
-  const int U = pref + g * dec::ceil16(L);
-  const int c0 = U / C, n = (U + L - 1) / C - c0 + 1;
+  const int C = chunk_tokens(total, p.num_workers, p.chunk_cap);
+  const int U = pref + g * ceil32(L);
+  const int c0 = U / C, n = (U + ceil32(L) - 1) / C - c0 + 1;
   if (n <= 1) return;  // written by the decode kernel itself
   const int64_t row0 = (static_cast<int64_t>(b) * p.vh + g + c0) * p.hs + hg - slc * p.hs;
   const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);

@@ -1215,8 +1215,8 @@ pa_status fp4_plan(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, 
   const int64_t units = static_cast<int64_t>(num_kv_heads) * sl.nc;
   if (static_cast<int64_t>(max_context_len) > (1 << 30) ||
       (num_seqs > 0 &&
-       units * ((max_context_len + 15) / 16) * 16 > ((1LL << 30) - 1) / num_seqs) ||
-      num_seqs > pa::kFp4MostSeqs)
+       units * ((max_context_len + 31) / 32) * 32 > ((1LL << 30) - 1) / num_seqs) ||
+      num_seqs > pa::kFp4MostSeqs || num_kv_heads > 65536)
     return PA_ERR_UNSUPPORTED;
   const cudaError_t e = current_num_sms(sms);
   if (e != cudaSuccess) return cuda_fail(e);

@@ -199,34 +199,33 @@ struct DecodeArgs {
 };
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream);
 
-// The decode over 4-bit pools: CTAs of four warps, each a worker; the balanced split
-// over all of them, chunks of 16 tokens or more.
+// The decode over 4-bit pools: CTAs of four warps, each a worker with a ring of stages of
+// its own; the balanced split over all of them.
+#ifndef FP4_MIN
+#define FP4_MIN 32
+#endif
 constexpr int kFp4Warps = 4;
-constexpr int kFp4ChunkCap = 1 << 18;  // most tokens per chunk (workers x cap < 2^31)
-#ifndef FP4_CTAS
-#define FP4_CTAS 4
-#endif
-constexpr int fp4_ctas_per_sm(int ng) { return ng == 2 ? 3 : FP4_CTAS; }
-#ifndef FP4_STAGES
-#define FP4_STAGES 3
-#endif
-constexpr int kFp4StageTokens = 32;  // of a warp's stage
-constexpr int kFp4Stages = FP4_STAGES;
-constexpr int kFp4MostSeqs = 16384;  // prefix sums and lengths, 8 bytes each in shared memory
+constexpr int kFp4StageTokens = 64;
+constexpr int kFp4MinTokens = FP4_MIN;   // a worker's share, where there are fewer than workers
+constexpr int kFp4ChunkCap = 1 << 18;    // most tokens per chunk (workers x cap < 2^31)
+constexpr int kFp4MostSeqs = 8192;       // prefix sums and lengths, 8 bytes each in shared memory
+constexpr int fp4_stages(int head_dim) { return head_dim == 128 ? 2 : 3; }
+constexpr int fp4_ctas_per_sm(int head_dim, int ng) { return head_dim == 64 && ng == 1 ? 4 : 3; }
 // Shared memory: the stages (keys and values, 4.5 bits an element), a barrier each, then
 // prefix sums and lengths.
 inline int fp4_decode_smem(int head_dim, int num_seqs) {
-  return kFp4Warps * kFp4Stages * (kFp4StageTokens * head_dim * 9 / 8 + 8) +
+  return kFp4Warps * fp4_stages(head_dim) * (kFp4StageTokens * head_dim * 9 / 8 + 8) +
          4 * (2 * num_seqs + 1);
 }
 inline DecodeBalance fp4_balance(int num_seqs, int units, int ng, int head_dim, int max_ctx,
                                  int num_sms) {
   DecodeBalance d;
-  const int64_t t_max = static_cast<int64_t>(num_seqs) * units * ((max_ctx + 15) / 16) * 16;
+  const int64_t t_max = static_cast<int64_t>(num_seqs) * units * ((max_ctx + 31) / 32) * 32;
   // CTAs that are resident at once: 1 KB of an SM's 228 is taken for each
   int64_t most = 228 * 1024 / (fp4_decode_smem(head_dim, num_seqs) + 1024);
-  most = (most < fp4_ctas_per_sm(ng) ? most : fp4_ctas_per_sm(ng)) * num_sms;
-  int64_t grid = (t_max / 16 + kFp4Warps - 1) / kFp4Warps;
+  if (most > fp4_ctas_per_sm(head_dim, ng)) most = fp4_ctas_per_sm(head_dim, ng);
+  most *= num_sms;
+  int64_t grid = (t_max / kFp4MinTokens + kFp4Warps - 1) / kFp4Warps;
   grid = grid < 1 ? 1 : (grid > most ? most : grid);
   d.grid = static_cast<int>(grid);
   d.workers = d.grid * kFp4Warps;

@@ -136,7 +136,7 @@ DECODE = [(dict(s=-1), 2), (dict(mc=-1), 2), (dict(mb=-1), 2), (dict(hkv=3), 2),
           (dict(kc=3 * M + 8), 4), (dict(ks=8 * M + 2), 4), (dict(bt=5 * M + 2), 4),
           (dict(ctx=6 * M + 2), 4),
           # beyond the schedule's 32 bits, or its prefix sums' shared memory
-          (dict(s=1 << 10, mc=1 << 19), 3), (dict(mc=2**31 - 1), 3), (dict(s=16385, mc=16), 3)]
+          (dict(s=1 << 10, mc=1 << 19), 3), (dict(mc=2**31 - 1), 3), (dict(s=8193, mc=16), 3)]
 
 
 @pytest.mark.parametrize("new", [False, True])
@@ -159,7 +159,7 @@ def test_decode_write_refuses_what_the_write_refuses(lib, kw, status):
 
 
 def test_the_plan_refuses_what_the_call_refuses(lib):
-    for s, mc in ((1 << 10, 1 << 19), (4, 2**31 - 1), (16385, 16)):
+    for s, mc in ((1 << 10, 1 << 19), (4, 2**31 - 1), (8193, 16)):
         assert lib.pa_decode_fp4_plan(s, 8, 2, 128, mc, None) == 3
     for a in ((4, 8, 3, 128, 10), (-1, 8, 2, 128, 10), (4, 8, 2, 128, -1), (4, 0, 2, 128, 1)):
         assert lib.pa_decode_fp4_plan(*a, None) == 2
