@@ -565,11 +565,11 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
 
 // Joins the pieces of each (sequence, query head), their references m_i, sums l_i and
 // unnormalised outputs o_i: M = max m_i, w_i = 2^(m_i - M), out = sum w_i o_i / sum w_i l_i.
-// One CTA of four warps per (sequence, query head); a lane holds D / 32 elements, warp w
-// takes pieces w, w + 4, ..., eight at a time.
-constexpr int kJoinWarps = 4, kJoinBatch = 8;
+// One CTA per (sequence, query head); a lane holds D / 32 elements, warp w of W takes pieces
+// w, w + W, ..., eight at a time.
+constexpr int kJoinBatch = 8;
 
-template <class E, int D>
+template <class E, int D, int kJoinWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32) decode_fp4_join_kernel(const DecodeParams p) {
   constexpr int V = D / 32;
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_o[kJoinWarps][D];
@@ -598,8 +598,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_fp4_join_kernel(const 
       const int i = i0 + k * kJoinWarps;
       const int64_t r = row0 + static_cast<int64_t>(i < n ? i : i0) * p.hs;
       st[k] = i < n ? ml[r] : make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int v = 0; v < V; ++v) ov[k][v] = i < n ? p.ws_o[r * D + V * lane + v] : 0.f;
+      const float *src = p.ws_o + r * D + V * lane;
+      if constexpr (V == 4) {
+        const float4 x = i < n ? *reinterpret_cast<const float4 *>(src) : make_float4(0, 0, 0, 0);
+        ov[k][0] = x.x, ov[k][1] = x.y, ov[k][2] = x.z, ov[k][3] = x.w;
+      } else {
+        const float2 x = i < n ? *reinterpret_cast<const float2 *>(src) : make_float2(0, 0);
+        ov[k][0] = x.x, ov[k][1] = x.y;
+      }
     }
     float Mn = M;
 #pragma unroll
@@ -653,9 +659,13 @@ cudaError_t launch(const DecodeArgs &a, const DecodeParams &p, cudaStream_t stre
                  dim3(kWarps * 32), smem, stream, p, static_cast<const uint8_t *>(a.k_pool),
                  static_cast<const uint8_t *>(a.v_pool));
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_fp4_join_kernel<E, D>,
-                    dim3(static_cast<unsigned>(static_cast<int64_t>(a.num_seqs) * a.num_q_heads)),
-                    dim3(kJoinWarps * 32), 0, stream, p);
+  const dim3 rows(static_cast<unsigned>(static_cast<int64_t>(a.num_seqs) * a.num_q_heads));
+  // Units of many pieces take 16 warps a row (4 and 16, device us of the whole call: 125
+  // pieces, one sequence of 8000 tokens, 32/8 heads 12.8 and 11.0; 228, 30000, 64/8 27.1
+  // and 22.3; 62, 2 of 4000, 32/8 11.5 and 12.6).
+  const bool many = p.num_workers > 64LL * a.num_seqs * p.vh;
+  return many ? launch_pdl(decode_fp4_join_kernel<E, D, 16>, rows, dim3(16 * 32), 0, stream, p)
+              : launch_pdl(decode_fp4_join_kernel<E, D, 4>, rows, dim3(4 * 32), 0, stream, p);
 }
 
 template <class E>

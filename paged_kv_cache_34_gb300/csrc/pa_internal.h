@@ -201,12 +201,8 @@ cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream);
 
 // The decode over 4-bit pools: CTAs of four warps, each a worker with a ring of stages of
 // its own; the balanced split over all of them.
-#ifndef FP4_MIN
-#define FP4_MIN 32
-#endif
 constexpr int kFp4Warps = 4;
 constexpr int kFp4StageTokens = 64;
-constexpr int kFp4MinTokens = FP4_MIN;   // a worker's share, where there are fewer than workers
 constexpr int kFp4ChunkCap = 1 << 18;    // most tokens per chunk (workers x cap < 2^31)
 constexpr int kFp4MostSeqs = 8192;       // prefix sums and lengths, 8 bytes each in shared memory
 constexpr int fp4_stages(int head_dim) { return head_dim == 128 ? 2 : 3; }
@@ -225,7 +221,12 @@ inline DecodeBalance fp4_balance(int num_seqs, int units, int ng, int head_dim, 
   int64_t most = 228 * 1024 / (fp4_decode_smem(head_dim, num_seqs) + 1024);
   if (most > fp4_ctas_per_sm(head_dim, ng)) most = fp4_ctas_per_sm(head_dim, ng);
   most *= num_sms;
-  int64_t grid = (t_max / kFp4MinTokens + kFp4Warps - 1) / kFp4Warps;
+  // A worker takes 32 tokens at least, and 64 where that leaves 768 workers or more: fewer
+  // states to join (32 / 64 tokens throughout, device us; one sequence of 8000 tokens,
+  // 32/8 heads 17.7 / 11.2; 2 of 1500, 32/32 11.9 / 10.5; but 8 of 200, 32/8 7.3 / 9.0).
+  const int64_t shares = t_max / 32;
+  int64_t grid = shares <= 768 ? shares : (shares / 2 > 768 ? shares / 2 : 768);
+  grid = (grid + kFp4Warps - 1) / kFp4Warps;
   grid = grid < 1 ? 1 : (grid > most ? most : grid);
   d.grid = static_cast<int>(grid);
   d.workers = d.grid * kFp4Warps;
