@@ -565,8 +565,8 @@ pa_status pa_decode_write_fp8(void *out, int64_t out_row_stride, const void *que
  * then their scales, head_dim / 16 bytes a token.  Token s % block_size of block
  * s / block_size is slot s, as in the other pools, and pa_copy_blocks copies
  * blocks of num_kv_heads * block_size * 9 / 16 * head_dim bytes.
- * All calls: head_dim 64 or 128, block_size 8, 16, 32, 64 or 128, pools 16-byte
- * aligned, k_scale and v_scale device fp32 [num_kv_heads].
+ * All calls: up to 65536 KV heads, head_dim 64 or 128, block_size 8, 16, 32, 64
+ * or 128, pools 16-byte aligned, k_scale and v_scale device fp32 [num_kv_heads].
  */
 
 /*

@@ -1181,7 +1181,7 @@ pa_status prepare_write_fp4(const void *key, const void *value, int64_t kv_row_s
                                      num_blocks, dtype, d_error, out, empty);
   if (st != PA_OK) return st;
   if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
-  if (!valid_block_size(block_size)) return PA_ERR_UNSUPPORTED;
+  if (!valid_block_size(block_size) || num_kv_heads > 65536) return PA_ERR_UNSUPPORTED;
   if (!k_scale || !v_scale) return PA_ERR_NULL;
   if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u)
     return PA_ERR_ALIGN;
@@ -1321,7 +1321,8 @@ pa_status pa_gather_cache_fp4(void *key_out, int64_t k_out_row_stride, void *val
     return PA_ERR_SHAPE;
   if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
   if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
-  if (!valid_block_size(block_size) || num_seqs > 65535) return PA_ERR_UNSUPPORTED;
+  if (!valid_block_size(block_size) || num_seqs > 65535 || num_kv_heads > 65536)
+    return PA_ERR_UNSUPPORTED;
   const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
   if (k_out_row_stride < row || v_out_row_stride < row) return PA_ERR_SHAPE;
   if (num_rows > 0 && (k_out_row_stride > INT64_MAX / 4 / num_rows ||

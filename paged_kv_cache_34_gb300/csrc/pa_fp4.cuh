@@ -60,23 +60,67 @@ __device__ __forceinline__ uint32_t to_e2m1(const float *f) {
   return r;
 }
 
-// One group: 16 values -> 16 codes and their scale's byte.  With S the head's scale
-// (usable) and every operation in fp32, rounded to nearest:
-//   c = E4M3(max |x| / (6 S)), w = value(c) S, codes E2M1(x / w); c = 0: codes 0.
-// NaN counts as 0.  The quotients are the correctly rounded ones (div_rn_recip: w is
-// normal, w >= 2^-73).
-__device__ __forceinline__ uint2 quantise16(float (&x)[16], float S, uint32_t &scale) {
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    x[i] = x[i] != x[i] ? 0.f : x[i];
-    m = fmaxf(m, fabsf(x[i]));
+// The larger magnitudes of two pairs of 16-bit values; NaN where either is.
+template <class E>
+__device__ __forceinline__ typename E::T2 max_abs(typename E::T2 a, uint32_t w) {
+  return __hmax2_nan(a, __habs2(*reinterpret_cast<typename E::T2 *>(&w)));
+}
+
+// What a head's groups share: its scale S (0: unusable), 6 S and RN(1 / (6 S)).
+struct HeadScale {
+  float s, six, r;
+  __device__ __forceinline__ HeadScale(float S) {
+    s = head_scale_ok(S) ? S : 0.f;
+    six = __fmul_rn(6.f, S);
+    r = __frcp_rn(six);
   }
-  scale = to_e4m3(__fdiv_rn(m, __fmul_rn(6.f, S)));
-  if (scale == 0) return make_uint2(0, 0);
-  const float w = __fmul_rn(F16::lo(e4m3_to_f16x2(scale)), S), r = __frcp_rn(w);
+};
+
+// One group: 16 values (eight words of two) -> 16 codes and their scale's byte.  With S
+// the head's scale and every operation in fp32, rounded to nearest:
+//   c = E4M3(max |x| / (6 S)), w = value(c) S, codes E2M1(x / w); c = 0: codes 0.
+// NaN counts as 0.  Both divisors are normal numbers (w >= 2^-73), so their correctly
+// rounded quotients take a reciprocal, a product and two fused steps (div_rn_recip), and
+// while no value is NaN or infinite and c not at its end, none of its special cases.
+template <class E>
+__device__ __forceinline__ uint2 quantise16(const uint32_t (&v)[8], const HeadScale &h,
+                                            uint32_t &scale) {
+  scale = 0;
+  if (h.s == 0.f) return make_uint2(0, 0);
+  typename E::T2 m2 = max_abs<E>(*reinterpret_cast<const typename E::T2 *>(&v[0]), v[0]);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = div_rn_recip(x[i], w, r);
+  for (int i = 1; i < 8; ++i) m2 = max_abs<E>(m2, v[i]);
+  const uint32_t mw = *reinterpret_cast<const uint32_t *>(&m2);
+  float m = fmaxf(fabsf(E::lo(mw)), fabsf(E::hi(mw)));
+  const bool odd = !(fabsf(E::lo(mw)) + fabsf(E::hi(mw)) < INFINITY);
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = E::lo(v[i]);
+    x[2 * i + 1] = E::hi(v[i]);
+  }
+  if (odd) {
+    m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      x[i] = x[i] != x[i] ? 0.f : x[i];
+      m = fmaxf(m, fabsf(x[i]));
+    }
+  }
+  scale = to_e4m3(div_rn_recip(m, h.six, h.r));
+  if (scale == 0) return make_uint2(0, 0);
+  const float w = __fmul_rn(F16::lo(e4m3_to_f16x2(scale)), h.s), r = __frcp_rn(w);
+  if (odd || scale == 126) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = div_rn_recip(x[i], w, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      // (with the remainder negated, -0 stays -0: -(-0 w + 0) r - 0)
+      const float q = __fmul_rn(x[i], r);
+      x[i] = __fmaf_rn(-__fmaf_rn(q, w, -x[i]), r, q);
+    }
+  }
   return make_uint2(to_e2m1(x), to_e2m1(x + 8));
 }
 

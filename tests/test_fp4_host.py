@@ -71,7 +71,7 @@ def write(lib, **kw):
 
 
 WRITE = [(dict(n=-1), 2), (dict(hkv=0), 2), (dict(bs=0), 2), (dict(nb=-1), 2), (dict(nb=1 << 60), 2),
-         (dict(d=96), 3), (dict(d=32), 3), (dict(bs=24), 3), (dict(bs=4), 3), (dict(dtype=7), 3),
+         (dict(d=96), 3), (dict(d=32), 3), (dict(hkv=65537, kvs=1 << 24), 3), (dict(bs=24), 3), (dict(bs=4), 3), (dict(dtype=7), 3),
          (dict(k=0), 1), (dict(v=0), 1), (dict(kc=0), 1), (dict(vc=0), 1), (dict(sm=0), 1),
          (dict(ks=0), 1), (dict(vs=0), 1), (dict(kvs=248), 2), (dict(kvs=260), 4),
          (dict(k=M + 8), 4), (dict(kc=3 * M + 8), 4), (dict(ks=6 * M + 2), 4),
@@ -99,7 +99,7 @@ def gather(lib, **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(r=-1), 2), (dict(mb=-1), 2), (dict(s=-1), 2), (dict(mc=-1), 2), (dict(hkv=0), 2),
     (dict(bs=0), 2), (dict(nb=-1), 2), (dict(bts=7), 2), (dict(dtype=2), 3), (dict(d=80), 3),
-    (dict(bs=256), 3), (dict(s=65536), 3), (dict(kos=248), 2), (dict(vos=248), 2),
+    (dict(bs=256), 3), (dict(s=65536), 3), (dict(hkv=65537, kos=1 << 24, vos=1 << 24), 3), (dict(kos=248), 2), (dict(vos=248), 2),
     (dict(kos=260), 4), (dict(vos=1 << 62), 2), (dict(ko=0), 1), (dict(vo=0), 1), (dict(kc=0), 1),
     (dict(vc=0), 1), (dict(bt=0), 1), (dict(ctx=0), 1), (dict(rs=0), 1), (dict(ks=0), 1),
     (dict(vs=0), 1), (dict(ko=M + 8), 4), (dict(vo=2 * M + 2), 4), (dict(kc=3 * M + 4), 4),
@@ -136,7 +136,8 @@ DECODE = [(dict(s=-1), 2), (dict(mc=-1), 2), (dict(mb=-1), 2), (dict(hkv=3), 2),
           (dict(kc=3 * M + 8), 4), (dict(ks=8 * M + 2), 4), (dict(bt=5 * M + 2), 4),
           (dict(ctx=6 * M + 2), 4),
           # beyond the schedule's 32 bits, or its prefix sums' shared memory
-          (dict(s=1 << 10, mc=1 << 19), 3), (dict(mc=2**31 - 1), 3), (dict(s=8193, mc=16), 3)]
+          (dict(s=1 << 10, mc=1 << 19), 3), (dict(mc=2**31 - 1), 3), (dict(s=8193, mc=16), 3),
+          (dict(hq=65537, hkv=65537, qs=1 << 24, os=1 << 24), 3)]
 
 
 @pytest.mark.parametrize("new", [False, True])
