@@ -201,32 +201,41 @@ def pa_reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, *,
     _check(lib, st, "pa_reshape_and_cache")
 
 
+def _row(t, d, name):
+    """_rows of a tensor that is known to have three dimensions, the last d."""
+    st = t.stride()
+    if st[1] != d or st[2] != 1:
+        raise ValueError(f"{name} must be [rows, heads, head_dim] with contiguous heads")
+    return st[0]
+
+
 def _rope(what, query_out, key_out, query, key, value, key_cache, value_cache, slot_mapping,
           positions, cos_sin, interleaved, q_weight, k_weight, eps, d_error, stream, lib):
     lib = lib or _lib or library()
-    t, hq, d = query.shape
-    tk, hkv, dk = key.shape
-    dtype, dev = query.dtype, query.get_device()
-    if query_out.shape != query.shape or tk != t or dk != d:
+    shape, kshape, dtype, dev = query.shape, key.shape, query.dtype, query.get_device()
+    t, hq, d = shape
+    tk, hkv, dk = kshape
+    if query_out.shape != shape or tk != t or dk != d:
         raise ValueError("query_out/query must be [T, Hq, D] and key [T, Hkv, D]")
     if dtype not in _DTYPE or query_out.dtype is not dtype or key.dtype is not dtype:
         raise ValueError("query_out, query and key must share a dtype, float16 or bfloat16")
     if query_out.get_device() != dev or key.get_device() != dev:
         _bad_device("query_out or key", dev)
-    os, qs, ks = _rows(query_out, "query_out"), _rows(query, "query"), _rows(key, "key")
+    ks = _row(key, d, "key")
     kos = ko = v = kc = vc = sm = pos = cs = qw = kw = None
     rot = most = bs = nb = 0
     if key_out is not None:
-        if key_out.shape != key.shape or key_out.dtype is not dtype:
+        if key_out.shape != kshape or key_out.dtype is not dtype:
             raise ValueError("key_out must be like key")
         if key_out.get_device() != dev:
             _bad_device("key_out", dev)
-        kos, ko = _rows(key_out, "key_out"), key_out.data_ptr()
+        kos, ko = _row(key_out, d, "key_out"), key_out.data_ptr()
     if key_cache is not None:
-        nb, bs, hc, dc = key_cache.shape
-        if value.shape != key.shape or value.dtype is not dtype or _rows(value, "value") != ks:
+        cshape = key_cache.shape
+        nb, bs, hc, dc = cshape
+        if value.shape != kshape or value.dtype is not dtype or _row(value, d, "value") != ks:
             raise ValueError("value must be like key, with its row stride")
-        if hc != hkv or dc != d or value_cache.shape != key_cache.shape \
+        if hc != hkv or dc != d or value_cache.shape != cshape \
                 or key_cache.dtype is not dtype or value_cache.dtype is not dtype \
                 or not key_cache.is_contiguous() or not value_cache.is_contiguous():
             raise ValueError("caches must be contiguous [num_blocks, block_size, Hkv, D] of key's "
@@ -249,20 +258,27 @@ def _rope(what, query_out, key_out, query, key, value, key_cache, value_cache, s
             _bad_vector(positions, t, torch.int32, "positions", dev)
         most, rot = cos_sin.shape
         pos, cs = positions.data_ptr(), cos_sin.data_ptr()
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.dtype is not dtype or w.numel() != d or not w.is_contiguous()
-                              or w.get_device() != dev):
-            _bad_vector(w, d, dtype, name, dev)
+    if q_weight is not None:
+        qw = _weight(q_weight, d, dtype, "q_weight", dev)
+    if k_weight is not None:
+        kw = _weight(k_weight, d, dtype, "k_weight", dev)
     if d_error is not None:
         _check_error(d_error, dev)
+        d_error = d_error.data_ptr()
     _current(dev)
     st = lib.pa_rope_and_cache(
-        query_out.data_ptr(), os, ko, kos or 0, query.data_ptr(), qs, key.data_ptr(), v, ks, pos,
-        cs, most, rot, 1 if interleaved else 0, None if q_weight is None else q_weight.data_ptr(),
-        None if k_weight is None else k_weight.data_ptr(), eps, kc, vc, sm, t, hq, hkv, d, bs, nb,
-        _DTYPE[dtype], None if d_error is None else d_error.data_ptr(), _raw_stream(stream, dev))
+        query_out.data_ptr(), _row(query_out, d, "query_out"), ko, kos or 0, query.data_ptr(),
+        _row(query, d, "query"), key.data_ptr(), v, ks, pos, cs, most, rot,
+        1 if interleaved else 0, qw, kw, eps, kc, vc, sm, t, hq, hkv, d, bs, nb, _DTYPE[dtype],
+        d_error, _raw_stream(stream, dev))
     if st:
         _check(lib, st, what)
+
+
+def _weight(w, d, dtype, name, dev):
+    if w.dtype is not dtype or w.numel() != d or not w.is_contiguous() or w.get_device() != dev:
+        _bad_vector(w, d, dtype, name, dev)
+    return w.data_ptr()
 
 
 def pa_rope_and_cache(query_out, query, key, value, key_cache, value_cache, slot_mapping, positions,
@@ -343,35 +359,39 @@ def pa_reshape_and_cache_fp8(key, value, key_cache, value_cache, slot_mapping, k
 
 def _pools4(key_cache, value_cache, dev):
     """(num_blocks, num_kv_heads, block_size, head_dim) of a pair of FP4 pools."""
+    shape = key_cache.shape
     if key_cache.dtype is not torch.uint8 or value_cache.dtype is not torch.uint8 \
-            or key_cache.dim() != 4 or value_cache.shape != key_cache.shape \
+            or len(shape) != 4 or value_cache.shape != shape or shape[3] % 9 \
             or not key_cache.is_contiguous() or not value_cache.is_contiguous():
         raise ValueError("FP4 caches must be contiguous uint8 [num_blocks, Hkv, block_size / 8, "
                          "9 * head_dim / 2]")
     if key_cache.get_device() != dev or value_cache.get_device() != dev:
         _bad_device("caches", dev)
-    nb, hkv, tiles, width = key_cache.shape
-    if width % 9:
-        raise ValueError("an FP4 cache's tiles are 9 * head_dim / 2 bytes")
+    nb, hkv, tiles, width = shape
     return nb, hkv, 8 * tiles, width // 9 * 2
 
 
-def _scales4(t, hkv, dev, what):
-    if t.dtype is not torch.float32 or t.numel() != hkv or not t.is_contiguous() \
-            or t.get_device() != dev:
-        _bad_vector(t, hkv, torch.float32, what, dev)
-    return t.data_ptr()
+def _scales4(k, v, hkv, dev):
+    f32 = torch.float32
+    if not (k.dtype is f32 and v.dtype is f32 and k.numel() == hkv and v.numel() == hkv
+            and k.is_contiguous() and v.is_contiguous() and k.get_device() == dev
+            and v.get_device() == dev):
+        for t, what in ((k, "k_scale"), (v, "v_scale")):
+            if t.dtype is not f32 or t.numel() != hkv or not t.is_contiguous() \
+                    or t.get_device() != dev:
+                _bad_vector(t, hkv, f32, what, dev)
+    return k.data_ptr(), v.data_ptr()
 
 
 def _new_rows4(key, value, slot_mapping, hkv, d, dev):
     """(row stride, token count) of the rows that a write into FP4 pools takes."""
-    ks = _rows(key, "key")
-    if key.dtype not in _DTYPE or value.dtype is not key.dtype or value.shape != key.shape \
-            or key.shape[1] != hkv or key.shape[2] != d:
+    shape, dtype = key.shape, key.dtype
+    n, h, dk = shape
+    if dtype not in _DTYPE or value.dtype is not dtype or value.shape != shape or h != hkv or dk != d:
         raise ValueError("key and value must be [N, Hkv, D] of one dtype, float16 or bfloat16")
-    if _rows(value, "value") != ks:
+    ks = _row(key, d, "key")
+    if _row(value, d, "value") != ks:
         raise ValueError("key and value must share a row stride")
-    n = key.shape[0]
     if key.get_device() != dev or value.get_device() != dev:
         _bad_device("key or value", dev)
     if slot_mapping.dtype is not torch.int64 or slot_mapping.numel() != n \
@@ -389,7 +409,7 @@ def pa_reshape_and_cache_fp4(key, value, key_cache, value_cache, slot_mapping, k
     dev = key.get_device()
     nb, hkv, bs, d = _pools4(key_cache, value_cache, dev)
     ks, n = _new_rows4(key, value, slot_mapping, hkv, d, dev)
-    k_sc, v_sc = _scales4(k_scale, hkv, dev, "k_scale"), _scales4(v_scale, hkv, dev, "v_scale")
+    k_sc, v_sc = _scales4(k_scale, v_scale, hkv, dev)
     if d_error is not None:
         _check_error(d_error, dev)
     _current(dev)
@@ -430,13 +450,13 @@ def pa_gather_cache_fp4(key_out, value_out, key_cache, value_cache, block_table,
                          "bfloat16")
     if value_out.get_device() != dev:
         _bad_device("value_out", dev)
-    ks, vs = _rows(key_out, "key_out"), _rows(value_out, "value_out")
+    ks, vs = _row(key_out, d, "key_out"), _row(value_out, d, "value_out")
     stride, width = _table4(block_table, s, dev)
     for t, name in ((context_lens, "context_lens"), (row_starts, "row_starts")):
         if t.dtype is not torch.int32 or t.numel() != s or t.get_device() != dev \
                 or not t.is_contiguous():
             _bad_vector(t, s, torch.int32, name, dev)
-    k_sc, v_sc = _scales4(k_scale, hkv, dev, "k_scale"), _scales4(v_scale, hkv, dev, "v_scale")
+    k_sc, v_sc = _scales4(k_scale, v_scale, hkv, dev)
     max_context_len = _bound(max_context_len, "max_context_len")
     if d_error is not None:
         _check_error(d_error, dev)
@@ -775,12 +795,12 @@ def _decode4(what, out, query, new, key_cache, value_cache, block_table, context
     nb, hkv, bs, d = _pools4(key_cache, value_cache, dev)
     if out.shape != query.shape or dq != d or dtype not in _DTYPE or out.dtype is not dtype:
         raise ValueError("out/query must be [S, Hq, D] of one dtype, float16 or bfloat16")
-    os, qs = _rows(out, "out"), _rows(query, "query")
+    os, qs = _row(out, d, "out"), _row(query, d, "query")
     stride, width = _table4(block_table, s, dev)
     if context_lens.dtype is not torch.int32 or context_lens.numel() != s \
             or context_lens.get_device() != dev or not context_lens.is_contiguous():
         _bad_vector(context_lens, s, torch.int32, "context_lens", dev)
-    k_sc, v_sc = _scales4(k_scale, hkv, dev, "k_scale"), _scales4(v_scale, hkv, dev, "v_scale")
+    k_sc, v_sc = _scales4(k_scale, v_scale, hkv, dev)
     if out.get_device() != dev or workspace is not None and workspace.get_device() != dev:
         _bad_device("out or workspace", dev)
     max_context_len = _bound(max_context_len, "max_context_len")
