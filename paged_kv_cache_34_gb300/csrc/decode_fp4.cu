@@ -37,7 +37,8 @@ __host__ __device__ __forceinline__ int ceil32(int x) { return (x + 31) & ~31; }
 // The balanced split: the units' contexts, each rounded up to 32 tokens, end to end, cut
 // into chunks of a multiple of 32, at most one or two per worker (32-bit arithmetic is
 // exact while total < 2^30 and workers * cap < 2^31).  So a piece starts at a multiple of
-// 32 of its sequence, and a stage of 32 tokens lies in one block of 32 or more.
+// 32 of its sequence.  Where the bound is a few stages, units are chunks instead, all of
+// the bound's length (partition_size), and nothing is joined.
 __device__ __forceinline__ int chunk_tokens(int total, int workers, int cap) {
   const uint32_t t = total, per = static_cast<uint32_t>(workers) * cap;
   const uint32_t n = (t > per ? (t + per - 1) / per : 1u) * workers;
@@ -72,13 +73,15 @@ __device__ inline bool next_piece(const DecodeParams &p, const int *pref, const 
       if (pref[mid] <= cu.at) lo = mid;
       else hi = mid;
     }
-    const int L = len[lo], W = ceil32(L), rel = cu.at - pref[lo];
+    const int L = len[lo], W = p.partition_size ? p.partition_size : ceil32(L);
+    const int rel = cu.at - pref[lo];
     m.b = lo;
     m.g = rel / W;
     m.start = rel - m.g * W;
     const int stop = min(W, m.start + (end - cu.at));
     cu.at += stop - m.start;
     m.end = min(stop, L);
+    if (m.end <= m.start) continue;  // (an empty sequence, where units are one chunk each)
     m.chunk = cu.chunk;
     m.whole = m.start == 0 && stop == W;
     return true;
@@ -182,7 +185,7 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
         const int L = checked_context_len(__ldg(p.context_lens + b), p.capacity, p.max_ctx, p.err,
                                           blockIdx.x == 0);
         s_len[b] = L;
-        items = ceil32(L) * p.vh;
+        items = (p.partition_size ? p.partition_size : ceil32(L)) * p.vh;
       }
       int incl = items;
 #pragma unroll
@@ -197,7 +200,9 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
   }
   __syncthreads();
   const int total = s_pref[nseq];
-  const int C = chunk_tokens(total, p.num_workers, p.chunk_cap), chunks = (total + C - 1) / C;
+  const int C =
+      p.partition_size ? p.partition_size : chunk_tokens(total, p.num_workers, p.chunk_cap);
+  const int chunks = (total + C - 1) / C;
   const int gw = blockIdx.x * kWarps + warp;
   if (blockIdx.x == 0)
     for (int i = tid; i <= nseq; i += blockDim.x) p.ws_pref[i] = s_pref[i];
@@ -565,16 +570,18 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
 
 // Joins the pieces of each (sequence, query head), their references m_i, sums l_i and
 // unnormalised outputs o_i: M = max m_i, w_i = 2^(m_i - M), out = sum w_i o_i / sum w_i l_i.
-// One CTA per (sequence, query head); a lane holds D / 32 elements, warp w of W takes pieces
-// w, w + W, ..., eight at a time.
+// A group of W warps per (sequence, query head); a lane holds D / 32 elements, warp w of them
+// takes pieces w, w + W, ..., eight at a time.
 constexpr int kJoinBatch = 8;
 
-template <class E, int D, int kJoinWarps>
-__global__ void __launch_bounds__(kJoinWarps * 32) decode_fp4_join_kernel(const DecodeParams p) {
+template <class E, int D, int W>
+__global__ void __launch_bounds__(W < 4 ? 128 : W * 32) decode_fp4_join_kernel(const DecodeParams p) {
   constexpr int V = D / 32;
-  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_o[kJoinWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.x / p.hq, h = blockIdx.x - b * p.hq;
+  __shared__ float s_m[W], s_l[W], s_o[W][D];  // (used where W > 1)
+  const int warp = W == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = W == 1 ? blockIdx.x * 4LL + (threadIdx.x >> 5) : blockIdx.x;
+  if (row >= static_cast<int64_t>(p.num_seqs) * p.hq) return;
+  const int b = static_cast<int>(row / p.hq), h = static_cast<int>(row - static_cast<int64_t>(b) * p.hq);
   // (context_lens is no output of the launch before: read while that runs)
   const int L = checked_context_len(__ldg(p.context_lens + b), p.capacity, p.max_ctx, p.err, false);
   griddep_wait();
@@ -590,12 +597,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_fp4_join_kernel(const 
   const int64_t row0 = (static_cast<int64_t>(b) * p.vh + g + c0) * p.hs + hg - slc * p.hs;
   const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
   float M = -INFINITY, l = 0.f, acc[V] = {};
-  for (int i0 = warp; i0 < n; i0 += kJoinWarps * kJoinBatch) {
+  for (int i0 = warp; i0 < n; i0 += W * kJoinBatch) {
     float2 st[kJoinBatch];
     float ov[kJoinBatch][V];
 #pragma unroll
     for (int k = 0; k < kJoinBatch; ++k) {
-      const int i = i0 + k * kJoinWarps;
+      const int i = i0 + k * W;
       const int64_t r = row0 + static_cast<int64_t>(i < n ? i : i0) * p.hs;
       st[k] = i < n ? ml[r] : make_float2(-INFINITY, 0.f);
       const float *src = p.ws_o + r * D + V * lane;
@@ -624,30 +631,35 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_fp4_join_kernel(const 
     }
     M = Mn;
   }
-  if (lane == 0) {
-    s_m[warp] = M;
-    s_l[warp] = l;
+  if constexpr (W > 1) {
+    if (lane == 0) {
+      s_m[warp] = M;
+      s_l[warp] = l;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = acc[v];
+    __syncthreads();
+    if (warp != 0) return;
+    M = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) M = fmaxf(M, s_m[w]);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = s_m[w] == -INFINITY ? 1.f : exp2f(s_m[w] - M);
+      l += f * s_l[w];
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += f * s_o[w][lane * V + v];
+    }
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = acc[v];
-  __syncthreads();
-  if (warp != 0) return;
-  float Mt = -INFINITY, lt = 0.f, out[V] = {};
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) Mt = fmaxf(Mt, s_m[w]);
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    const float f = s_m[w] == -INFINITY ? 1.f : exp2f(s_m[w] - Mt);
-    lt += f * s_l[w];
-#pragma unroll
-    for (int v = 0; v < V; ++v) out[v] += f * s_o[w][lane * V + v];
-  }
-  const float inv = lt == 0.f ? 0.f : 1.f / lt;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   typename E::T *dst =
       static_cast<typename E::T *>(p.out) + b * p.out_row_stride + h * D + lane * V;
 #pragma unroll
   for (int v = 0; v < V; v += 2)
-    *reinterpret_cast<uint32_t *>(dst + v) = E::pack2(out[v] * inv, out[v + 1] * inv);
+    *reinterpret_cast<uint32_t *>(dst + v) = E::pack2(acc[v] * inv, acc[v + 1] * inv);
 }
 
 template <class E, int D, int NG>
@@ -659,13 +671,22 @@ cudaError_t launch(const DecodeArgs &a, const DecodeParams &p, cudaStream_t stre
                  dim3(kWarps * 32), smem, stream, p, static_cast<const uint8_t *>(a.k_pool),
                  static_cast<const uint8_t *>(a.v_pool));
   if (e != cudaSuccess) return e;
-  const dim3 rows(static_cast<unsigned>(static_cast<int64_t>(a.num_seqs) * a.num_q_heads));
-  // Units of many pieces take 16 warps a row (4 and 16, device us of the whole call: 125
+  if (p.partition_size) return cudaSuccess;  // every piece is its unit's whole context
+  // 16 warps a row for units of many pieces (4 and 16, device us of the whole call: 125
   // pieces, one sequence of 8000 tokens, 32/8 heads 12.8 and 11.0; 228, 30000, 64/8 27.1
-  // and 22.3; 62, 2 of 4000, 32/8 11.5 and 12.6).
-  const bool many = p.num_workers > 64LL * a.num_seqs * p.vh;
-  return many ? launch_pdl(decode_fp4_join_kernel<E, D, 16>, rows, dim3(16 * 32), 0, stream, p)
-              : launch_pdl(decode_fp4_join_kernel<E, D, 4>, rows, dim3(4 * 32), 0, stream, p);
+  // and 22.3; 62, 2 of 4000, 32/8 11.5 and 12.6), one for units of few (1 and 4: 1, 256 of
+  // 133 to 200, 32/8 31.4 and 40.3; 7, 8 of 512 to 2048, 32/32 21.2 and 21.7; 14, 16 of
+  // 1300 to 2000, 32/8 19.9 and 18.4).
+  const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
+  const int64_t units = static_cast<int64_t>(a.num_seqs) * p.vh;
+  if (p.num_workers > 64 * units)
+    return launch_pdl(decode_fp4_join_kernel<E, D, 16>, dim3(static_cast<unsigned>(rows)),
+                      dim3(512), 0, stream, p);
+  if (p.num_workers > 8 * units)
+    return launch_pdl(decode_fp4_join_kernel<E, D, 4>, dim3(static_cast<unsigned>(rows)),
+                      dim3(128), 0, stream, p);
+  return launch_pdl(decode_fp4_join_kernel<E, D, 1>, dim3(static_cast<unsigned>((rows + 3) / 4)),
+                    dim3(128), 0, stream, p);
 }
 
 template <class E>
@@ -683,6 +704,9 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t stream) {
                                       a.head_dim, a.max_context_len, a.num_sms);
   p.num_workers = d.workers;
   p.chunk_cap = kFp4ChunkCap;
+  const int64_t units = static_cast<int64_t>(a.num_seqs) * p.vh;
+  p.partition_size =
+      fp4_whole_units(a.max_context_len, units) ? (a.max_context_len + 31) / 32 * 32 : 0;
   return a.dtype == PA_BF16 ? fp4::launch_type<BF16>(a, p, stream)
                             : fp4::launch_type<F16>(a, p, stream);
 }

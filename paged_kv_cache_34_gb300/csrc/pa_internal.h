@@ -207,6 +207,12 @@ constexpr int kFp4ChunkCap = 1 << 18;    // most tokens per chunk (workers x cap
 constexpr int kFp4MostSeqs = 8192;       // prefix sums and lengths, 8 bytes each in shared memory
 constexpr int fp4_stages(int head_dim) { return head_dim == 128 ? 2 : 3; }
 constexpr int fp4_ctas_per_sm(int head_dim, int ng) { return head_dim == 64 && ng == 1 ? 4 : 3; }
+// Short contexts are not cut: no states, no second launch (cut / whole, device us: 4
+// sequences of 64 / 128 / 192 tokens, 8/2 heads of 64, 5.9 / 4.4, 6.0 / 5.6, 5.9 / 6.7; 32,
+// 32/8 8.4 / 5.6, 10.0 / 7.2, 10.9 / 8.8; 256 of 128 / 256 22.0 / 20.4, 32.5 / 31.4).
+inline bool fp4_whole_units(int max_ctx, int64_t units) {
+  return max_ctx > 0 && max_ctx <= (units < 128 ? 128 : 256);
+}
 // Shared memory: the stages (keys and values, 4.5 bits an element), a barrier each, then
 // prefix sums and lengths.
 inline int fp4_decode_smem(int head_dim, int num_seqs) {
@@ -226,6 +232,8 @@ inline DecodeBalance fp4_balance(int num_seqs, int units, int ng, int head_dim, 
   // 32/8 heads 17.7 / 11.2; 2 of 1500, 32/32 11.9 / 10.5; but 8 of 200, 32/8 7.3 / 9.0).
   const int64_t shares = t_max / 32;
   int64_t grid = shares <= 768 ? shares : (shares / 2 > 768 ? shares / 2 : 768);
+  const int64_t all = static_cast<int64_t>(num_seqs) * units;
+  if (fp4_whole_units(max_ctx, all)) grid = all;
   grid = (grid + kFp4Warps - 1) / kFp4Warps;
   grid = grid < 1 ? 1 : (grid > most ? most : grid);
   d.grid = static_cast<int>(grid);

@@ -231,6 +231,7 @@ def test_groups(grp, dtype):
     ([50, 2000, 130, 0, 777, 1999, 64, 51], 32, 8, 128, 32),
     ([40001, 20000], 64, 8, 128, 128), ([9000], 8, 1, 64, 64), ([20000, 3], 128, 8, 128, 32),
     ([16] * 700, 8, 2, 64, 8), ([1] * 1500 + [0] * 30, 4, 2, 64, 16),
+    ([200, 1, 0, 256, 130, 33] * 16, 8, 2, 128, 16), ([256, 128, 0, 129] * 4, 16, 8, 64, 32),
 ])
 def test_long_and_many(lens, hq, hkv, d, bs):
     run(lens, hq, hkv, d, bs, torch.bfloat16 if hkv == 8 else torch.float16, len(lens) + hq)
