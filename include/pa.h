@@ -185,8 +185,11 @@ pa_status pa_reshape_and_cache(const void *key, const void *value,
  *   slot_mapping all NULL: nothing is written to a cache (then key_out is
  *                required, and value, block_size and num_blocks are not used).
  * Outputs may not overlap inputs or each other otherwise (PA_ERR_SHAPE); columns
- * of one buffer's rows side by side are no overlap.
- * Supported: fp16 / bf16, head_dim 64 or 128, any numbers of heads and any
+ * of one buffer's rows side by side are no overlap.  The pools lie apart from all
+ * of them (not checked).  Over the other pools' formats the same takes two calls: this
+ * one without a cache, in place, then the format's write.
+ * The sum of a row's squares has to stay within fp32.
+ * Supported: fp16 / bf16, head_dim 64 or 128, up to 65536 query and KV heads, any
  * block_size.
  */
 pa_status pa_rope_and_cache(void *query_out, int64_t q_out_row_stride, void *key_out,

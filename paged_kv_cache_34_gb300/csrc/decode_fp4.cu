@@ -141,6 +141,20 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
+// A stage's wait, bounded.  The first test does not block (a blocking one can take longer than
+// a short bound), and a bound below the timer's resolution (1 us) leaves it at that.
+__device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (ok) return true;
+  return limit_ns >= 1000 && mbar_wait_bounded(bar, parity, limit_ns);
+}
 // Untiled copy of `bytes` (a multiple of 16) into shared memory, both ends 16-byte aligned.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
                                           uint32_t bar) {
@@ -312,7 +326,7 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
 #pragma unroll 1
     for (int j0 = m.start; j0 < m.end; j0 += kTokens) {
       // (one lane's wait running out ends the warp's)
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(full + 8 * s, phase, p.wait_ns))) {
+      if (!__all_sync(0xffffffffu, wait_stage(full + 8 * s, phase, p.wait_ns))) {
         if (lane == 0) raise_error(p.err, PA_DEVERR_TIMEOUT);
         alive = false;
         break;
@@ -671,18 +685,19 @@ cudaError_t launch(const DecodeArgs &a, const DecodeParams &p, cudaStream_t stre
                  dim3(kWarps * 32), smem, stream, p, static_cast<const uint8_t *>(a.k_pool),
                  static_cast<const uint8_t *>(a.v_pool));
   if (e != cudaSuccess) return e;
-  if (p.partition_size) return cudaSuccess;  // every piece is its unit's whole context
+  // nothing to join: every piece is its unit's whole context, or every context is empty
+  if (p.partition_size || a.max_context_len == 0) return cudaSuccess;
   // 16 warps a row for units of many pieces (4 and 16, device us of the whole call: 125
   // pieces, one sequence of 8000 tokens, 32/8 heads 12.8 and 11.0; 228, 30000, 64/8 27.1
   // and 22.3; 62, 2 of 4000, 32/8 11.5 and 12.6), one for units of few (1 and 4: 1, 256 of
-  // 133 to 200, 32/8 31.4 and 40.3; 7, 8 of 512 to 2048, 32/32 21.2 and 21.7; 14, 16 of
-  // 1300 to 2000, 32/8 19.9 and 18.4).
+  // 133 to 200, 32/8 31.4 and 40.3; 4, 64 of 2700 to 4000, 32/8 57.5 and 60.2; 6.5, 32 of 50
+  // to 2000, 32/8 15.7 and 14.9).
   const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
   const int64_t units = static_cast<int64_t>(a.num_seqs) * p.vh;
   if (p.num_workers > 64 * units)
     return launch_pdl(decode_fp4_join_kernel<E, D, 16>, dim3(static_cast<unsigned>(rows)),
                       dim3(512), 0, stream, p);
-  if (p.num_workers > 8 * units)
+  if (p.num_workers > 4 * units)
     return launch_pdl(decode_fp4_join_kernel<E, D, 4>, dim3(static_cast<unsigned>(rows)),
                       dim3(128), 0, stream, p);
   return launch_pdl(decode_fp4_join_kernel<E, D, 1>, dim3(static_cast<unsigned>((rows + 3) / 4)),

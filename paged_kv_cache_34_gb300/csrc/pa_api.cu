@@ -287,6 +287,7 @@ pa_status pa_rope_and_cache(void *query_out, int64_t q_out_row_stride, void *key
   if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
   if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
   if (rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+  if (num_q_heads > 65536 || num_kv_heads > 65536) return PA_ERR_UNSUPPORTED;
   if (num_tokens == 0) return PA_OK;
   if (!query_out || !query || !key || (!cache && !key_out)) return PA_ERR_NULL;
   if (cache && (!key_cache || !value_cache || !slot_mapping || !value)) return PA_ERR_NULL;

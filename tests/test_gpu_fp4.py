@@ -403,3 +403,52 @@ def test_copy_blocks():
     torch.cuda.synchronize()
     for a, b in zip(pools, before):
         assert torch.equal(a[pairs[0, 1]], b[pairs[0, 0]])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_wait_that_runs_out(d):
+    # pools larger than L2, so that copies are waited for longer than one try of a wait
+    # takes; the launches after it are as before
+    lens = [4000] * (48 if d == 128 else 96)
+    table, pools, scales, _ = state(lens, 8, d, 128, 15)
+    q = torch.randn(len(lens), 8, d, generator=gen(16), device=DEV).half()
+    first, again, err = torch.empty_like(q), torch.empty_like(q), new_err()
+    args = (q, *pools, table, i32(lens), *scales)
+    pa.pa_decode_fp4(first, *args, scale=0.1, max_context_len=4000)
+    pa.pa_debug_set_wait_limit_ns(1)
+    try:
+        pa.pa_decode_fp4(again, *args, scale=0.1, max_context_len=4000, d_error=err)
+        torch.cuda.synchronize()
+    finally:
+        pa.pa_debug_set_wait_limit_ns(0)
+    assert int(err) == pa.DEVERR_TIMEOUT
+    err.zero_()
+    for _ in range(3):
+        pa.pa_decode_fp4(again, *args, scale=0.1, max_context_len=4000, d_error=err)
+        assert torch.equal(first, again)
+    done(err)
+
+
+def test_empty_calls():
+    table, pools, scales, _ = state([40, 5], 2, 64, 16, 17)
+    before = [p.clone() for p in pools]
+    q = torch.full((2, 8, 64), 3.0, dtype=torch.float16, device=DEV)
+    out, err = torch.full_like(q, 7.0), new_err()
+    pa.pa_decode_fp4(out, q, *pools, table, i32([0, 0]), *scales, scale=0.1, max_context_len=0,
+                     d_error=err)
+    done(err)
+    assert bool((out == 0).all())
+    none = torch.empty(0, 2, 64, dtype=torch.float16, device=DEV)
+    slots = torch.empty(0, dtype=torch.int64, device=DEV)
+    pa.pa_reshape_and_cache_fp4(none, none, *pools, slots, *scales, d_error=err)
+    pa.pa_gather_cache_fp4(none, none, *pools, table, i32([0, 0]), i32([9, -1]), *scales,
+                           max_context_len=40, d_error=err)
+    pa.pa_decode_fp4(q[:0], q[:0], *pools, table[:0], i32([]), *scales, scale=0.1,
+                     max_context_len=40, d_error=err)
+    # a step whose batch decodes nothing still writes
+    pa.pa_decode_write_fp4(q[:0], q[:0], q[:1, :2], q[1:, 2:4], *pools, table[0, :1].long() * 16,
+                           table[:0], i32([]), *scales, scale=0.1, max_context_len=40, d_error=err)
+    done(err)
+    for pool, was, s in zip(pools, before, scales):
+        F.put(was, table[0, :1].long() * 16, *F.quantise(q[:1, :2], s))
+        assert torch.equal(pool, was)

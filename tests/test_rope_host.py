@@ -39,7 +39,7 @@ NONE = dict(kc=0, vc=0, sm=0)
 @pytest.mark.parametrize("kw,status", [
     (dict(t=0), 0), (dict(t=0, q=0, qo=0, k=0), 0), (dict(t=-1), 2), (dict(hq=0), 2),
     (dict(hkv=0), 2), (dict(rot=-16), 2), (dict(rot=144), 2), (dict(rot=24), 3), (dict(rot=8), 3),
-    (dict(d=96, rot=96), 3), (dict(dtype=2), 3), (dict(eps=-1.0), 2), (dict(eps=float("nan")), 2),
+    (dict(d=96, rot=96), 3), (dict(hq=65537), 3), (dict(hkv=65537), 3), (dict(dtype=2), 3), (dict(eps=-1.0), 2), (dict(eps=float("nan")), 2),
     (dict(eps=float("inf")), 2), (dict(most=-1), 2), (dict(bs=0), 2), (dict(nb=-1), 2),
     (dict(nb=1 << 60), 2), (dict(qo=0), 1), (dict(q=0), 1), (dict(k=0), 1), (dict(v=0), 1),
     (dict(kc=0), 1), (dict(vc=0), 1), (dict(sm=0), 1), (dict(pos=0), 1), (dict(cs=0), 1),
