@@ -74,6 +74,7 @@ struct RopeArgs {
   pa_dtype dtype;
   int32_t *d_error;
   int num_sms;
+  int groups;  // lane groups per token where tokens share a CTA (the launcher's)
 };
 cudaError_t launch_rope_and_cache(const RopeArgs &a, cudaStream_t stream);
 

@@ -105,6 +105,38 @@ def test_matches_formula(t, hq, hkv, d, rot, pairs, norm, bs, rows, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("t,hq,hkv,d,rot,pairs,norm", [
+    (305, 8, 2, 128, 128, False, "qk"), (701, 3, 1, 64, 48, True, ""),
+    (4901, 8, 4, 128, 96, True, "qk"), (5003, 1, 1, 64, 64, False, "q"),
+    (6007, 12, 4, 64, 64, False, "qk"), (20011, 5, 3, 64, 32, True, "k"),
+])
+def test_many_tokens_of_few_heads(t, hq, hkv, d, rot, pairs, norm):
+    # several tokens share a CTA, the last CTA's places are not all taken
+    run(t, hq, hkv, d, torch.bfloat16, rot, pairs, norm, 16, True, seed=t)
+
+
+@gpu
+def test_a_bad_position_leaves_the_tokens_beside_it():
+    q, k, v, qw, kw, pos, g = make(5000, 4, 2, 64, torch.float16, 11)
+    bad = torch.randperm(5000, generator=g, device=DEV)[:300]
+    cs = table(4096, 64)
+    want_q, size_q = formula(q, pos, cs, qw, 1e-6, False)
+    want_k, size_k = formula(k, pos, cs, kw, 1e-6, False)
+    pos[bad] = 4096
+    q_out, k_out = torch.full((5000, 4, 64), 5.0, dtype=q.dtype, device=DEV), \
+        torch.full((5000, 2, 64), 6.0, dtype=q.dtype, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pa.pa_qk_norm_rope(q_out, k_out, q, k, pos, cs, q_weight=qw, k_weight=kw, d_error=err)
+    torch.cuda.synchronize()
+    assert int(err) == pa.DEVERR_POSITION
+    assert bool((q_out[bad] == 5).all()) and bool((k_out[bad] == 6).all())
+    good = torch.ones(5000, dtype=torch.bool, device=DEV)
+    good[bad] = False
+    check(q_out[good], want_q[good], size_q[good], q.dtype, "query_out")
+    check(k_out[good], want_k[good], size_k[good], q.dtype, "key_out")
+
+
+@gpu
 @pytest.mark.parametrize("spread", [1e-4, 300.0])
 def test_sizes_of_values(spread):
     for norm in ("", "qk"):
