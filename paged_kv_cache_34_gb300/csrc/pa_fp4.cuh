@@ -94,17 +94,12 @@ __device__ __forceinline__ uint2 quantise16(const uint32_t (&v)[8], const HeadSc
   float m = fmaxf(fabsf(E::lo(mw)), fabsf(E::hi(mw)));
   const bool odd = !(fabsf(E::lo(mw)) + fabsf(E::hi(mw)) < INFINITY);
   float x[16];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = E::lo(v[i]);
-    x[2 * i + 1] = E::hi(v[i]);
-  }
   if (odd) {
     m = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      x[i] = x[i] != x[i] ? 0.f : x[i];
-      m = fmaxf(m, fabsf(x[i]));
+      const float y = i & 1 ? E::hi(v[i / 2]) : E::lo(v[i / 2]);
+      m = fmaxf(m, y != y ? 0.f : fabsf(y));
     }
   }
   scale = to_e4m3(div_rn_recip(m, h.six, h.r));
@@ -112,13 +107,18 @@ __device__ __forceinline__ uint2 quantise16(const uint32_t (&v)[8], const HeadSc
   const float w = __fmul_rn(F16::lo(e4m3_to_f16x2(scale)), h.s), r = __frcp_rn(w);
   if (odd || scale == 126) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = div_rn_recip(x[i], w, r);
-  } else {
-#pragma unroll
     for (int i = 0; i < 16; ++i) {
-      // (with the remainder negated, -0 stays -0: -(-0 w + 0) r - 0)
-      const float q = __fmul_rn(x[i], r);
-      x[i] = __fmaf_rn(-__fmaf_rn(q, w, -x[i]), r, q);
+      const float y = i & 1 ? E::hi(v[i / 2]) : E::lo(v[i / 2]);
+      x[i] = div_rn_recip(y != y ? 0.f : y, w, r);
+    }
+  } else {
+    // two at a time, from -x: q = (-x)(-r), e = q w - x, q - e r, which leaves -0 as it is
+    const uint64_t w2 = f2_pack(w, w), nr = f2_pack(-r, -r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t n = v[i] ^ 0x80008000u;
+      const uint64_t nx = f2_pack(E::lo(n), E::hi(n)), q = f2_mul(nx, nr);
+      f2_unpack(f2_fma(f2_fma(q, w2, nx), nr, q), x[2 * i], x[2 * i + 1]);
     }
   }
   return make_uint2(to_e2m1(x), to_e2m1(x + 8));
