@@ -6,10 +6,13 @@
 // K_j, V_j the values of position j's codes (pa_fp4.cuh).
 //
 // Design: HBM bound by its bytes (72 a row of 128 values), and next to that by the
-// instructions that widen the codes.  The units, slices and the balanced split of the
-// token stream are those of decode_kernel.cuh; every warp is a worker with a chunk of
-// its own.  Scores are transposed on the tensor cores, S^T[16 tokens x 8 heads] =
-// K[16 x D] Q^T[D x 8], then O^T[D x 8] += V^T[D x 16] P^T[16 x 8].
+// instructions that widen the codes and the issue of the products.  The units, slices and
+// the balanced split of the token stream are those of decode_kernel.cuh; every warp is a
+// worker with a chunk of its own.  Scores are transposed on the tensor cores, S^T[16
+// tokens x 8 heads] = K[16 x D] Q^T[D x 8], then O^T[D x 8] += V^T[D x 16] P^T[16 x 8].
+//  * Each warp feeds a ring of its own: a stage is 64 tokens of a piece, a bulk copy per
+//    block and pool (a tile's codes and scales are one run of bytes), and is refilled as
+//    soon as the warp has read it; no warp waits for another.
 //  * Codes are widened in registers, two per instruction, and multiplied by their
 //    group's scale in fp16, which is exact (2 + 4 significant bits, at least 2^-10).  The
 //    head's scale goes into the scores' factor (K) and the output (V).
@@ -19,6 +22,12 @@
 //  * V: lane (g, t) owns elements (D / 8) g .. of O, all of one group, for the tokens
 //    2t, 2t + 1 of a tile.  The fragment pairs tokens: their codes' halves are
 //    interleaved before they are widened, four instructions for 16 values.
+// Measured (4 sequences up to 100000 tokens, 64/8 heads of 128, 443 MB): 88 us, 5.0 TB/s of
+// the 6.75 of a copy; direct loads 188, stages of 32 tokens 97, five CTAs an SM with 96
+// registers 114, the next tile's scores beside this one's sums 94.  The copies alone take 74
+// and the products with their widening alone 84 (stages of 32 tokens).  Operands widened
+// into tensor memory for products of 128 tokens 111: a tile's waits cost more than the
+// narrow products.
 #include "decode_kernel.cuh"
 #include "pa_fp4.cuh"
 
@@ -337,186 +346,186 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
       }
 #pragma unroll 1
       for (int sub = 0; sub < kTokens && j0 + sub < m.end; sub += kSub) {
-      const uint32_t kst = ring + s * 2 * kHalf + sub / 8 * TL::kBytes, vst = kst + kHalf;
-      const int left = m.end - j0 - sub;  // tokens from here on
-      float s2[NG][2][4];
+        const uint32_t kst = ring + s * 2 * kHalf + sub / 8 * TL::kBytes, vst = kst + kHalf;
+        const int left = m.end - j0 - sub;  // tokens from here on
+        float s2[NG][2][4];
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
+        for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) s2[n][u][0] = s2[n][u][1] = s2[n][u][2] = s2[n][u][3] = 0.f;
-      uint32_t kw[4][KW];  // row g of each tile
-      __half2 kf[4][2];    // its groups' scales
+          for (int u = 0; u < 2; ++u) s2[n][u][0] = s2[n][u][1] = s2[n][u][2] = s2[n][u][3] = 0.f;
+        uint32_t kw[4][KW];  // row g of each tile
+        __half2 kf[4][2];    // its groups' scales
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t tile = kst + i * TL::kBytes;
-        const uint32_t src = tile + g8 * TL::kRowBytes + t4 * (D / 8);
-        const uint32_t ss = tile + TL::kScales + g8 * TL::kScaleBytes;
-        uint32_t sb;
-        if constexpr (D == 128) {
-          const uint4 v = lds_v4(src);
-          kw[i][0] = v.x, kw[i][1] = v.y, kw[i][2] = v.z, kw[i][3] = v.w;
-          sb = lds_u16(ss + 2 * t4);
-        } else {
-          const uint2 v = lds_v2(src);
-          kw[i][0] = v.x, kw[i][1] = v.y;
-          sb = lds_u8(ss + t4);
-        }
-        const __half2 f = as_half2(e4m3_to_f16x2(sb));
-        kf[i][0] = __low2half2(f);
-        kf[i][1] = __high2half2(f);
-      }
-#pragma unroll
-      for (int w = 0; w < KW; ++w) {  // k-steps 2w, 2w + 1
-        const int hf = D == 128 ? w >> 1 : 0;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint32_t a[4], b[4];
-          widen8(kw[2 * u][w], a[0], a[1], a[2], a[3]);
-          widen8(kw[2 * u + 1][w], b[0], b[1], b[2], b[3]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            a[i] = hmul2(a[i], kf[2 * u][hf]);
-            b[i] = hmul2(b[i], kf[2 * u + 1][hf]);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t tile = kst + i * TL::kBytes;
+          const uint32_t src = tile + g8 * TL::kRowBytes + t4 * (D / 8);
+          const uint32_t ss = tile + TL::kScales + g8 * TL::kScaleBytes;
+          uint32_t sb;
+          if constexpr (D == 128) {
+            const uint4 v = lds_v4(src);
+            kw[i][0] = v.x, kw[i][1] = v.y, kw[i][2] = v.z, kw[i][3] = v.w;
+            sb = lds_u16(ss + 2 * t4);
+          } else {
+            const uint2 v = lds_v2(src);
+            kw[i][0] = v.x, kw[i][1] = v.y;
+            sb = lds_u8(ss + t4);
           }
-#pragma unroll
-          for (int n = 0; n < NG; ++n) {
-            mma(s2[n][u], a[0], b[0], a[1], b[1], qf[n][2 * w]);
-            mma(s2[n][u], a[2], b[2], a[3], b[3], qf[n][2 * w + 1]);
-          }
+          const __half2 f = as_half2(e4m3_to_f16x2(sb));
+          kf[i][0] = __low2half2(f);
+          kf[i][1] = __high2half2(f);
         }
-      }
-      uint32_t vx[4][VW], vy[4][VW];  // tokens 2t and 2t + 1 of each tile
-      __half2 vf[4];                  // their scales
-      auto load_v = [&](int i) {
-        const uint32_t tile = vst + i * TL::kBytes;
-        const uint32_t src = tile + 2 * t4 * TL::kRowBytes + g8 * (D / 16);
-        const uint32_t ss = tile + TL::kScales + 2 * t4 * TL::kScaleBytes +
-                            (D == 128 ? g8 : g8 >> 1);
-        if constexpr (D == 128) {
-          const uint2 x = lds_v2(src), y = lds_v2(src + TL::kRowBytes);
-          vx[i][0] = x.x, vx[i][1] = x.y, vy[i][0] = y.x, vy[i][1] = y.y;
-        } else {
-          vx[i][0] = lds_u32(src);
-          vy[i][0] = lds_u32(src + TL::kRowBytes);
-        }
-        uint32_t sx = lds_u8(ss), sy = lds_u8(ss + TL::kScaleBytes);
-        if (left < kSub) {
-          // rows past the context hold anything: their scale, and so their value, is 0
-          const int t0 = 8 * i + 2 * t4;
-          if (t0 >= left) sx = 0;
-          if (t0 + 1 >= left) sy = 0;
-        }
-        vf[i] = as_half2(e4m3_to_f16x2(sx | sy << 8));
-      };
-      // (their loads run under the softmax, where the registers allow it)
-      if constexpr (NG == 1)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load_v(i);
-      // Scores of tokens j0 + 16u + g (s2[n][u][0..1], heads 8n + 2t, +1) and + 8 (2..3).
-      uint32_t pb[NG][2][2];
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        const float slA = QS ? slh[QS ? n : 0][0] : sl, slB = QS ? slh[QS ? n : 0][1] : sl;
-        // Exponents against a reference that only follows the largest score once that
-        // is more than 8 above it: weights up to 256, which fp16 holds as well, and a
-        // stage whose scores stay below needs one vote and no maximum over lanes.
-        float a[2][4];
-        auto exponents = [&]() {
+        for (int w = 0; w < KW; ++w) {  // k-steps 2w, 2w + 1
+          const int hf = D == 128 ? w >> 1 : 0;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            a[u][0] = s2[n][u][0] * slA - ref[n][0];
-            a[u][1] = s2[n][u][1] * slB - ref[n][1];
-            a[u][2] = s2[n][u][2] * slA - ref[n][0];
-            a[u][3] = s2[n][u][3] * slB - ref[n][1];
+            uint32_t a[4], b[4];
+            widen8(kw[2 * u][w], a[0], a[1], a[2], a[3]);
+            widen8(kw[2 * u + 1][w], b[0], b[1], b[2], b[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a[i] = hmul2(a[i], kf[2 * u][hf]);
+              b[i] = hmul2(b[i], kf[2 * u + 1][hf]);
+            }
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+              mma(s2[n][u], a[0], b[0], a[1], b[1], qf[n][2 * w]);
+              mma(s2[n][u], a[2], b[2], a[3], b[3], qf[n][2 * w + 1]);
+            }
           }
+        }
+        uint32_t vx[4][VW], vy[4][VW];  // tokens 2t and 2t + 1 of each tile
+        __half2 vf[4];                  // their scales
+        auto load_v = [&](int i) {
+          const uint32_t tile = vst + i * TL::kBytes;
+          const uint32_t src = tile + 2 * t4 * TL::kRowBytes + g8 * (D / 16);
+          const uint32_t ss = tile + TL::kScales + 2 * t4 * TL::kScaleBytes +
+                              (D == 128 ? g8 : g8 >> 1);
+          if constexpr (D == 128) {
+            const uint2 x = lds_v2(src), y = lds_v2(src + TL::kRowBytes);
+            vx[i][0] = x.x, vx[i][1] = x.y, vy[i][0] = y.x, vy[i][1] = y.y;
+          } else {
+            vx[i][0] = lds_u32(src);
+            vy[i][0] = lds_u32(src + TL::kRowBytes);
+          }
+          uint32_t sx = lds_u8(ss), sy = lds_u8(ss + TL::kScaleBytes);
           if (left < kSub) {
+            // rows past the context hold anything: their scale, and so their value, is 0
+            const int t0 = 8 * i + 2 * t4;
+            if (t0 >= left) sx = 0;
+            if (t0 + 1 >= left) sy = 0;
+          }
+          vf[i] = as_half2(e4m3_to_f16x2(sx | sy << 8));
+        };
+        // (their loads run under the softmax, where the registers allow it)
+        if constexpr (NG == 1)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) load_v(i);
+        // Scores of tokens j0 + 16u + g (s2[n][u][0..1], heads 8n + 2t, +1) and + 8 (2..3).
+        uint32_t pb[NG][2][2];
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          const float slA = QS ? slh[QS ? n : 0][0] : sl, slB = QS ? slh[QS ? n : 0][1] : sl;
+          // Exponents against a reference that only follows the largest score once that
+          // is more than 8 above it: weights up to 256, which fp16 holds as well, and a
+          // stage whose scores stay below needs one vote and no maximum over lanes.
+          float a[2][4];
+          auto exponents = [&]() {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              if (16 * u + g8 >= left) a[u][0] = a[u][1] = -INFINITY;
-              if (16 * u + g8 + 8 >= left) a[u][2] = a[u][3] = -INFINITY;
+              a[u][0] = s2[n][u][0] * slA - ref[n][0];
+              a[u][1] = s2[n][u][1] * slB - ref[n][1];
+              a[u][2] = s2[n][u][2] * slA - ref[n][0];
+              a[u][3] = s2[n][u][3] * slB - ref[n][1];
             }
+            if (left < kSub) {
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                if (16 * u + g8 >= left) a[u][0] = a[u][1] = -INFINITY;
+                if (16 * u + g8 + 8 >= left) a[u][2] = a[u][3] = -INFINITY;
+              }
+            }
+          };
+          exponents();
+          float mx0 = fmaxf(fmaxf(a[0][0], a[0][2]), fmaxf(a[1][0], a[1][2]));
+          float mx1 = fmaxf(fmaxf(a[0][1], a[0][3]), fmaxf(a[1][1], a[1][3]));
+          if (__any_sync(0xffffffffu, fmaxf(mx0, mx1) > 8.f)) {
+            // (the first stage always: the reference is -inf)
+            mx0 = mx1 = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (16 * u + g8 < left) {
+                mx0 = fmaxf(mx0, s2[n][u][0] * slA);
+                mx1 = fmaxf(mx1, s2[n][u][1] * slB);
+              }
+              if (16 * u + g8 + 8 < left) {
+                mx0 = fmaxf(mx0, s2[n][u][2] * slA);
+                mx1 = fmaxf(mx1, s2[n][u][3] * slB);
+              }
+            }
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) {
+              mx0 = fmaxf(mx0, dec::shfl_xor(mx0, x));
+              mx1 = fmaxf(mx1, dec::shfl_xor(mx1, x));
+            }
+            mx0 = fmaxf(mx0, ref[n][0]);
+            mx1 = fmaxf(mx1, ref[n][1]);
+            const float cr0 = mx0 == -INFINITY ? 0.f : fast_exp2(ref[n][0] - mx0);
+            const float cr1 = mx1 == -INFINITY ? 0.f : fast_exp2(ref[n][1] - mx1);
+            ref[n][0] = mx0;
+            ref[n][1] = mx1;
+            lst[n][0] *= cr0;
+            lst[n][1] *= cr1;
+#pragma unroll
+            for (int mt = 0; mt < KSTEPS; ++mt) {
+              o[n][mt][0] *= cr0;
+              o[n][mt][1] *= cr1;
+              o[n][mt][2] *= cr0;
+              o[n][mt][3] *= cr1;
+            }
+            exponents();
           }
-        };
-        exponents();
-        float mx0 = fmaxf(fmaxf(a[0][0], a[0][2]), fmaxf(a[1][0], a[1][2]));
-        float mx1 = fmaxf(fmaxf(a[0][1], a[0][3]), fmaxf(a[1][1], a[1][3]));
-        if (__any_sync(0xffffffffu, fmaxf(mx0, mx1) > 8.f)) {
-          // (the first stage always: the reference is -inf)
-          mx0 = mx1 = -INFINITY;
+          // P is rounded to fp16 for the tensor core; the sums take the same rounded
+          // values, so the output is a weighted mean of V under the rounded weights.
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            if (16 * u + g8 < left) {
-              mx0 = fmaxf(mx0, s2[n][u][0] * slA);
-              mx1 = fmaxf(mx1, s2[n][u][1] * slB);
-            }
-            if (16 * u + g8 + 8 < left) {
-              mx0 = fmaxf(mx0, s2[n][u][2] * slA);
-              mx1 = fmaxf(mx1, s2[n][u][3] * slB);
-            }
+            const uint32_t w0 = F16::pack2(fast_exp2(a[u][0]), fast_exp2(a[u][1]));
+            const uint32_t w1 = F16::pack2(fast_exp2(a[u][2]), fast_exp2(a[u][3]));
+            F16::add_halves(w0, lst[n][0], lst[n][1]);
+            F16::add_halves(w1, lst[n][0], lst[n][1]);
+            pb[n][u][0] = transpose(w0);
+            pb[n][u][1] = transpose(w1);
           }
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) {
-            mx0 = fmaxf(mx0, dec::shfl_xor(mx0, x));
-            mx1 = fmaxf(mx1, dec::shfl_xor(mx1, x));
-          }
-          mx0 = fmaxf(mx0, ref[n][0]);
-          mx1 = fmaxf(mx1, ref[n][1]);
-          const float cr0 = mx0 == -INFINITY ? 0.f : fast_exp2(ref[n][0] - mx0);
-          const float cr1 = mx1 == -INFINITY ? 0.f : fast_exp2(ref[n][1] - mx1);
-          ref[n][0] = mx0;
-          ref[n][1] = mx1;
-          lst[n][0] *= cr0;
-          lst[n][1] *= cr1;
-#pragma unroll
-          for (int mt = 0; mt < KSTEPS; ++mt) {
-            o[n][mt][0] *= cr0;
-            o[n][mt][1] *= cr1;
-            o[n][mt][2] *= cr0;
-            o[n][mt][3] *= cr1;
-          }
-          exponents();
         }
-        // P is rounded to fp16 for the tensor core; the sums take the same rounded
-        // values, so the output is a weighted mean of V under the rounded weights.
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint32_t w0 = F16::pack2(fast_exp2(a[u][0]), fast_exp2(a[u][1]));
-          const uint32_t w1 = F16::pack2(fast_exp2(a[u][2]), fast_exp2(a[u][3]));
-          F16::add_halves(w0, lst[n][0], lst[n][1]);
-          F16::add_halves(w1, lst[n][0], lst[n][1]);
-          pb[n][u][0] = transpose(w0);
-          pb[n][u][1] = transpose(w1);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if constexpr (NG != 1) {
-          load_v(2 * u);
-          load_v(2 * u + 1);
-        }
-#pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          uint32_t ev[2][4], od[2][4];  // elements 2b and 2b + 1 of the lane's words, both tokens
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint32_t x = vx[2 * u + r][w], y = vy[2 * u + r][w];
-            const uint32_t e = (x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u);
-            const uint32_t d = ((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
-            widen8(e, ev[r][0], ev[r][1], ev[r][2], ev[r][3]);
-            widen8(d, od[r][0], od[r][1], od[r][2], od[r][3]);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              ev[r][b] = hmul2(ev[r][b], vf[2 * u + r]);
-              od[r][b] = hmul2(od[r][b], vf[2 * u + r]);
-            }
+          if constexpr (NG != 1) {
+            load_v(2 * u);
+            load_v(2 * u + 1);
           }
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
+          for (int w = 0; w < VW; ++w) {
+            uint32_t ev[2][4], od[2][4];  // elements 2b and 2b + 1 of the lane's words, both tokens
 #pragma unroll
-            for (int n = 0; n < NG; ++n)
-              mma(o[n][4 * w + b], ev[0][b], od[0][b], ev[1][b], od[1][b], pb[n][u]);
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t x = vx[2 * u + r][w], y = vy[2 * u + r][w];
+              const uint32_t e = (x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u);
+              const uint32_t d = ((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
+              widen8(e, ev[r][0], ev[r][1], ev[r][2], ev[r][3]);
+              widen8(d, od[r][0], od[r][1], od[r][2], od[r][3]);
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                ev[r][b] = hmul2(ev[r][b], vf[2 * u + r]);
+                od[r][b] = hmul2(od[r][b], vf[2 * u + r]);
+              }
+            }
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+              for (int n = 0; n < NG; ++n)
+                mma(o[n][4 * w + b], ev[0][b], od[0][b], ev[1][b], od[1][b], pb[n][u]);
+          }
         }
-      }
       }
       __syncwarp();  // every lane has read the stage
       if (f_end) ++issued;
