@@ -262,31 +262,24 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
   auto issue = [&](int s) {
     if (f_end == 0) return;
     const uint32_t bar = full + 8 * s;
-    uint32_t dst = ring + s * 2 * kHalf, sum = 0;
-    bool wrong = false;
     const int stop = min(f_end, f_cur + kTokens);
-    int j = f_cur;
-#pragma unroll 1
-    for (int q = 0; j < stop; ++q) {
-      const int id = __shfl_sync(0xffffffffu, f_id, q);
-      const int n = min(bs - (j & (bs - 1)), stop - j);  // tokens in this block
-      const uint32_t bytes = (n + 7) / 8 * TL::kBytes;
-      if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(p.num_blocks)) {
-        wrong = true;
-      } else {
-        const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(id)) * block_bytes +
-                            ((f_kvh << (bs_shift - 3)) + ((j & (bs - 1)) >> 3)) * TL::kBytes;
-        sum += 2 * bytes;
-        if (lane == 0) {
-          bulk_load(dst, kpool + at, bytes, bar);
-          bulk_load(dst + kHalf, vpool + at, bytes, bar);
-        }
-      }
-      dst += bytes;
-      j += n;
+    // lane q's tokens of the stage: from .. to - 1, of its q-th block
+    const int base = (f_cur & -bs) + (lane << bs_shift);
+    const int from = max(f_cur, base), to = min(stop, base + bs);
+    const bool wrong =
+        from < to && static_cast<uint32_t>(f_id) >= static_cast<uint32_t>(p.num_blocks);
+    uint32_t bytes = 0;
+    if (from < to && !wrong) {
+      bytes = (to - from + 7) / 8 * TL::kBytes;
+      const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(f_id)) * block_bytes +
+                          ((f_kvh << (bs_shift - 3)) + ((from & (bs - 1)) >> 3)) * TL::kBytes;
+      const uint32_t dst = ring + s * 2 * kHalf + (from - f_cur) / 8 * TL::kBytes;
+      bulk_load(dst, kpool + at, bytes, bar);
+      bulk_load(dst + kHalf, vpool + at, bytes, bar);
     }
-    if (lane == 0) mbar_arrive_expect_tx(bar, sum);
-    bad_stages = wrong ? bad_stages | (1u << s) : bad_stages & ~(1u << s);
+    const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);
+    if (lane == 0) mbar_arrive_expect_tx(bar, 2 * sum);
+    bad_stages = __any_sync(0xffffffffu, wrong) ? bad_stages | (1u << s) : bad_stages & ~(1u << s);
     f_cur += kTokens;
     look();
   };
@@ -593,28 +586,51 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
 
 // Joins the pieces of each (sequence, query head), their references m_i, sums l_i and
 // unnormalised outputs o_i: M = max m_i, w_i = 2^(m_i - M), out = sum w_i o_i / sum w_i l_i.
-// A group of W warps per (sequence, query head); a lane holds D / 32 elements, warp w of them
-// takes pieces w, w + W, ..., eight at a time.
+// W warps per (sequence, query head), at least four a CTA; a lane holds D / 32 elements, warp
+// w of them takes pieces w, w + W, ..., eight at a time.
 constexpr int kJoinBatch = 8;
+// Up to so many sequences each warp sums the lengths up itself while the decode still runs,
+// instead of reading the sums that it leaves (128 of 400 to 700 tokens 33.0 against 33.2 us, 8
+// of 1500, 32/8 heads, 10.6 and 11.1; with 256 lengths a warp 39.7 against 39.4).
+constexpr int kJoinSums = 128;
 
 template <class E, int D, int W>
-__global__ void __launch_bounds__(W < 4 ? 128 : W * 32) decode_fp4_join_kernel(const DecodeParams p) {
-  constexpr int V = D / 32;
-  __shared__ float s_m[W], s_l[W], s_o[W][D];  // (used where W > 1)
-  const int warp = W == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = W == 1 ? blockIdx.x * 4LL + (threadIdx.x >> 5) : blockIdx.x;
-  if (row >= static_cast<int64_t>(p.num_seqs) * p.hq) return;
-  const int b = static_cast<int>(row / p.hq), h = static_cast<int>(row - static_cast<int64_t>(b) * p.hq);
-  // (context_lens is no output of the launch before: read while that runs)
-  const int L = checked_context_len(__ldg(p.context_lens + b), p.capacity, p.max_ctx, p.err, false);
+__global__ void __launch_bounds__(W < 4 ? 128 : W * 32)
+    decode_fp4_join_kernel(const DecodeParams p) {
+  constexpr int V = D / 32, kRows = W < 4 ? 4 / W : 1;  // rows of a CTA
+  __shared__ float s_m[kRows * W], s_l[kRows * W], s_o[kRows * W][D];  // (used where W > 1)
+  const int first = threadIdx.x / 32 / W * W;  // the row's first warp
+  const int warp = (threadIdx.x >> 5) - first, lane = threadIdx.x & 31;
+  const int row = blockIdx.x * kRows + first / W;
+  if (row >= p.num_seqs * p.hq) return;
+  const int b = row / p.hq, h = row - b * p.hq;
+  const int kvh = h / p.group, hg = h - kvh * p.group, slc = hg / p.hs, g = kvh * p.nc + slc;
+  // (context_lens is no output of the launch before: read, and for few sequences summed up,
+  // while that runs)
+  auto length = [&](int i) {
+    return checked_context_len(__ldg(p.context_lens + i), p.capacity, p.max_ctx, p.err, false);
+  };
+  const int L = length(b);
+  int total = 0, pref = 0;
+  const bool sums = p.num_seqs <= kJoinSums;
+  if (sums) {
+    for (int i = lane; i < p.num_seqs; i += 32) {
+      const int items = ceil32(length(i)) * p.vh;
+      total += items;
+      if (i < b) pref += items;
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    pref = __reduce_add_sync(0xffffffffu, pref);
+  }
   griddep_wait();
   griddep_launch_dependents();
   if (L <= 0) return;
-  const int total = p.ws_pref[p.num_seqs], pref = p.ws_pref[b];
-  const int kvh = h / p.group, hg = h - kvh * p.group, slc = hg / p.hs;
-  const int g = kvh * p.nc + slc;
-  const int C = chunk_tokens(total, p.num_workers, p.chunk_cap);
+  if (!sums) {
+    total = p.ws_pref[p.num_seqs];
+    pref = p.ws_pref[b];
+  }
   const int U = pref + g * ceil32(L);
+  const int C = chunk_tokens(total, p.num_workers, p.chunk_cap);
   const int c0 = U / C, n = (U + ceil32(L) - 1) / C - c0 + 1;
   if (n <= 1) return;  // written by the decode kernel itself
   const int64_t row0 = (static_cast<int64_t>(b) * p.vh + g + c0) * p.hs + hg - slc * p.hs;
@@ -627,13 +643,14 @@ __global__ void __launch_bounds__(W < 4 ? 128 : W * 32) decode_fp4_join_kernel(c
     for (int k = 0; k < kJoinBatch; ++k) {
       const int i = i0 + k * W;
       const int64_t r = row0 + static_cast<int64_t>(i < n ? i : i0) * p.hs;
-      st[k] = i < n ? ml[r] : make_float2(-INFINITY, 0.f);
+      st[k] = i < n ? __ldcg(ml + r) : make_float2(-INFINITY, 0.f);
       const float *src = p.ws_o + r * D + V * lane;
       if constexpr (V == 4) {
-        const float4 x = i < n ? *reinterpret_cast<const float4 *>(src) : make_float4(0, 0, 0, 0);
+        const float4 x =
+            i < n ? __ldcg(reinterpret_cast<const float4 *>(src)) : make_float4(0, 0, 0, 0);
         ov[k][0] = x.x, ov[k][1] = x.y, ov[k][2] = x.z, ov[k][3] = x.w;
       } else {
-        const float2 x = i < n ? *reinterpret_cast<const float2 *>(src) : make_float2(0, 0);
+        const float2 x = i < n ? __ldcg(reinterpret_cast<const float2 *>(src)) : make_float2(0, 0);
         ov[k][0] = x.x, ov[k][1] = x.y;
       }
     }
@@ -656,25 +673,25 @@ __global__ void __launch_bounds__(W < 4 ? 128 : W * 32) decode_fp4_join_kernel(c
   }
   if constexpr (W > 1) {
     if (lane == 0) {
-      s_m[warp] = M;
-      s_l[warp] = l;
+      s_m[first + warp] = M;
+      s_l[first + warp] = l;
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = acc[v];
-    __syncthreads();
+    for (int v = 0; v < V; ++v) s_o[first + warp][lane * V + v] = acc[v];
+    asm volatile("bar.sync %0, %1;" ::"r"(first / W), "n"(32 * W) : "memory");
     if (warp != 0) return;
     M = -INFINITY;
     l = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) M = fmaxf(M, s_m[w]);
+    for (int w = 0; w < W; ++w) M = fmaxf(M, s_m[first + w]);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const float f = s_m[w] == -INFINITY ? 1.f : exp2f(s_m[w] - M);
-      l += f * s_l[w];
+      const float f = s_m[first + w] == -INFINITY ? 1.f : exp2f(s_m[first + w] - M);
+      l += f * s_l[first + w];
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += f * s_o[w][lane * V + v];
+      for (int v = 0; v < V; ++v) acc[v] += f * s_o[first + w][lane * V + v];
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -696,21 +713,23 @@ cudaError_t launch(const DecodeArgs &a, const DecodeParams &p, cudaStream_t stre
   if (e != cudaSuccess) return e;
   // nothing to join: every piece is its unit's whole context, or every context is empty
   if (p.partition_size || a.max_context_len == 0) return cudaSuccess;
-  // 16 warps a row for units of many pieces (4 and 16, device us of the whole call: 125
-  // pieces, one sequence of 8000 tokens, 32/8 heads 12.8 and 11.0; 228, 30000, 64/8 27.1
-  // and 22.3; 62, 2 of 4000, 32/8 11.5 and 12.6), one for units of few (1 and 4: 1, 256 of
-  // 133 to 200, 32/8 31.4 and 40.3; 4, 64 of 2700 to 4000, 32/8 57.5 and 60.2; 6.5, 32 of 50
-  // to 2000, 32/8 15.7 and 14.9).
+  // Many rows: a warp each.  Else by the pieces of a row, about workers / units (1, 2, 4 and
+  // 16 warps a row, device us of the whole call; rows, pieces: 4096, 8 (32 of 2700 to 4000,
+  // 128/8 heads) 48.4, 53.0, 54.9, 83.4; 2048, 4 (64 of them, 32/8) 54.8, 56.6, 57.8, 72.2;
+  // 1024, 7 (32 of 50 to 2000, 32/8) 15.6, 14.4, 14.2, 21.6; 256, 8 (8 of 500 to 2000, 32/32)
+  // 20.4, 19.6, 20.6, 20.7; 256, 19 (8 of 1500, 32/8) 13.0, 11.5, 10.7, 12.1; 256, 57 (4 of
+  // 32000 to 131000, 64/8) 96.1, 89.2, 86.6, 85.6; 64, 228 (30000, 64/8) 46, 32, 24.4, 21.0).
   const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
   const int64_t units = static_cast<int64_t>(a.num_seqs) * p.vh;
-  if (p.num_workers > 64 * units)
-    return launch_pdl(decode_fp4_join_kernel<E, D, 16>, dim3(static_cast<unsigned>(rows)),
-                      dim3(512), 0, stream, p);
-  if (p.num_workers > 4 * units)
-    return launch_pdl(decode_fp4_join_kernel<E, D, 4>, dim3(static_cast<unsigned>(rows)),
-                      dim3(128), 0, stream, p);
-  return launch_pdl(decode_fp4_join_kernel<E, D, 1>, dim3(static_cast<unsigned>((rows + 3) / 4)),
-                    dim3(128), 0, stream, p);
+  auto join = [&](auto kernel, int per_row) {
+    const int per_cta = per_row < 4 ? 4 / per_row : 1;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>((rows + per_cta - 1) / per_cta)),
+                      dim3(32 * per_row * per_cta), 0, stream, p);
+  };
+  if (rows >= 2048) return join(decode_fp4_join_kernel<E, D, 1>, 1);
+  if (p.num_workers > 48 * units) return join(decode_fp4_join_kernel<E, D, 16>, 16);
+  if (p.num_workers > 12 * units) return join(decode_fp4_join_kernel<E, D, 4>, 4);
+  return join(decode_fp4_join_kernel<E, D, 2>, 2);
 }
 
 template <class E>

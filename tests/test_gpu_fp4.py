@@ -237,6 +237,17 @@ def test_long_and_many(lens, hq, hkv, d, bs):
     run(lens, hq, hkv, d, bs, torch.bfloat16 if hkv == 8 else torch.float16, len(lens) + hq)
 
 
+@pytest.mark.parametrize("lens,hq,hkv,d,bs", [
+    ([700, 0, 333, 900] * 33, 32, 8, 128, 32),  # many rows, more sequences than a warp sums up
+    ([900, 33, 0, 1500] * 16, 64, 8, 64, 32), ([2700, 1, 500] * 8, 128, 8, 128, 16),
+    ([600] * 128, 16, 2, 64, 64), ([600] * 129, 16, 2, 64, 64),
+    ([1500, 20, 900], 32, 8, 128, 32), ([3000, 0, 2500], 6, 2, 64, 16),
+])
+def test_pieces_of_many_and_few_rows(lens, hq, hkv, d, bs):
+    for dtype in BOTH:
+        run(lens, hq, hkv, d, bs, dtype, len(lens) + d, most=max(lens) + 500)
+
+
 @pytest.mark.parametrize("dtype", BOTH)
 def test_scales_and_sizes_of_queries(dtype):
     for scale in (0.0, -0.1, 1e-30, 3.0):
