@@ -11,8 +11,9 @@
 // worker with a chunk of its own.  Scores are transposed on the tensor cores, S^T[16
 // tokens x 8 heads] = K[16 x D] Q^T[D x 8], then O^T[D x 8] += V^T[D x 16] P^T[16 x 8].
 //  * Each warp feeds a ring of its own: a stage is 64 tokens of a piece, a bulk copy per
-//    block and pool (a tile's codes and scales are one run of bytes), and is refilled as
-//    soon as the warp has read it; no warp waits for another.
+//    block and pool (a tile's codes and scales are one run of bytes), which the lane that
+//    holds the block's id issues, as soon as the warp has read what was there; no warp
+//    waits for another.
 //  * Codes are widened in registers, two per instruction, and multiplied by their
 //    group's scale in fp16, which is exact (2 + 4 significant bits, at least 2^-10).  The
 //    head's scale goes into the scores' factor (K) and the output (V).
@@ -22,12 +23,13 @@
 //  * V: lane (g, t) owns elements (D / 8) g .. of O, all of one group, for the tokens
 //    2t, 2t + 1 of a tile.  The fragment pairs tokens: their codes' halves are
 //    interleaved before they are widened, four instructions for 16 values.
-// Measured (4 sequences up to 100000 tokens, 64/8 heads of 128, 443 MB): 88 us, 5.0 TB/s of
-// the 6.75 of a copy; direct loads 188, stages of 32 tokens 97, five CTAs an SM with 96
-// registers 114, the next tile's scores beside this one's sums 94.  The copies alone take 74
-// and the products with their widening alone 84 (stages of 32 tokens).  Operands widened
-// into tensor memory for products of 128 tokens 111: a tile's waits cost more than the
-// narrow products.
+// Measured (4 sequences up to 131072 tokens, 64/8 heads of 128, 443 MB): 85 us, 5.2 TB/s of
+// the 6.75 of a copy.  On the way: direct loads 188, stages of 32 tokens 97, of 64 with the
+// block ids passed round 88 (64 of 4000, 64/8 heads of 64, 53 and 47 with each lane's copies
+// its own).  Dropped: five CTAs an SM with 96 registers 114, stages of 32 tokens and four
+// CTAs 94, the next tile's scores beside this one's sums 94.  The copies alone take 68, the
+// products with their widening alone 73, the join 4.  Operands widened into tensor memory
+// for products of 128 tokens 111: a tile's waits cost more than the narrow products.
 #include "decode_kernel.cuh"
 #include "pa_fp4.cuh"
 
@@ -239,8 +241,8 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
   const int bs = p.block_size, bs_shift = 31 - __clz(bs);
 
   // Feeding the ring.  A stage is kTokens of a piece: a run of tiles per block, keys and
-  // values.  Lane 0 copies; lane q loads the id of the stage's q-th block, for the stage
-  // after as one is issued.
+  // values.  Lane q loads the id of the stage's q-th block, for the stage after as one is
+  // issued, and copies that block's part.
   Cursor pc = {gw, gw * C};
   int f_cur = 0, f_end = 0, f_kvh = 0, f_id = -1;  // the stage to issue next (f_end 0: none)
   const int32_t *f_row = nullptr;

@@ -209,8 +209,9 @@ constexpr int kFp4MostSeqs = 8192;       // prefix sums and lengths, 8 bytes eac
 constexpr int fp4_stages(int head_dim) { return head_dim == 128 ? 2 : 3; }
 constexpr int fp4_ctas_per_sm(int head_dim, int ng) { return head_dim == 64 && ng == 1 ? 4 : 3; }
 // Short contexts are not cut: no states, no second launch (cut / whole, device us: 4
-// sequences of 64 / 128 / 192 tokens, 8/2 heads of 64, 5.9 / 4.4, 6.0 / 5.6, 5.9 / 6.7; 32,
-// 32/8 8.4 / 5.6, 10.0 / 7.2, 10.9 / 8.8; 256 of 128 / 256 22.0 / 20.4, 32.5 / 31.4).
+// sequences of 64 / 128 / 192 tokens, 8/2 heads of 64, 5.5 / 4.3, 5.7 / 5.3, 5.7 / 6.4; 32 of
+// 128 / 256 / 384, 32/8 9.1 / 6.8, 10.5 / 9.8, 10.6 / 12.8; 256 of 128 / 256 25.7 / 21.8,
+// 32.7 / 30.9).
 inline bool fp4_whole_units(int max_ctx, int64_t units) {
   return max_ctx > 0 && max_ctx <= (units < 128 ? 128 : 256);
 }
@@ -230,7 +231,8 @@ inline DecodeBalance fp4_balance(int num_seqs, int units, int ng, int head_dim, 
   most *= num_sms;
   // A worker takes 32 tokens at least, and 64 where that leaves 768 workers or more: fewer
   // states to join (32 / 64 tokens throughout, device us; one sequence of 8000 tokens,
-  // 32/8 heads 17.7 / 11.2; 2 of 1500, 32/32 11.9 / 10.5; but 8 of 200, 32/8 7.3 / 9.0).
+  // 32/8 heads 11.5 / 10.4; 16 of 600 12.3 / 10.4; but 8 of 192 7.3 / 7.7, 1 of 1000 6.9 /
+  // 7.4).
   const int64_t shares = t_max / 32;
   int64_t grid = shares <= 768 ? shares : (shares / 2 > 768 ? shares / 2 : 768);
   const int64_t all = static_cast<int64_t>(num_seqs) * units;
