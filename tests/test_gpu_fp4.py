@@ -240,7 +240,7 @@ def test_long_and_many(lens, hq, hkv, d, bs):
 @pytest.mark.parametrize("lens,hq,hkv,d,bs", [
     ([700, 0, 333, 900] * 33, 32, 8, 128, 32),  # many rows, more sequences than a warp sums up
     ([900, 33, 0, 1500] * 16, 64, 8, 64, 32), ([2700, 1, 500] * 8, 128, 8, 128, 16),
-    ([600] * 128, 16, 2, 64, 64), ([600] * 129, 16, 2, 64, 64),
+    ([600] * 128, 16, 2, 64, 64), ([600] * 129, 16, 2, 64, 64), ([2000] * 130, 4, 1, 128, 16),
     ([1500, 20, 900], 32, 8, 128, 32), ([3000, 0, 2500], 6, 2, 64, 16),
 ])
 def test_pieces_of_many_and_few_rows(lens, hq, hkv, d, bs):
