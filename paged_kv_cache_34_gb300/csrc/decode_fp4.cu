@@ -40,8 +40,6 @@ using dec::DecodeParams;
 
 constexpr int kWarps = kFp4Warps;
 constexpr int kTokens = kFp4StageTokens;
-template <int D>
-constexpr int kStages = fp4_stages(D);
 
 __host__ __device__ __forceinline__ int ceil32(int x) { return (x + 31) & ~31; }
 
@@ -179,18 +177,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 template <class E, int D, int NG>
 __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
     decode_fp4_kernel(const DecodeParams p, const uint8_t *__restrict__ kpool,
-                      const uint8_t *__restrict__ vpool) {
+                      const uint8_t *__restrict__ vpool, const int stages) {
   using TL = Tile<D>;
-  constexpr int KSTEPS = D / 16, KW = D / 32, VW = D / 64, NS = kStages<D>;
+  constexpr int KSTEPS = D / 16, KW = D / 32, VW = D / 64;
   constexpr int kHalf = kTokens / 8 * TL::kBytes, kSub = 32;  // a stage's keys, or its values
   constexpr bool QS = E::kBF16;
   // each warp's stages; barriers; [S + 1] prefix sums, [S] lengths
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
-  const uint32_t ring = smem_u32(smem) + warp * NS * 2 * kHalf;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kWarps * NS * 2 * kHalf);
-  const uint32_t full = smem_u32(bars + warp * NS);
-  int *s_pref = reinterpret_cast<int *>(bars + kWarps * NS);
+  const uint32_t ring = smem_u32(smem) + warp * stages * 2 * kHalf;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kWarps * stages * 2 * kHalf);
+  const uint32_t full = smem_u32(bars + warp * stages);
+  int *s_pref = reinterpret_cast<int *>(bars + kWarps * stages);
   int *s_len = s_pref + p.num_seqs + 1;
   const int nseq = p.num_seqs;
   // Inputs come from earlier kernels; right after the step's write, only the pools'
@@ -198,7 +196,7 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
   if (!p.after_write) griddep_wait();
   griddep_launch_dependents();
   if (lane == 0) {
-    for (int s = 0; s < NS; ++s) mbar_init(full + 8 * s, 1);
+    for (int s = 0; s < stages; ++s) mbar_init(full + 8 * s, 1);
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -289,7 +287,7 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
   if (p.after_write) griddep_wait();
   int issued = 0;
 #pragma unroll 1
-  for (int s = 0; s < NS; ++s) {
+  for (int s = 0; s < stages; ++s) {
     if (f_end) ++issued;
     issue(s);
   }
@@ -536,7 +534,7 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
       if (f_end) ++issued;
       issue(s);
       --issued;
-      if (++s == NS) {
+      if (++s == stages) {
         s = 0;
         phase ^= 1;
       }
@@ -589,7 +587,7 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
   // A wait ran out: leave once the copies in flight are in.
   for (; issued > 0; --issued) {
     mbar_wait_bounded(full + 8 * s, phase);
-    if (++s == NS) {
+    if (++s == stages) {
       s = 0;
       phase ^= 1;
     }
@@ -715,13 +713,13 @@ __global__ void __launch_bounds__(W < 4 ? 128 : W * 32)
 }
 
 template <class E, int D, int NG>
-cudaError_t launch(const DecodeArgs &a, const DecodeParams &p, cudaStream_t stream) {
-  const int smem = fp4_decode_smem(D, a.num_seqs);
+cudaError_t launch(const DecodeArgs &a, const DecodeParams &p, int stages, cudaStream_t stream) {
+  const int smem = fp4_decode_smem(D, stages, a.num_seqs);
   cudaError_t e = allow_dynamic_smem<decode_fp4_kernel<E, D, NG>>();
   if (e != cudaSuccess) return e;
   e = launch_pdl(decode_fp4_kernel<E, D, NG>, dim3(static_cast<unsigned>(a.grid)),
                  dim3(kWarps * 32), smem, stream, p, static_cast<const uint8_t *>(a.k_pool),
-                 static_cast<const uint8_t *>(a.v_pool));
+                 static_cast<const uint8_t *>(a.v_pool), stages);
   if (e != cudaSuccess) return e;
   // nothing to join: every piece is its unit's whole context, or every context is empty
   if (p.partition_size || a.max_context_len == 0) return cudaSuccess;
@@ -745,10 +743,13 @@ cudaError_t launch(const DecodeArgs &a, const DecodeParams &p, cudaStream_t stre
 }
 
 template <class E>
-cudaError_t launch_type(const DecodeArgs &a, const DecodeParams &p, cudaStream_t stream) {
+cudaError_t launch_type(const DecodeArgs &a, const DecodeParams &p, int stages,
+                        cudaStream_t stream) {
   if (a.head_dim == 128)
-    return a.slices.ng == 2 ? launch<E, 128, 2>(a, p, stream) : launch<E, 128, 1>(a, p, stream);
-  return a.slices.ng == 2 ? launch<E, 64, 2>(a, p, stream) : launch<E, 64, 1>(a, p, stream);
+    return a.slices.ng == 2 ? launch<E, 128, 2>(a, p, stages, stream)
+                            : launch<E, 128, 1>(a, p, stages, stream);
+  return a.slices.ng == 2 ? launch<E, 64, 2>(a, p, stages, stream)
+                          : launch<E, 64, 1>(a, p, stages, stream);
 }
 
 }  // namespace fp4
@@ -762,8 +763,8 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t stream) {
   const int64_t units = static_cast<int64_t>(a.num_seqs) * p.vh;
   p.partition_size =
       fp4_whole_units(a.max_context_len, units) ? (a.max_context_len + 31) / 32 * 32 : 0;
-  return a.dtype == PA_BF16 ? fp4::launch_type<BF16>(a, p, stream)
-                            : fp4::launch_type<F16>(a, p, stream);
+  return a.dtype == PA_BF16 ? fp4::launch_type<BF16>(a, p, d.stages, stream)
+                            : fp4::launch_type<F16>(a, p, d.stages, stream);
 }
 
 }  // namespace pa
