@@ -23,7 +23,7 @@
 //  * V: lane (g, t) owns elements (D / 8) g .. of O, all of one group, for the tokens
 //    2t, 2t + 1 of a tile.  The fragment pairs tokens: their codes' halves are
 //    interleaved before they are widened, four instructions for 16 values.
-// Measured (4 sequences up to 131072 tokens, 64/8 heads of 128, 443 MB): 84 us, 5.3 TB/s of
+// Measured (4 sequences up to 131072 tokens, 64/8 heads of 128, 443 MB): 83 us, 5.3 TB/s of
 // the 6.75 of a copy.  On the way: direct loads 188, stages of 32 tokens 97, of 64 with the
 // block ids passed round 88 (64 of 4000, 64/8 heads of 64, 53 and 47 with each lane's copies
 // its own).  Dropped: five CTAs an SM with 96 registers 114, stages of 32 tokens and four
