@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(256, 4) reshape_and_cache_fp4_kernel(const Res
   const HeadScale hs(__ldg((value ? p.v_scale : p.k_scale) + h));
   const char *rows = static_cast<const char *>(value ? p.value : p.key) + 32 * j;
   uint8_t *pool = static_cast<uint8_t *>(value ? p.value_cache : p.key_cache);
-  const int tiles = p.block_size / 8;
+  const int shift = 31 - __clz(p.block_size);
   auto fetch = [&](int64_t t, int64_t &slot, uint4 &a, uint4 &b) {
     if (t >= p.num_tokens) return;
     slot = __ldg(p.slot_mapping + t);
@@ -64,13 +64,11 @@ __global__ void __launch_bounds__(256, 4) reshape_and_cache_fp4_kernel(const Res
     if (hs.s == 0.f) raise_error(p.d_error, PA_DEVERR_SCALE);
     uint32_t scale;
     const uint2 codes = quantise16<E>(v, hs, scale);
-    // (the pool's slots are fewer than 2^31 or the division is the slow one)
-    const int64_t block = at >> 31 ? at / p.block_size
-                                   : static_cast<uint32_t>(at) / static_cast<uint32_t>(p.block_size);
-    const int off = static_cast<int>(at - block * p.block_size);
-    uint8_t *tile = pool + ((block * p.num_kv_heads + h) * tiles + off / 8) * TL::kBytes;
-    *reinterpret_cast<uint2 *>(tile + (off % 8) * TL::kRowBytes + 8 * g) = codes;
-    tile[TL::kScales + (off % 8) * TL::kScaleBytes + g] = static_cast<uint8_t>(scale);
+    const int64_t block = at >> shift;
+    const uint32_t off = static_cast<uint32_t>(at) & (p.block_size - 1), row = off & 7;
+    uint8_t *tile = pool + (((block * p.num_kv_heads + h) << (shift - 3)) + (off >> 3)) * TL::kBytes;
+    *reinterpret_cast<uint2 *>(tile + row * TL::kRowBytes + 8 * g) = codes;
+    tile[TL::kScales + row * TL::kScaleBytes + g] = static_cast<uint8_t>(scale);
   }
 }
 
