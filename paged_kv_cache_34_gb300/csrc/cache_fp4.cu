@@ -40,22 +40,25 @@ __global__ void __launch_bounds__(256, 4) reshape_and_cache_fp4_kernel(const Res
   const char *rows = static_cast<const char *>(value ? p.value : p.key) + 32 * j;
   uint8_t *pool = static_cast<uint8_t *>(value ? p.value_cache : p.key_cache);
   const int shift = 31 - __clz(p.block_size);
-  auto fetch = [&](int64_t t, int64_t &slot, uint4 &a, uint4 &b) {
-    if (t >= p.num_tokens) return;
-    slot = __ldg(p.slot_mapping + t);
-    const uint4 *src = reinterpret_cast<const uint4 *>(rows + t * p.row_stride_bytes);
-    a = __ldg(src);
-    b = __ldg(src + 1);
-  };
   int64_t slot = -1;
   uint4 a, b;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens + mine;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * tokens;
-  fetch(t0, slot, a, b);
-  for (int64_t t = t0; t < p.num_tokens; t += step) {
+  const uint32_t t0 = blockIdx.x * tokens + mine, step = gridDim.x * tokens;
+  const char *src = rows + t0 * p.row_stride_bytes;  // the next token's
+  const int64_t *slots = p.slot_mapping + t0;
+  const int64_t src_step = step * p.row_stride_bytes;
+  auto fetch = [&](uint32_t t) {
+    if (t >= static_cast<uint32_t>(p.num_tokens)) return;
+    slot = __ldg(slots);
+    a = __ldg(reinterpret_cast<const uint4 *>(src));
+    b = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
+    slots += step;
+    src += src_step;
+  };
+  fetch(t0);
+  for (uint32_t t = t0; t < static_cast<uint32_t>(p.num_tokens); t += step) {
     const int64_t at = slot;
     const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    fetch(t + step, slot, a, b);
+    fetch(t + step);
     if (at < 0) continue;
     if (at >= p.num_slots) {
       if (i == 0) raise_error(p.d_error, PA_DEVERR_SLOT);
