@@ -13,7 +13,7 @@
 //  * Read: a thread holds eight elements of a head's row, so that rows are written in whole
 //    lines, and takes a tile of eight tokens at a time: one block id, eight rows on their way.
 // Measured (16 prompts up to 2000 tokens, 32 KV heads of 128, bf16, 333 MB each way): write
-// 61 us, 5.5 TB/s; read 57 us, 5.8 TB/s, of the 6.75 of a copy; 162 us together with a
+// 59 us, 5.6 TB/s; read 57 us, 5.8 TB/s, of the 6.75 of a copy; 162 us together with a
 // thread per group and token in both and the checked quotient throughout.
 #include "pa_fp4.cuh"
 #include "pa_internal.h"
@@ -151,7 +151,7 @@ cudaError_t launch_reshape_and_cache_fp4(const ReshapeArgs &a, cudaStream_t stre
   const int threads = parts > 1 ? 256 : per * tokens;
   const int64_t ctas = (static_cast<int64_t>(a.num_tokens) + tokens - 1) / tokens;
   // Two CTAs to each of the five that an SM holds, so that the last ones do not end
-  // together (16 prompts up to 2000 tokens, 32/32 heads: 61 us, with one each 73, with a
+  // together (16 prompts up to 2000 tokens, 32/32 heads: 62 us, with one each 73, with a
   // CTA per token 93).
   const int64_t most = (static_cast<int64_t>(a.num_sms) * 10 + parts - 1) / parts;
   const int grid = static_cast<int>(ctas < most ? ctas : most);
