@@ -13,7 +13,7 @@
 //  * Read: a thread holds eight elements of a head's row, so that rows are written in whole
 //    lines, and takes a tile of eight tokens at a time: one block id, eight rows on their way.
 // Measured (16 prompts up to 2000 tokens, 32 KV heads of 128, bf16, 333 MB each way): write
-// 59 us, 5.6 TB/s; read 57 us, 5.8 TB/s, of the 6.75 of a copy; 162 us together with a
+// 55 us, 6.0 TB/s; read 57 us, 5.8 TB/s, of the 6.75 of a copy; 162 us together with a
 // thread per group and token in both and the checked quotient throughout.
 #include "pa_fp4.cuh"
 #include "pa_internal.h"
@@ -150,10 +150,11 @@ cudaError_t launch_reshape_and_cache_fp4(const ReshapeArgs &a, cudaStream_t stre
   const int tokens = per <= 128 ? 256 / per : 1, parts = (per + 255) / 256;
   const int threads = parts > 1 ? 256 : per * tokens;
   const int64_t ctas = (static_cast<int64_t>(a.num_tokens) + tokens - 1) / tokens;
-  // Two CTAs to each of the five that an SM holds, so that the last ones do not end
-  // together (16 prompts up to 2000 tokens, 32/32 heads: 62 us, with one each 73, with a
-  // CTA per token 93).
-  const int64_t most = (static_cast<int64_t>(a.num_sms) * 10 + parts - 1) / parts;
+  // As many CTAs as run at once, four an SM: a thread's next token is on its way while it
+  // works on one (4, 8, 10 and 24 an SM: 16 prompts up to 2000 tokens, 32 heads, 55.3, 55.6,
+  // 59.0, 57.9 us; 64 of 300 to 500, 8 heads, 23.8, 24.4, 26.0, 27.1; three resident 61,
+  // five, of 51 registers, 61).
+  const int64_t most = (static_cast<int64_t>(a.num_sms) * 4 + parts - 1) / parts;
   const int grid = static_cast<int>(ctas < most ? ctas : most);
   auto kernel = a.dtype == PA_BF16 ? (a.head_dim == 128 ? fp4::reshape_and_cache_fp4_kernel<BF16, 128>
                                                         : fp4::reshape_and_cache_fp4_kernel<BF16, 64>)
