@@ -623,8 +623,9 @@ pa_status pa_gather_cache_fp4(void *key_out, int64_t k_out_row_stride, void *val
  * Scores and weighted sums are accumulated in fp32 from the products of codes and
  * group scales, which fp16 holds exactly, and the query rounded to fp16 after a
  * power of two that depends on its head (bf16 queries keep their range, as over
- * the one-byte pools); the softmax weights are rounded to fp16.  A NaN in a query
- * makes that (sequence, head) NaN.  Arguments and errors as for pa_decode_fp8,
+ * the one-byte pools); the softmax weights are rounded to fp16, with 11 bits down to
+ * 2^-21 of a worker's largest and fewer down to 2^-32, below which they are 0.  A NaN
+ * in a query makes that (sequence, head) NaN.  Arguments and errors as for pa_decode_fp8,
  * without its partition size.  The workspace (256-byte aligned) is of
  * pa_decode_fp4_plan's size for the same shape; calls that may run at the same
  * time need one each.

@@ -40,6 +40,7 @@ using dec::DecodeParams;
 
 constexpr int kWarps = kFp4Warps;
 constexpr int kTokens = kFp4StageTokens;
+constexpr float kLift = 7.f;  // log2 of the weight of the score that a reference was taken from
 
 __host__ __device__ __forceinline__ int ceil32(int x) { return (x + 31) & ~31; }
 
@@ -429,8 +430,12 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
         for (int n = 0; n < NG; ++n) {
           const float slA = QS ? slh[QS ? n : 0][0] : sl, slB = QS ? slh[QS ? n : 0][1] : sl;
           // Exponents against a reference that only follows the largest score once that
-          // is more than 8 above it: weights up to 256, which fp16 holds as well, and a
-          // stage whose scores stay below needs one vote and no maximum over lanes.
+          // is more than 8 above where the reference was taken: a stage whose scores stay
+          // below needs one vote and no maximum over lanes.  The reference is kLift below
+          // its score, so that weights reach up to 2^15, the top of fp16's range, and keep
+          // its 11 bits down to 2^-21 of the largest and something down to 2^-32 (a
+          // reference at the score itself lost keys 2^25 times less likely than one before
+          // them: with 2^18 of them behind it in a worker's share, 1/128 of the sum).
           float a[2][4];
           auto exponents = [&]() {
 #pragma unroll
@@ -451,7 +456,7 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
           exponents();
           float mx0 = fmaxf(fmaxf(a[0][0], a[0][2]), fmaxf(a[1][0], a[1][2]));
           float mx1 = fmaxf(fmaxf(a[0][1], a[0][3]), fmaxf(a[1][1], a[1][3]));
-          if (__any_sync(0xffffffffu, fmaxf(mx0, mx1) > 8.f)) {
+          if (__any_sync(0xffffffffu, fmaxf(mx0, mx1) > 8.f + kLift)) {
             // (the first stage always: the reference is -inf)
             mx0 = mx1 = -INFINITY;
 #pragma unroll
@@ -470,8 +475,8 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
               mx0 = fmaxf(mx0, dec::shfl_xor(mx0, x));
               mx1 = fmaxf(mx1, dec::shfl_xor(mx1, x));
             }
-            mx0 = fmaxf(mx0, ref[n][0]);
-            mx1 = fmaxf(mx1, ref[n][1]);
+            mx0 = fmaxf(mx0 - kLift, ref[n][0]);
+            mx1 = fmaxf(mx1 - kLift, ref[n][1]);
             const float cr0 = mx0 == -INFINITY ? 0.f : fast_exp2(ref[n][0] - mx0);
             const float cr1 = mx1 == -INFINITY ? 0.f : fast_exp2(ref[n][1] - mx1);
             ref[n][0] = mx0;

@@ -1,0 +1,111 @@
+"""The calls over FP4 pools at the edges of what they document: keys far below a dominant
+one, rows that nothing wrote, batches of one long and many short sequences, many
+sequences."""
+import pytest
+import torch
+
+import fp4_util as F
+import paged_kv_cache_34_gb300 as pa
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BOTH = [torch.float16, torch.bfloat16]
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def new_err():
+    return torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+def done(err, want=0):
+    torch.cuda.synchronize()
+    assert int(err) == want
+
+
+def cache(lens, hkv, d, bs, seed):
+    """(block table, pools, head scales) of contexts `lens`: codes of every kind, group
+    scales a few steps apart, and NaN scales behind each context."""
+    g = gen(seed)
+    count = torch.tensor([-(-n // bs) for n in lens])
+    nb, width = int(count.sum()) + 2, int(count.max())
+    held = (torch.arange(width) < count[:, None]).to(DEV)
+    table = torch.full((len(lens), width), -1, dtype=torch.int32, device=DEV)
+    table[held] = torch.randperm(nb, generator=g, device=DEV)[:int(held.sum())].to(torch.int32)
+    n = torch.tensor(lens, device=DEV)
+    last = [(table[b, -(-m // bs) - 1], m % bs) for b, m in enumerate(lens) if m % bs]
+    pools = []
+    for _ in range(2):
+        pool = torch.randint(0, 256, (nb, hkv, bs // 8, 9 * d // 2), generator=g, device=DEV,
+                             dtype=torch.uint8)
+        pool[..., 4 * d:] = 90 + pool[..., 4 * d:] % 32
+        ps = F.parts(pool, d)[1]
+        for block, m in last:
+            behind = torch.arange(bs, device=DEV).view(-1, 8) >= m
+            ps[block.long()] = torch.where(behind[..., None], 0x7f, ps[block.long()])
+        pools.append(pool)
+    scales = [0.001 + 0.002 * torch.rand(hkv, generator=g, device=DEV) for _ in range(2)]
+    assert int(n.max()) > 0
+    return table, pools, scales
+
+
+# ----------------------------------------------------------------- weights --
+@pytest.mark.parametrize("dtype", BOTH)
+def test_weights_far_below_a_dominant_key(dtype):
+    # One key of each head's context is 2^24 to 2^26.8 times as likely as every other, and
+    # its value is 0 where theirs is 1: what is left of theirs is the output.  Batches of
+    # long contexts, so that a worker meets some hundred thousand keys behind the
+    # dominant one (all sequences share one context's blocks).
+    d, bs, n, seqs, heads = 64, 128, 1 << 20, 600, 8
+    pools = [F.new_pool(n // bs, 1, bs, d, code=0, scale=0x38) for _ in range(2)]
+    F.parts(pools[1], d)[0][:] = 0x22  # value 1
+    slot = torch.tensor([7], device=DEV)
+    row, one = torch.zeros(1, 1, d, device=DEV, dtype=torch.long), \
+        torch.full((1, 1, d // 16), 0x38, device=DEV)
+    F.put(pools[1], slot, row, one)
+    row[..., 0] = 7  # 6
+    F.put(pools[0], slot, row, one)
+    S = torch.ones(1, device=DEV)
+    q = torch.zeros(seqs, heads, d, device=DEV)
+    q[:, :, 0] = (24 + 0.4 * torch.arange(heads, device=DEV)) * 0.6931471805599453 / 6
+    q = q.to(dtype)
+    table = torch.arange(n // bs, dtype=torch.int32, device=DEV).repeat(seqs, 1)
+    out, err = torch.empty_like(q), new_err()
+    pa.pa_decode_fp4(out, q, *pools, table, i32([n] * seqs), S, S, scale=1.0, max_context_len=n,
+                     d_error=err)
+    done(err)
+    # weights of 1 beside exp(6 q): out = m / (m + exp(6 q)), m = n - 1 keys, in 64 bits;
+    # the score 6 q is exact (one product of 2 and 8 or 11 bits), scaled and turned into a
+    # power of two in fp32 (relative 2^-23 of up to 20, twice, and the exponential's 2^-21);
+    # weights keep 2^-11 (fp16), fp32 sums of 2^18 equal values a lane: n / 32 steps of
+    # 2^-24 at most, the output rounded.  Below 2^-14 fp16's steps are 2^-24 whatever the
+    # weight, so one is off by up to 2^-25 where the dominant key's is 2^7 or more: 2^-32 of
+    # the sum for each of the at most 2^18 keys that share its worker.
+    big = torch.exp(6 * q[0, :, 0].double())
+    want = ((n - 1) / (n - 1 + big))[None, :, None].expand(seqs, heads, d)
+    u = torch.finfo(dtype).eps / 2
+    rel = u + 2.0 ** -11 + 20 * 2.0 ** -22 + 2.0 ** -20 + n / 32 * 2.0 ** -24
+    F.check(out, want, 1.01 * (rel * want + 2.0 ** (18 - 32)), "what is left beside the dominant key")
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d", [([700, 3, 1999, 64], 32, 8, 128), ([9000], 16, 2, 64),
+                                           ([150, 20, 90], 8, 2, 64), ([2500] * 40, 32, 2, 128)])
+def test_a_decode_repeats_itself(lens, hq, hkv, d):
+    # no order of work depends on timing: the same bits again, whatever ran in between
+    table, pools, scales = cache(lens, hkv, d, 16, 3)
+    q = torch.randn(len(lens), hq, d, generator=gen(4), device=DEV).bfloat16()
+    args = (*pools, table, i32(lens), *scales)
+    first, again = torch.empty_like(q), torch.empty_like(q)
+    pa.pa_decode_fp4(first, q, *args, scale=0.1, max_context_len=max(lens))
+    for _ in range(5):
+        pa.pa_decode_fp4(again, q.roll(1, 0), *args, scale=0.3, max_context_len=max(lens))
+        pa.pa_decode_fp4(again, q, *args, scale=0.1, max_context_len=max(lens))
+        assert torch.equal(first, again)
