@@ -115,6 +115,13 @@ __global__ void __launch_bounds__(256) gather_cache_fp4_kernel(const GatherArgs 
     }
     const uint8_t *tile = pool + (((static_cast<int64_t>(now) * p.num_kv_heads + h) << shift) +
                                   (t & ((1 << shift) - 1))) * TL::kBytes;
+    char *dst = out + 8 * static_cast<int64_t>(t) * stride;
+    const int n = min(8, len - 8 * t);
+    if (S == 0.f) {  // zeros, even where the pool's scales are NaN
+      for (int r = 0; r < n; ++r)
+        *reinterpret_cast<uint4 *>(dst + r * stride) = make_uint4(0, 0, 0, 0);
+      continue;
+    }
     // (all eight rows of a tile are the pool's, whatever the context ends at)
     uint32_t codes[8], scale[8];
 #pragma unroll
@@ -122,8 +129,6 @@ __global__ void __launch_bounds__(256) gather_cache_fp4_kernel(const GatherArgs 
       codes[r] = *reinterpret_cast<const uint32_t *>(tile + r * TL::kRowBytes + 4 * c);
       scale[r] = tile[TL::kScales + r * TL::kScaleBytes + c / 2];
     }
-    char *dst = out + 8 * static_cast<int64_t>(t) * stride;
-    const int n = len - 8 * t;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       if (r >= n) break;

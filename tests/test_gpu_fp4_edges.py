@@ -109,3 +109,19 @@ def test_a_decode_repeats_itself(lens, hq, hkv, d):
         pa.pa_decode_fp4(again, q.roll(1, 0), *args, scale=0.3, max_context_len=max(lens))
         pa.pa_decode_fp4(again, q, *args, scale=0.1, max_context_len=max(lens))
         assert torch.equal(first, again)
+
+
+# ------------------------------------------------------------------ gather --
+@pytest.mark.parametrize("dtype", BOTH)
+def test_an_unusable_head_scale_reads_zeros_whatever_the_pool_holds(dtype):
+    d, bs = 128, 16
+    pools = [F.new_pool(2, 3, bs, d) for _ in range(2)]  # NaN group scales everywhere
+    for bad in (0.0, float("nan"), float("inf"), -1.0, 2.0 ** -65, 2.0 ** 65):
+        S = torch.tensor([1.0, bad, 1.0], device=DEV)
+        out, err = torch.full((2, 40, 3, d), 7.0, dtype=dtype, device=DEV), new_err()
+        pa.pa_gather_cache_fp4(out[0], out[1], *pools, i32([[0, 1]]), i32([30]), i32([4]), S, S,
+                               max_context_len=32, d_error=err)
+        done(err, pa.DEVERR_SCALE)
+        assert bool((out[:, 4:34, 1] == 0).all())
+        assert bool(out[:, 4:34, ::2].isnan().all())
+        assert bool((out[:, :4] == 7).all()) and bool((out[:, 34:] == 7).all())
