@@ -588,11 +588,12 @@ pa_status pa_reshape_and_cache_fp4(const void *key, const void *value, int64_t k
  * pa_gather_cache_fp4 -- FP4 pools read back as 16-bit rows.
  *
  * Position j of sequence b, j < context_lens[b], goes to row row_starts[b] + j of
- * key_out and value_out, all heads, rounded once from its value.  A chunk of a
- * prompt over what an FP4 cache holds: write the chunk, gather, and attend with
- * pa_prefill_varlen, whose 16-bit pools the rows are where each start is a
- * multiple of its block size (block r of sequence b then starts at row
- * row_starts[b] + r * block_size).
+ * key_out and value_out, all heads, as code * scale (exact) times S, rounded to fp32
+ * and then to dtype: near a tie, for about one value in 10^5, that is not the nearest
+ * one but its neighbour.  A chunk of a prompt over what an FP4 cache holds: write the
+ * chunk, gather, and attend with pa_prefill_varlen, whose 16-bit pools the rows are
+ * where each start is a multiple of its block size (block r of sequence b then starts
+ * at row row_starts[b] + r * block_size).
  *
  *   key_out,
  *   value_out       [num_rows, num_kv_heads, head_dim] of dtype at their row

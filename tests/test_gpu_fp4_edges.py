@@ -125,3 +125,29 @@ def test_an_unusable_head_scale_reads_zeros_whatever_the_pool_holds(dtype):
         assert bool((out[:, 4:34, 1] == 0).all())
         assert bool(out[:, 4:34, ::2].isnan().all())
         assert bool((out[:, :4] == 7).all()) and bool((out[:, 34:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_rows_are_rounded_to_fp32_and_then_to_16_bits(dtype):
+    # every code under every group scale, under head scales near enough to ties that the
+    # two roundings are not one
+    d, bs, hkv = 64, 128, 1000
+    code = torch.arange(16, device=DEV).repeat(4).expand(128, hkv, d)
+    c = torch.arange(128, device=DEV).clamp(max=126)[:, None, None].expand(128, hkv, 4)
+    pool = F.new_pool(1, hkv, bs, d)
+    F.put(pool, torch.arange(128, device=DEV), code, c)
+    S = 0.001 + 0.002 * torch.rand(hkv, generator=gen(5), device=DEV)
+    S[:5] = torch.tensor([float.fromhex(x) for x in (
+        "0x1.13e8bap-9", "0x1.9305bp-10", "0x1.8d89d8p-10", "0x1.ce6668p-10", "0x1.a3b13cp-10")])
+    out, err = torch.empty(2, 128, hkv, d, dtype=dtype, device=DEV), new_err()
+    pa.pa_gather_cache_fp4(out[0], out[1], pool, pool, i32([[0]]), i32([128]), i32([0]), S, S,
+                           max_context_len=128, d_error=err)
+    done(err)
+    exact = F.values(code, c) * S.double()[:, None]
+    want = exact.float().to(dtype)
+    assert torch.equal(out[0], want) and torch.equal(out[1], want)
+    # the test would not tell the two apart without such values
+    step = (torch.nextafter(want, torch.full_like(want, float("inf"))).double(),
+            torch.nextafter(want, torch.full_like(want, float("-inf"))).double())
+    off = (want.double() - exact).abs()
+    assert bool(((step[0] - exact).abs() < off).any() | ((step[1] - exact).abs() < off).any())
