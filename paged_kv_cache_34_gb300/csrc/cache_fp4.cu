@@ -12,6 +12,7 @@
 //    once; the next token's values are on their way meanwhile.
 //  * Read: a thread holds eight elements of a head's row, so that rows are written in whole
 //    lines, and takes a tile of eight tokens at a time: one block id, eight rows on their way.
+//    CTAs have a sequence each, or, where lengths may be far apart, all sequences' tiles by turns.
 // Measured (16 prompts up to 2000 tokens, 32 KV heads of 128, bf16, 333 MB each way): write
 // 55 us, 6.0 TB/s; read 57 us, 5.8 TB/s, of the 6.75 of a copy; 162 us together with a
 // thread per group and token in both and the checked quotient throughout.
@@ -75,6 +76,41 @@ __global__ void __launch_bounds__(256, 4) reshape_and_cache_fp4_kernel(const Res
   }
 }
 
+// One tile's `n` rows of one 16-byte chunk: chunk c of head scale S, rows `stride` bytes apart.
+template <class E, int D>
+__device__ __forceinline__ void gather_tile(const uint8_t *tile, char *dst, int64_t stride, int n,
+                                            float S, int c) {
+  using TL = Tile<D>;
+  if (S == 0.f) {  // zeros, even where the pool's scales are NaN
+    for (int r = 0; r < n; ++r)
+      *reinterpret_cast<uint4 *>(dst + r * stride) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  // (all eight rows of a tile are the pool's, whatever the context ends at)
+  uint32_t codes[8], scale[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    codes[r] = *reinterpret_cast<const uint32_t *>(tile + r * TL::kRowBytes + 4 * c);
+    scale[r] = tile[TL::kScales + r * TL::kScaleBytes + c / 2];
+  }
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    if (r >= n) break;
+    uint32_t e[4], w[4];
+    widen8(codes[r], e[0], e[1], e[2], e[3]);
+    // code * scale is exact in fp16 (six bits); times S it is rounded to fp32, then to 16
+    const uint32_t f = e4m3_to_f16x2(scale[r] * 0x101u);
+    const __half2 s2 = *reinterpret_cast<const __half2 *>(&f);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&e[x]), s2);
+      const uint32_t z = *reinterpret_cast<const uint32_t *>(&y);
+      w[x] = E::pack2(F16::lo(z) * S, F16::hi(z) * S);
+    }
+    *reinterpret_cast<uint4 *>(dst + r * stride) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 // blockIdx.y: the sequence; blockIdx.z: which blockDim.x of the 2 Hkv D / 8 chunks of a row.
 template <class E, int D>
 __global__ void __launch_bounds__(256) gather_cache_fp4_kernel(const GatherArgs p) {
@@ -115,36 +151,100 @@ __global__ void __launch_bounds__(256) gather_cache_fp4_kernel(const GatherArgs 
     }
     const uint8_t *tile = pool + (((static_cast<int64_t>(now) * p.num_kv_heads + h) << shift) +
                                   (t & ((1 << shift) - 1))) * TL::kBytes;
-    char *dst = out + 8 * static_cast<int64_t>(t) * stride;
-    const int n = min(8, len - 8 * t);
-    if (S == 0.f) {  // zeros, even where the pool's scales are NaN
-      for (int r = 0; r < n; ++r)
-        *reinterpret_cast<uint4 *>(dst + r * stride) = make_uint4(0, 0, 0, 0);
-      continue;
+    gather_tile<E, D>(tile, out + 8 * static_cast<int64_t>(t) * stride, stride, min(8, len - 8 * t),
+                      S, c);
+  }
+}
+
+// The tiles of all sequences as one list, dealt out to the CTAs in turn.  A CTA goes through
+// the sequences kListSeqs at a time: their tiles are summed up, and those of its places that
+// fall among them are looked up by bisection.  blockIdx.y: which blockDim.x of a row's chunks;
+// where a CTA has room for several rows, that many tiles share a turn.
+constexpr int kListSeqs = 256;
+
+template <class E, int D>
+__global__ void __launch_bounds__(kListSeqs) gather_list_fp4_kernel(const GatherArgs p) {
+  using TL = Tile<D>;
+  constexpr int L = D / 8;
+  __shared__ int64_t s_sum[kListSeqs + 1];  // tiles ahead of each sequence
+  __shared__ int64_t s_warp[kListSeqs / 32];
+  __shared__ int s_len[kListSeqs], s_start[kListSeqs];
+  const int half = p.num_kv_heads * L, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int at_once = 2 * half < kListSeqs ? kListSeqs / (2 * half) : 1;
+  const int mine = at_once > 1 ? tid / (2 * half) : 0;
+  const int i = blockIdx.y * kListSeqs + tid - mine * 2 * half;
+  const bool value = i >= half, live = i < 2 * half && mine < at_once;
+  const int k = value ? i - half : i, h = k / L, c = k % L;
+  const bool report = blockIdx.x == 0 && blockIdx.y == 0;
+  griddep_wait();
+  griddep_launch_dependents();
+  float S = live ? __ldg((value ? p.v_scale : p.k_scale) + h) : 1.f;
+  const bool usable = head_scale_ok(S);
+  if (!usable) S = 0.f;
+  const uint8_t *pool = static_cast<const uint8_t *>(value ? p.value_cache : p.key_cache);
+  const int64_t stride = value ? p.v_stride_bytes : p.k_stride_bytes;
+  char *out = static_cast<char *>(value ? p.value_out : p.key_out) + 16 * k;
+  const int shift = 31 - __clz(p.block_size) - 3;  // (tiles a block: 2^shift)
+  if (tid == 0) s_sum[0] = 0;
+  int64_t at = static_cast<int64_t>(blockIdx.x) * at_once + mine;  // place in the list from here on
+  const int64_t step = static_cast<int64_t>(gridDim.x) * at_once;
+  int len = 0, start = 0;
+  auto fetch = [&](int b) {  // a thread's sequence of the next round
+    len = b < p.num_seqs ? __ldg(p.context_lens + b) : 0;
+    start = b < p.num_seqs ? __ldg(p.row_starts + b) : 0;
+  };
+  fetch(tid);
+  for (int base = 0; base < p.num_seqs; base += kListSeqs) {
+    int n = checked_context_len(len, p.capacity, p.max_context_len, p.d_error, report);
+    if (n > 0 && (start < 0 || start > p.num_rows - n)) {
+      if (report) raise_error(p.d_error, PA_DEVERR_CU_SEQLENS);
+      n = 0;
     }
-    // (all eight rows of a tile are the pool's, whatever the context ends at)
-    uint32_t codes[8], scale[8];
+    s_len[tid] = n;
+    s_start[tid] = start;
+    fetch(base + kListSeqs + tid);
+    int64_t sum = (n + 7) / 8;
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      codes[r] = *reinterpret_cast<const uint32_t *>(tile + r * TL::kRowBytes + 4 * c);
-      scale[r] = tile[TL::kScales + r * TL::kScaleBytes + c / 2];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
     }
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) sum += s_warp[w];
+    s_sum[tid + 1] = sum;
+    __syncthreads();
+    const int64_t total = s_sum[kListSeqs];
+    int q = 0, t = 0, id = 0;  // the place's sequence, its tile and its block
+    auto look = [&]() {
+      if (at >= total) return;
+      int lo = 0;
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      if (r >= n) break;
-      uint32_t e[4], w[4];
-      widen8(codes[r], e[0], e[1], e[2], e[3]);
-      // code * scale is exact in fp16 (six bits); times S it is rounded to fp32, then to 16
-      const uint32_t f = e4m3_to_f16x2(scale[r] * 0x101u);
-      const __half2 s2 = *reinterpret_cast<const __half2 *>(&f);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&e[x]), s2);
-        const uint32_t z = *reinterpret_cast<const uint32_t *>(&y);
-        w[x] = E::pack2(F16::lo(z) * S, F16::hi(z) * S);
+      for (int w = kListSeqs / 2; w > 0; w >>= 1)
+        if (s_sum[lo + w] <= at) lo += w;
+      q = lo;
+      t = static_cast<int>(at - s_sum[lo]);
+      id = __ldg(p.block_table + (base + lo) * p.block_table_stride + (t >> shift));
+    };
+    if (live) {
+      look();
+      while (at < total) {
+        const int now = id, tile = t, rows = s_len[q];
+        const int64_t row = s_start[q] + 8 * static_cast<int64_t>(t);
+        at += step;
+        look();
+        if (!usable) raise_error(p.d_error, PA_DEVERR_SCALE);
+        if (now < 0 || now >= p.num_blocks) {
+          if (i == 0) raise_error(p.d_error, PA_DEVERR_BLOCK_ID);
+          continue;
+        }
+        const int64_t place = (static_cast<int64_t>(now) * p.num_kv_heads + h) << shift;
+        gather_tile<E, D>(pool + (place + (tile & ((1 << shift) - 1))) * TL::kBytes,
+                          out + row * stride, stride, min(8, rows - 8 * tile), S, c);
       }
-      *reinterpret_cast<uint4 *>(dst + r * stride) = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    at -= total;
+    __syncthreads();  // everyone is done with the sums
   }
 }
 
@@ -178,6 +278,28 @@ cudaError_t launch_gather_cache_fp4(const GatherArgs &a, cudaStream_t stream) {
   int64_t x = (static_cast<int64_t>(a.num_sms) * (4096 / threads) + parts - 1) / parts;
   x = (x + a.num_seqs - 1) / a.num_seqs;
   if (x > tiles) x = tiles;
+  // Where a CTA may have more than eight tiles of its sequence to go through, lengths far
+  // apart would leave most of them idle behind one long context: all sequences' tiles as one
+  // list instead (each for itself / list, us, 8 heads of 128: one of 100000 among 127 of 100
+  // 760 / 98, among 1999 6050 / 256; one of 10000 among 31 of 100 21 / 13; but even lengths,
+  // 16 of 20000 267 / 269, 16 of 2000 with 32 heads, at most 6.6 tiles a CTA, 110 / 113, 64 of
+  // 10000 with 2 heads of 64, 4.1 tiles, 70.7 / 74).
+  if (a.num_seqs > 1 && tiles > 8 * x) {
+    // 16 CTAs an SM, four of them resident, where the lengths are one round of sums, else
+    // the resident ones alone (4 / 16: 16 of 20000 274 / 269, one of 100000 among 127 of 100
+    // 100 / 98; among 5000 of 64, 2 heads of 64, 58 / 98, one of 30000 among 40000 172 / 528).
+    const int per_sm = a.num_seqs <= fp4::kListSeqs ? 16 : 4;
+    const int lists = (per + fp4::kListSeqs - 1) / fp4::kListSeqs;
+    int64_t ctas = (static_cast<int64_t>(a.num_sms) * per_sm + lists - 1) / lists;
+    const int64_t places = a.num_rows / 8 + static_cast<int64_t>(a.num_seqs);  // tiles at most
+    if (ctas > places) ctas = places;
+    auto kernel = a.dtype == PA_BF16 ? (a.head_dim == 128 ? fp4::gather_list_fp4_kernel<BF16, 128>
+                                                          : fp4::gather_list_fp4_kernel<BF16, 64>)
+                                     : (a.head_dim == 128 ? fp4::gather_list_fp4_kernel<F16, 128>
+                                                          : fp4::gather_list_fp4_kernel<F16, 64>);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(lists)),
+                      dim3(fp4::kListSeqs), 0, stream, a);
+  }
   auto kernel = a.dtype == PA_BF16 ? (a.head_dim == 128 ? fp4::gather_cache_fp4_kernel<BF16, 128>
                                                         : fp4::gather_cache_fp4_kernel<BF16, 64>)
                                    : (a.head_dim == 128 ? fp4::gather_cache_fp4_kernel<F16, 128>

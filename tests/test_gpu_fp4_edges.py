@@ -57,6 +57,27 @@ def cache(lens, hkv, d, bs, seed):
     return table, pools, scales
 
 
+def device_us(call, calls=5):
+    """Device time of a call among others, the median of nine replays of a graph."""
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        for _ in range(calls):
+            call()
+    times = []
+    for _ in range(11):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(1000 * a.elapsed_time(b) / calls)
+    return sorted(times[2:])[4]
+
+
 # ----------------------------------------------------------------- weights --
 @pytest.mark.parametrize("dtype", BOTH)
 def test_weights_far_below_a_dominant_key(dtype):
@@ -151,3 +172,49 @@ def test_rows_are_rounded_to_fp32_and_then_to_16_bits(dtype):
             torch.nextafter(want, torch.full_like(want, float("-inf"))).double())
     off = (want.double() - exact).abs()
     assert bool(((step[0] - exact).abs() < off).any() | ((step[1] - exact).abs() < off).any())
+
+
+def gathered(lens, hkv, d, bs, dtype, seed, most=None):
+    """The gather of `lens` in another order than the sequences', checked exactly."""
+    table, pools, scales = cache(lens, hkv, d, bs, seed)
+    starts, r = [0] * len(lens), 1
+    for b in reversed(range(len(lens))):
+        starts[b] = r
+        r += lens[b] + b % 2
+    out, err = torch.full((2, r, hkv, d), 7.0, dtype=dtype, device=DEV), new_err()
+    args = (*pools, table, i32(lens), i32(starts), *scales)
+    most = most or max(lens)
+    pa.pa_gather_cache_fp4(out[0], out[1], *args, max_context_len=most, d_error=err)
+    done(err)
+    n = torch.tensor(lens, device=DEV)
+    seq = torch.repeat_interleave(torch.arange(len(lens), device=DEV), n)
+    j = torch.arange(seq.numel(), device=DEV) - (n.cumsum(0) - n)[seq]
+    slots = table[seq, j // bs].long() * bs + j % bs
+    at = torch.tensor(starts, device=DEV)[seq] + j
+    for o, pool, S in zip(out, pools, scales):
+        want = torch.full_like(o, 7.0)
+        for a in range(0, at.numel(), 1 << 15):
+            k = slice(a, a + (1 << 15))
+            v = F.values(*F.get(pool, slots[k], d)).float() * S[:, None]
+            want[at[k]] = v.to(dtype)
+        assert torch.equal(o, want)
+    return lambda: pa.pa_gather_cache_fp4(out[0], out[1], *args, max_context_len=most)
+
+
+@pytest.mark.parametrize("lens,hkv,d,bs,dtype", [
+    ([20000] + [3, 0, 17] * 40, 8, 128, 32, torch.float16),
+    ([5, 0, 30000, 9] * 2 + [1] * 250, 1, 64, 16, torch.bfloat16),
+    ([0] * 700 + [9000] + [33] * 1300, 2, 64, 8, torch.float16),
+    ([40] * 300 + [12000], 3, 128, 16, torch.bfloat16),
+    ([4000] + [1] * 90, 40, 128, 128, torch.bfloat16),
+    ([0] * 300, 8, 64, 8, torch.float16), ([2500] * 70, 5, 64, 64, torch.float16),
+])
+def test_gather_of_one_long_and_many_short(lens, hkv, d, bs, dtype):
+    gathered(lens if max(lens) else lens[:-1] + [1], hkv, d, bs, dtype, len(lens), most=40000)
+
+
+def test_gather_time_of_one_long_among_many():
+    # the work of 127 contexts of 100 tokens is an eighth of the long one's
+    alone = device_us(gathered([100000], 8, 128, 32, torch.bfloat16, 1))
+    among = device_us(gathered([100000] + [100] * 127, 8, 128, 32, torch.bfloat16, 1))
+    assert among < 2 * alone, f"{among:.0f} us beside {alone:.0f} us alone"
