@@ -212,14 +212,29 @@ constexpr int kFp4MostSeqs = 8192;       // prefix sums and lengths, 8 bytes eac
 constexpr int fp4_ctas_per_sm(int head_dim, int ng) {
   return head_dim == 128 ? 4 - ng : ng == 1 ? 4 : 3;
 }
+// Shared memory: the stages (keys and values, 4.5 bits an element), a barrier each, then
+// prefix sums and lengths.
+inline int fp4_decode_smem(int head_dim, int stages, int num_seqs) {
+  return kFp4Warps * stages * (kFp4StageTokens * head_dim * 9 / 8 + 8) + 4 * (2 * num_seqs + 1);
+}
+// CTAs of an SM by its 228 KB of shared memory, 1 KB of which is taken for each.
+inline int fp4_ctas_that_fit(int head_dim, int stages, int num_seqs) {
+  return 228 * 1024 / (fp4_decode_smem(head_dim, stages, num_seqs) + 1024);
+}
 // Stages of a worker's ring.  At 128 values two of them leave an SM's shared memory room
 // for three CTAs, three for two: fewer workers, most of their tokens on their way at once,
 // fewer states to join.  That is the better where the bound leaves those few workers 256
 // tokens or less (two / three, device us, 32/8 heads: 8 sequences of 100 to 2000 tokens
 // 11.4 / 10.0, 16 13.6 / 12.4, 16 of 2000 18.5 / 17.3; but 24 of 2000 20.6 / 22.2, 32 of 100
 // to 2000 18.5 / 19.3, 64 28.3 / 30.1; one of 30000, 64/8, 21.0 / 19.8, of 65000 27.1 / 27.9).
-inline int fp4_stages(int head_dim, int64_t t_max, int num_sms) {
-  return head_dim == 64 || t_max <= 256LL * 2 * kFp4Warps * num_sms ? 3 : 2;
+// From 628 sequences on their sums and lengths leave three stages one CTA only, two stages
+// two of them (two / three: 640 of 400 tokens, one KV head, 26.9 / 29.6, 700 28.8 / 33.2;
+// eight KV heads, 700 of 32 30.0 / 43.0, 1024 42.8 / 61.9).
+inline int fp4_stages(int head_dim, int num_seqs, int64_t t_max, int num_sms) {
+  if (head_dim == 64) return 3;
+  return t_max <= 256LL * 2 * kFp4Warps * num_sms && fp4_ctas_that_fit(head_dim, 3, num_seqs) >= 2
+             ? 3
+             : 2;
 }
 // Short contexts are not cut: no states, no second launch (cut / whole, device us: 4
 // sequences of 64 / 128 / 192 tokens, 8/2 heads of 64, 5.5 / 4.3, 5.7 / 5.3, 5.7 / 6.4; 32 of
@@ -228,18 +243,12 @@ inline int fp4_stages(int head_dim, int64_t t_max, int num_sms) {
 inline bool fp4_whole_units(int max_ctx, int64_t units) {
   return max_ctx > 0 && max_ctx <= (units < 128 ? 128 : 256);
 }
-// Shared memory: the stages (keys and values, 4.5 bits an element), a barrier each, then
-// prefix sums and lengths.
-inline int fp4_decode_smem(int head_dim, int stages, int num_seqs) {
-  return kFp4Warps * stages * (kFp4StageTokens * head_dim * 9 / 8 + 8) + 4 * (2 * num_seqs + 1);
-}
 inline DecodeBalance fp4_balance(int num_seqs, int units, int ng, int head_dim, int max_ctx,
                                  int num_sms) {
   DecodeBalance d;
   const int64_t t_max = static_cast<int64_t>(num_seqs) * units * ((max_ctx + 31) / 32) * 32;
-  d.stages = fp4_stages(head_dim, t_max, num_sms);
-  // CTAs that are resident at once: 1 KB of an SM's 228 is taken for each
-  int64_t most = 228 * 1024 / (fp4_decode_smem(head_dim, d.stages, num_seqs) + 1024);
+  d.stages = fp4_stages(head_dim, num_seqs, t_max, num_sms);
+  int64_t most = fp4_ctas_that_fit(head_dim, d.stages, num_seqs);  // resident at once
   if (most > fp4_ctas_per_sm(head_dim, ng)) most = fp4_ctas_per_sm(head_dim, ng);
   most *= num_sms;
   // A worker takes 32 tokens at least, and 64 where that leaves 768 workers or more: fewer

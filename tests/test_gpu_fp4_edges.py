@@ -57,6 +57,15 @@ def cache(lens, hkv, d, bs, seed):
     return table, pools, scales
 
 
+def slots_of(table, b, n, bs):
+    j = torch.arange(n, device=DEV)
+    return table[b].long()[j // bs] * bs + j % bs
+
+
+def rows64(pool, S, slots, d):
+    return F.values(*F.get(pool, slots, d)) * S.double()[:, None]
+
+
 def device_us(call, calls=5):
     """Device time of a call among others, the median of nine replays of a graph."""
     stream = torch.cuda.Stream()
@@ -218,3 +227,48 @@ def test_gather_time_of_one_long_among_many():
     alone = device_us(gathered([100000], 8, 128, 32, torch.bfloat16, 1))
     among = device_us(gathered([100000] + [100] * 127, 8, 128, 32, torch.bfloat16, 1))
     assert among < 2 * alone, f"{among:.0f} us beside {alone:.0f} us alone"
+
+
+# ------------------------------------------------------------------ decode --
+def decoded(lens, hq, hkv, d, bs, dtype, seed):
+    """The decode of `lens`, checked against 64 bits for some of its sequences."""
+    table, pools, scales = cache(lens, hkv, d, bs, seed)
+    q = torch.randn(len(lens), hq, d, generator=gen(seed + 1), device=DEV).to(dtype)
+    out, err = torch.full_like(q, float("nan")), new_err()
+    args = (*pools, table, i32(lens), *scales)
+    ws = torch.empty(pa.pa_decode_fp4_plan(len(lens), hq, hkv, d, max(lens)), dtype=torch.uint8,
+                     device=DEV)
+
+    def call(error=None):
+        pa.pa_decode_fp4(out, q, *args, scale=d ** -0.5, max_context_len=max(lens), workspace=ws,
+                         d_error=error)
+
+    call(err)
+    done(err)
+    assert bool(out.isfinite().all())
+    longest = sorted(range(len(lens)), key=lambda b: -lens[b])
+    grp = hq // hkv
+    for b in set(longest[:4] + longest[-4:] + [0, len(lens) - 1]):
+        if lens[b] == 0:
+            assert bool((out[b] == 0).all())
+            continue
+        slots = slots_of(table, b, lens[b], bs)
+        k, v = (rows64(pool, S, slots, d) for pool, S in zip(pools, scales))
+        for h in range(hkv):
+            r = slice(h * grp, (h + 1) * grp)
+            F.check(out[b, r], *F.attend(q[b, r], k[:, h], v[:, h], d ** -0.5), f"sequence {b}")
+    return call
+
+
+@pytest.mark.parametrize("n,most", [(600, 400), (640, 400), (700, 400), (1200, 200)])
+def test_many_sequences_leave_as_many_workers_as_fit(n, most):
+    # The plan's size says how many partial states a call may leave: one for each sequence's
+    # unit and worker.  Lengths and prefix sums, 8 bytes a sequence, leave room for two CTAs
+    # of four workers an SM beside rings of two stages up to thousands of sequences.  (Contexts
+    # that are not cut, up to 256 tokens, have no use for more workers than there are units:
+    # here one each.)
+    d, heads = 128, 8
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows = pa.pa_decode_fp4_plan(n, heads, 1, d, most) // (heads * (d + 2) * 4)
+    assert rows - n >= min(2 * 4 * sms - 1, n if most <= 256 else 1 << 30)
+    decoded([most, 0, 1, most // 2] * (n // 4), heads, 1, d, 16, torch.float16, n)
