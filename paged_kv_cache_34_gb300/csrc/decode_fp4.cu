@@ -601,31 +601,83 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(D, NG))
 
 // Joins the pieces of each (sequence, query head), their references m_i, sums l_i and
 // unnormalised outputs o_i: M = max m_i, w_i = 2^(m_i - M), out = sum w_i o_i / sum w_i l_i.
-// W warps per (sequence, query head), at least four a CTA; a lane holds D / 32 elements, warp
-// w of them takes pieces w, w + W, ..., eight at a time.
+// W warps per (sequence, query head), K a CTA; a lane holds D / 32 elements, warp w of them
+// takes pieces w, w + W, ..., eight at a time.  One long context among many short ones has most
+// of the pieces, in rows that follow one another: with SHARE a CTA's rows are gridDim.x apart,
+// and what is more than kJoinOwn pieces a warp is left to all of its warps together.
 constexpr int kJoinBatch = 8;
+constexpr int kJoinOwn = 16;
 // Up to so many sequences each warp sums the lengths up itself while the decode still runs,
 // instead of reading the sums that it leaves (128 of 400 to 700 tokens 33.0 against 33.2 us, 8
 // of 1500, 32/8 heads, 10.6 and 11.1; with 256 lengths a warp 39.7 against 39.4).
 constexpr int kJoinSums = 128;
 
-template <class E, int D, int W>
-__global__ void __launch_bounds__(W < 4 ? 128 : W * 32)
-    decode_fp4_join_kernel(const DecodeParams p) {
-  constexpr int V = D / 32, kRows = W < 4 ? 4 / W : 1;  // rows of a CTA
-  __shared__ float s_m[kRows * W], s_l[kRows * W], s_o[kRows * W][D];  // (used where W > 1)
-  const int first = threadIdx.x / 32 / W * W;  // the row's first warp
-  const int warp = (threadIdx.x >> 5) - first, lane = threadIdx.x & 31;
-  const int row = blockIdx.x * kRows + first / W;
-  if (row >= p.num_seqs * p.hq) return;
-  const int b = row / p.hq, h = row - b * p.hq;
+// A row's state: reference, sum and a lane's V = D / 32 elements.
+template <int V>
+struct JoinState {
+  float m = -INFINITY, l = 0.f, o[V] = {};
+};
+// Pieces first, first + step, ... of the n whose states start at workspace row row0.
+template <int D>
+__device__ __forceinline__ void join_pieces(const DecodeParams &p, int64_t row0, int n, int first,
+                                            int step, int lane, JoinState<D / 32> &t) {
+  constexpr int V = D / 32;
+  const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
+  for (int i0 = first; i0 < n; i0 += step * kJoinBatch) {
+    float2 st[kJoinBatch];
+    float ov[kJoinBatch][V];
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k) {
+      const int i = i0 + k * step;
+      const int64_t r = row0 + static_cast<int64_t>(i < n ? i : i0) * p.hs;
+      st[k] = i < n ? __ldcg(ml + r) : make_float2(-INFINITY, 0.f);
+      const float *src = p.ws_o + r * D + V * lane;
+      if constexpr (V == 4) {
+        const float4 x =
+            i < n ? __ldcg(reinterpret_cast<const float4 *>(src)) : make_float4(0, 0, 0, 0);
+        ov[k][0] = x.x, ov[k][1] = x.y, ov[k][2] = x.z, ov[k][3] = x.w;
+      } else {
+        const float2 x = i < n ? __ldcg(reinterpret_cast<const float2 *>(src)) : make_float2(0, 0);
+        ov[k][0] = x.x, ov[k][1] = x.y;
+      }
+    }
+    float m = t.m;
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k) m = fmaxf(m, st[k].x);
+    const float cr = m == -INFINITY ? 0.f : exp2f(t.m - m);
+    t.l *= cr;
+#pragma unroll
+    for (int v = 0; v < V; ++v) t.o[v] *= cr;
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k) {
+      // a piece that saw no key has sum 0 (a NaN query's: NaN, which stays)
+      const float w = st[k].x == -INFINITY ? 1.f : exp2f(st[k].x - m);
+      t.l += w * st[k].y;
+#pragma unroll
+      for (int v = 0; v < V; ++v) t.o[v] += w * ov[k][v];
+    }
+    t.m = m;
+  }
+}
+
+template <class E, int D, int W, int K, bool SHARE>
+__global__ void __launch_bounds__(K * 32) decode_fp4_join_kernel(const DecodeParams p) {
+  constexpr int V = D / 32, R = K / W;  // R rows a CTA
+  __shared__ float s_m[K], s_l[K], s_o[K][D];  // (used where warps share a row)
+  __shared__ int64_t s_row0[R];
+  __shared__ int s_n[R];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = warp / W, sub = warp % W;
+  const int rows = p.num_seqs * p.hq;
+  const int row = SHARE ? blockIdx.x + mine * gridDim.x : blockIdx.x * R + mine;
+  if (!SHARE && row >= rows) return;
+  const int b = row < rows ? row / p.hq : 0, h = row < rows ? row - b * p.hq : 0;
   const int kvh = h / p.group, hg = h - kvh * p.group, slc = hg / p.hs, g = kvh * p.nc + slc;
   // (context_lens is no output of the launch before: read, and for few sequences summed up,
   // while that runs)
   auto length = [&](int i) {
     return checked_context_len(__ldg(p.context_lens + i), p.capacity, p.max_ctx, p.err, false);
   };
-  const int L = length(b);
+  const int L = row < rows ? length(b) : 0;
   int total = 0, pref = 0;
   const bool sums = p.num_seqs <= kJoinSums;
   if (sums) {
@@ -639,82 +691,77 @@ __global__ void __launch_bounds__(W < 4 ? 128 : W * 32)
   }
   griddep_wait();
   griddep_launch_dependents();
-  if (L <= 0) return;
-  if (!sums) {
-    total = p.ws_pref[p.num_seqs];
-    pref = p.ws_pref[b];
+  int n = 0;
+  int64_t row0 = 0;
+  if (!SHARE && L <= 0) return;
+  if (L > 0) {
+    if (!sums) {
+      total = p.ws_pref[p.num_seqs];
+      pref = p.ws_pref[b];
+    }
+    const int U = pref + g * ceil32(L);
+    const int C = chunk_tokens(total, p.num_workers, p.chunk_cap);
+    const int c0 = U / C;
+    n = (U + ceil32(L) - 1) / C - c0 + 1;  // (one piece: written by the decode kernel itself)
+    row0 = (static_cast<int64_t>(b) * p.vh + g + c0) * p.hs + hg - slc * p.hs;
   }
-  const int U = pref + g * ceil32(L);
-  const int C = chunk_tokens(total, p.num_workers, p.chunk_cap);
-  const int c0 = U / C, n = (U + ceil32(L) - 1) / C - c0 + 1;
-  if (n <= 1) return;  // written by the decode kernel itself
-  const int64_t row0 = (static_cast<int64_t>(b) * p.vh + g + c0) * p.hs + hg - slc * p.hs;
-  const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
-  float M = -INFINITY, l = 0.f, acc[V] = {};
-  for (int i0 = warp; i0 < n; i0 += W * kJoinBatch) {
-    float2 st[kJoinBatch];
-    float ov[kJoinBatch][V];
+  auto leave = [&](const JoinState<V> &t) {
+    s_m[warp] = t.m;
+    s_l[warp] = t.l;
 #pragma unroll
-    for (int k = 0; k < kJoinBatch; ++k) {
-      const int i = i0 + k * W;
-      const int64_t r = row0 + static_cast<int64_t>(i < n ? i : i0) * p.hs;
-      st[k] = i < n ? __ldcg(ml + r) : make_float2(-INFINITY, 0.f);
-      const float *src = p.ws_o + r * D + V * lane;
-      if constexpr (V == 4) {
-        const float4 x =
-            i < n ? __ldcg(reinterpret_cast<const float4 *>(src)) : make_float4(0, 0, 0, 0);
-        ov[k][0] = x.x, ov[k][1] = x.y, ov[k][2] = x.z, ov[k][3] = x.w;
-      } else {
-        const float2 x = i < n ? __ldcg(reinterpret_cast<const float2 *>(src)) : make_float2(0, 0);
-        ov[k][0] = x.x, ov[k][1] = x.y;
-      }
+    for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = t.o[v];
+  };
+  auto collect = [&](int first, auto warps) {
+    constexpr int count = decltype(warps)::value;
+    JoinState<V> t;
+#pragma unroll
+    for (int w = 0; w < count; ++w) t.m = fmaxf(t.m, s_m[first + w]);
+#pragma unroll
+    for (int w = 0; w < count; ++w) {
+      const float f = s_m[first + w] == -INFINITY ? 1.f : exp2f(s_m[first + w] - t.m);
+      t.l += f * s_l[first + w];
+#pragma unroll
+      for (int v = 0; v < V; ++v) t.o[v] += f * s_o[first + w][lane * V + v];
     }
-    float Mn = M;
+    return t;
+  };
+  auto store = [&](int to, const JoinState<V> &t) {
+    const int q = to / p.hq;
+    const float inv = t.l == 0.f ? 0.f : 1.f / t.l;
+    typename E::T *dst = static_cast<typename E::T *>(p.out) + q * p.out_row_stride +
+                         (to - q * p.hq) * D + lane * V;
 #pragma unroll
-    for (int k = 0; k < kJoinBatch; ++k) Mn = fmaxf(Mn, st[k].x);
-    const float cr = Mn == -INFINITY ? 0.f : exp2f(M - Mn);
-    l *= cr;
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] *= cr;
-#pragma unroll
-    for (int k = 0; k < kJoinBatch; ++k) {
-      // a piece that saw no key has sum 0 (a NaN query's: NaN, which stays)
-      const float w = st[k].x == -INFINITY ? 1.f : exp2f(st[k].x - Mn);
-      l += w * st[k].y;
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += w * ov[k][v];
-    }
-    M = Mn;
+    for (int v = 0; v < V; v += 2)
+      *reinterpret_cast<uint32_t *>(dst + v) = E::pack2(t.o[v] * inv, t.o[v + 1] * inv);
+  };
+  if (!SHARE && n <= 1) return;
+  const bool joint = SHARE && n > kJoinOwn * W;
+  if (SHARE && sub == 0 && lane == 0) {
+    s_n[mine] = joint ? n : 0;
+    s_row0[mine] = row0;
   }
-  if constexpr (W > 1) {
-    if (lane == 0) {
-      s_m[first + warp] = M;
-      s_l[first + warp] = l;
+  if (n > 1 && !joint) {
+    JoinState<V> t;
+    join_pieces<D>(p, row0, n, sub, W, lane, t);
+    if constexpr (W > 1) {
+      leave(t);
+      asm volatile("bar.sync %0, %1;" ::"r"(mine + SHARE), "n"(32 * W) : "memory");
+      if (sub == 0) t = collect(warp, std::integral_constant<int, W>{});
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) s_o[first + warp][lane * V + v] = acc[v];
-    asm volatile("bar.sync %0, %1;" ::"r"(first / W), "n"(32 * W) : "memory");
-    if (warp != 0) return;
-    M = -INFINITY;
-    l = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) M = fmaxf(M, s_m[first + w]);
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float f = s_m[first + w] == -INFINITY ? 1.f : exp2f(s_m[first + w] - M);
-      l += f * s_l[first + w];
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += f * s_o[first + w][lane * V + v];
+    if (sub == 0) store(row, t);
+  }
+  if constexpr (SHARE) {
+    __syncthreads();
+    for (int r = 0; r < R; ++r) {
+      if (s_n[r] == 0) continue;
+      JoinState<V> t;
+      join_pieces<D>(p, s_row0[r], s_n[r], warp, K, lane, t);
+      leave(t);
+      __syncthreads();
+      if (warp == 0) store(blockIdx.x + r * gridDim.x, collect(0, std::integral_constant<int, K>{}));
+      __syncthreads();
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  typename E::T *dst =
-      static_cast<typename E::T *>(p.out) + b * p.out_row_stride + h * D + lane * V;
-#pragma unroll
-  for (int v = 0; v < V; v += 2)
-    *reinterpret_cast<uint32_t *>(dst + v) = E::pack2(acc[v] * inv, acc[v + 1] * inv);
 }
 
 template <class E, int D, int NG>
@@ -736,15 +783,30 @@ cudaError_t launch(const DecodeArgs &a, const DecodeParams &p, int stages, cudaS
   // 32000 to 131000, 64/8) 96.1, 89.2, 86.6, 85.6; 64, 228 (30000, 64/8) 46, 32, 24.4, 21.0).
   const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
   const int64_t units = static_cast<int64_t>(a.num_seqs) * p.vh;
-  auto join = [&](auto kernel, int per_row) {
-    const int per_cta = per_row < 4 ? 4 / per_row : 1;
+  // The most pieces that a row can have decide whether a CTA's rows lie apart and its warps
+  // share the long ones among them (one warp a row each for itself / four warps share / eight;
+  // 64/8 heads: one of 131072 among 31 of 100 82 / 58 / 54, of 20000 among 40 47 / 24 / 20, of
+  // 5000 among 80 26 / 19 / 20; but even lengths, 32 of 8000, 128/8, 82.5 / 82.4 / 84.7, 32 of
+  // 5000, 64/8 heads of 64, 31.1 / 31.7 / 31.9, 64 of 8000, 32/8, 109 / 109 / 109; two
+  // warps a row, one of 20000 among 24 26.6 / - / 19.5, 20 of 9000 49.9 / - / 48.4; four warps a
+  // row keep to themselves: sharing by eight 25.4 -> 20.8 with one of 20000 among 12, but 16 of
+  // 9000 41.1 -> 42.9).
+  const int64_t by_length = (a.max_context_len + 31) / 32 + 1, by_worker = p.num_workers / p.vh + 2;
+  const int64_t longest = by_length < by_worker ? by_length : by_worker;
+  auto join = [&](auto kernel, int per_row, int warps) {
+    const int per_cta = warps / per_row;
     return launch_pdl(kernel, dim3(static_cast<unsigned>((rows + per_cta - 1) / per_cta)),
-                      dim3(32 * per_row * per_cta), 0, stream, p);
+                      dim3(32 * warps), 0, stream, p);
   };
-  if (rows >= 2048) return join(decode_fp4_join_kernel<E, D, 1>, 1);
-  if (p.num_workers > 48 * units) return join(decode_fp4_join_kernel<E, D, 16>, 16);
-  if (p.num_workers > 12 * units) return join(decode_fp4_join_kernel<E, D, 4>, 4);
-  return join(decode_fp4_join_kernel<E, D, 2>, 2);
+  if (rows >= 2048)
+    return longest <= 64    ? join(decode_fp4_join_kernel<E, D, 1, 4, false>, 1, 4)
+           : longest <= 192 ? join(decode_fp4_join_kernel<E, D, 1, 4, true>, 1, 4)
+                            : join(decode_fp4_join_kernel<E, D, 1, 8, true>, 1, 8);
+  if (p.num_workers > 48 * units) return join(decode_fp4_join_kernel<E, D, 16, 16, false>, 16, 16);
+  if (p.num_workers > 12 * units) return join(decode_fp4_join_kernel<E, D, 4, 4, false>, 4, 4);
+  return longest <= 64    ? join(decode_fp4_join_kernel<E, D, 2, 4, false>, 2, 4)
+         : longest <= 192 ? join(decode_fp4_join_kernel<E, D, 2, 4, true>, 2, 4)
+                          : join(decode_fp4_join_kernel<E, D, 2, 8, true>, 2, 8);
 }
 
 template <class E>

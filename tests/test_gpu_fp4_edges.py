@@ -260,6 +260,27 @@ def decoded(lens, hq, hkv, d, bs, dtype, seed):
     return call
 
 
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("lens,hq,hkv,d,bs", [
+    ([60000] + [100] * 31, 64, 8, 128, 64), ([3, 30000, 0, 200] * 16, 32, 8, 128, 32),
+    ([200] * 255 + [40000], 32, 8, 64, 16), ([300] * 64 + [0] * 3 + [20000, 50], 32, 32, 64, 32),
+    ([50000] + [200] * 15, 64, 8, 128, 128), ([30000, 30000] + [257] * 130, 128, 8, 64, 128),
+    ([25000] + [40] * 180, 12, 4, 128, 8), ([100000, 700] + [30] * 40, 7, 7, 64, 16),
+])
+def test_decode_of_one_long_and_many_short(lens, hq, hkv, d, bs, dtype):
+    decoded(lens, hq, hkv, d, bs, dtype, len(lens))
+
+
+@pytest.mark.parametrize("short,n", [(100, 31), (200, 255)])
+def test_decode_time_of_one_long_among_many(short, n):
+    # the short ones are 2 % and 51 % of the long one's work
+    alone = device_us(decoded([100000], 64, 8, 128, 128, torch.bfloat16, 1))
+    others = device_us(decoded([short] * n, 64, 8, 128, 128, torch.bfloat16, 1))
+    among = device_us(decoded([100000] + [short] * n, 64, 8, 128, 128, torch.bfloat16, 1))
+    assert among < 1.15 * (alone + others), \
+        f"{among:.0f} us; {alone:.0f} us alone, the others {others:.0f}"
+
+
 @pytest.mark.parametrize("n,most", [(600, 400), (640, 400), (700, 400), (1200, 200)])
 def test_many_sequences_leave_as_many_workers_as_fit(n, most):
     # The plan's size says how many partial states a call may leave: one for each sequence's
