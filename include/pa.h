@@ -185,7 +185,8 @@ pa_status pa_reshape_and_cache(const void *key, const void *value,
  *   slot_mapping all NULL: nothing is written to a cache (then key_out is
  *                required, and value, block_size and num_blocks are not used).
  * Outputs may not overlap inputs or each other otherwise (PA_ERR_SHAPE); columns
- * of one buffer's rows side by side are no overlap.  The pools lie apart from all
+ * of one buffer's rows side by side are no overlap, but positions, cos_sin, the weights
+ * and slot_mapping lie outside all rows' span.  The pools lie apart from all
  * of them (not checked).  Over the other pools' formats the same takes two calls: this
  * one without a cache, in place, then the format's write.
  * The sum of a row's squares has to stay within fp32.

@@ -339,6 +339,30 @@ pa_status pa_rope_and_cache(void *query_out, int64_t q_out_row_stride, void *key
       !apart(k_in, q_o, false) || !apart(v_in, q_o, false) || !apart(v_in, k_o, false) ||
       !apart(q_o, k_o, false))
     return PA_ERR_SHAPE;
+  // the other inputs, wherever they lie between the first and the last byte of the rows written
+  struct Range {
+    const void *p;
+    uint64_t bytes;
+  };
+  const uint64_t n = num_tokens, weight = 2ull * head_dim;
+  const uint64_t most_table = UINT64_MAX / 4 / (rot_dim ? rot_dim : 1);
+  const Range other[] = {{positions, rot_dim ? 4 * n : 0},
+                         {cos_sin, 4 * static_cast<uint64_t>(rot_dim) *
+                                       (static_cast<uint64_t>(max_position) < most_table
+                                            ? static_cast<uint64_t>(max_position)
+                                            : most_table)},
+                         {q_weight, q_weight ? weight : 0},
+                         {k_weight, k_weight ? weight : 0},
+                         {slot_mapping, cache ? 8 * n : 0}};
+  for (const Rows &x : {q_o, k_o}) {
+    if (!x.p) continue;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(x.p);
+    const uintptr_t e = b + 2 * (last * x.stride + x.row);
+    for (const Range &y : other) {
+      const uintptr_t c = reinterpret_cast<uintptr_t>(y.p);
+      if (y.bytes > 0 && c < e && (b < c || b - c < y.bytes)) return PA_ERR_SHAPE;
+    }
+  }
   pa::RopeArgs a;
   a.query_out = query_out;
   a.key_out = key_out;
