@@ -230,7 +230,12 @@ def _rope(what, query_out, key_out, query, key, value, key_cache, value_cache, s
         if key_out.get_device() != dev:
             _bad_device("key_out", dev)
         kos, ko = _row(key_out, d, "key_out"), key_out.data_ptr()
-    if key_cache is not None:
+    if key_cache is None or value_cache is None or slot_mapping is None:
+        if not (key_cache is None and value_cache is None and slot_mapping is None):
+            raise ValueError("caches and slot_mapping must be given together")
+    else:
+        if value is None:
+            raise ValueError("value must be given with the caches")
         cshape = key_cache.shape
         nb, bs, hc, dc = cshape
         if value.shape != kshape or value.dtype is not dtype or _row(value, d, "value") != ks:
@@ -249,6 +254,8 @@ def _rope(what, query_out, key_out, query, key, value, key_cache, value_cache, s
         v, kc, vc = value.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr()
         sm = slot_mapping.data_ptr()
     if cos_sin is not None:
+        if positions is None:
+            raise ValueError("positions must be given with cos_sin")
         if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be a contiguous float32 tensor [max_position, rot_dim]")
         if cos_sin.get_device() != dev:

@@ -31,3 +31,21 @@ def test_other_inputs_beside_the_rows_written(lib, kw):  # noqa: F811
     if torch.cuda.is_available():
         pytest.skip("these pointers are none")
     assert call(lib, **kw) == 6
+
+
+def test_python_caches_and_slots_come_together():
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)  # noqa: E731
+    good = [z(3, 8, 64), z(3, 8, 64), z(3, 2, 64), z(3, 2, 64), z(9, 16, 2, 64), z(9, 16, 2, 64),
+            z(3, dt=torch.int64), z(3, dt=torch.int32), z(50, 64, dt=torch.float32)]
+    for gone, text in (((4,), "given together"), ((5,), "given together"), ((6,), "given together"),
+                       ((4, 5), "given together"), ((4, 6), "given together"),
+                       ((5, 6), "given together"), ((3,), "value must be given"),
+                       ((7,), "positions must be given")):
+        args = [None if n in gone else t for n, t in enumerate(good)]
+        with pytest.raises(ValueError, match=text):
+            pa.pa_rope_and_cache(*args, key_out=z(3, 2, 64))
+    # none of them: no cache write; no table: no rotation, and no positions
+    for gone in ((3, 4, 5, 6), (4, 5, 6), (7, 8), (8,)):
+        args = [None if n in gone else t for n, t in enumerate(good)]
+        with pytest.raises(ValueError, match="current CUDA device"):
+            pa.pa_rope_and_cache(*args, key_out=z(3, 2, 64))
