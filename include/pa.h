@@ -631,7 +631,8 @@ pa_status pa_gather_cache_fp4(void *key_out, int64_t k_out_row_stride, void *val
  * without its partition size.  The workspace (256-byte aligned) is of
  * pa_decode_fp4_plan's size for the same shape; calls that may run at the same
  * time need one each.
- * Supported: any num_q_heads % num_kv_heads == 0; up to 8192 sequences;
+ * Supported: any num_q_heads % num_kv_heads == 0 with num_q_heads * head_dim < 2^31
+ * (as in every decode); up to 8192 sequences;
  * num_seqs * num_kv_heads * max_context_len < 2^30 (lengths rounded up to 32; a
  * GQA group of more than 16 heads counts once per 16).  The plan refuses what
  * the call would refuse for it.

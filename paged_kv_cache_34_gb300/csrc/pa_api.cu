@@ -583,6 +583,8 @@ pa_status check_decode(void *out, int64_t out_row_stride, const void *query, int
   if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
   if (!valid_block_size(block_size)) return PA_ERR_UNSUPPORTED;
   if (num_blocks * block_size > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  // elements within a query's row are 32-bit
+  if (static_cast<int64_t>(num_q_heads) * head_dim > INT32_MAX) return PA_ERR_UNSUPPORTED;
   if (partition_size % pa::kDecodeSub != 0) return PA_ERR_SHAPE;
   setup->empty = num_seqs == 0;
   if (num_seqs == 0) return PA_OK;
@@ -1241,7 +1243,8 @@ pa_status fp4_plan(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, 
   if (static_cast<int64_t>(max_context_len) > (1 << 30) ||
       (num_seqs > 0 &&
        units * ((max_context_len + 31) / 32) * 32 > ((1LL << 30) - 1) / num_seqs) ||
-      num_seqs > pa::kFp4MostSeqs || num_kv_heads > 65536)
+      num_seqs > pa::kFp4MostSeqs || num_kv_heads > 65536 ||
+      static_cast<int64_t>(num_q_heads) * head_dim > INT32_MAX)
     return PA_ERR_UNSUPPORTED;
   const cudaError_t e = current_num_sms(sms);
   if (e != cudaSuccess) return cuda_fail(e);
