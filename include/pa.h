@@ -104,7 +104,8 @@ typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1 } pa_dtype;
 #define PA_DEVERR_CU_SEQLENS 4 /* cu_seqlens not a prefix sum of the batch    */
 #define PA_DEVERR_CONTEXT 8    /* context_len < 0, > capacity or > host hint  */
 #define PA_DEVERR_TIMEOUT 16   /* a bounded pipeline wait gave up             */
-#define PA_DEVERR_SCALE 32     /* an 8-bit pool's scale not positive finite   */
+#define PA_DEVERR_SCALE 32     /* an 8-bit pool's scale not positive finite, a
+                                  4-bit pool's not between 2^-64 and 2^64    */
 #define PA_DEVERR_NO_BLOCKS 64 /* the free list is too short for the step     */
 #define PA_DEVERR_POSITION 128 /* a position outside the rotation's table      */
 

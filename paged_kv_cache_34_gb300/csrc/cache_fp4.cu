@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(kListSeqs) gather_list_fp4_kernel(const Gather
   griddep_wait();
   griddep_launch_dependents();
   float S = live ? __ldg((value ? p.v_scale : p.k_scale) + h) : 1.f;
-  const bool usable = head_scale_ok(S);
-  if (!usable) S = 0.f;
+  bool tell = !head_scale_ok(S);  // once
+  if (tell) S = 0.f;
   const uint8_t *pool = static_cast<const uint8_t *>(value ? p.value_cache : p.key_cache);
   const int64_t stride = value ? p.v_stride_bytes : p.k_stride_bytes;
   char *out = static_cast<char *>(value ? p.value_out : p.key_out) + 16 * k;
@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(kListSeqs) gather_list_fp4_kernel(const Gather
         const int64_t row = s_start[q] + 8 * static_cast<int64_t>(t);
         at += step;
         look();
-        if (!usable) raise_error(p.d_error, PA_DEVERR_SCALE);
+        if (tell) raise_error(p.d_error, PA_DEVERR_SCALE);
+        tell = false;
         if (now < 0 || now >= p.num_blocks) {
           if (i == 0) raise_error(p.d_error, PA_DEVERR_BLOCK_ID);
           continue;

@@ -226,10 +226,10 @@ template <class E, int D>
 cudaError_t launch(const RopeArgs &a, cudaStream_t stream) {
   constexpr int L = D / 16;
   // Where every token has a CTA at once, wide CTAs take its rows in one round; beyond
-  // that, narrow ones keep more rounds' loads in flight (32/8 heads, norms, up to 512
-  // and up to 128 threads, measured with scalar arithmetic: 32 tokens 2.4 and 3.6 us,
-  // 304 3.1 and 4.0, 456 5.1 and 4.2, 2432 21.2 and 13.9, 16700 122 and 76.5; up to 64
-  // threads 76.1 and 13.3, but 456 6.4).
+  // that, narrow ones keep more rounds' loads in flight (device us, 32/8 heads of 128, norms,
+  // up to 512 and up to 128 threads: 32 tokens 2.4 and 2.7, 304 3.1 and 3.5, 380 4.5 and
+  // 3.8, 456 4.5 and 3.8, 2432 13.6 and 10.8, 16700 103 and 70; without norms 304 2.6 and
+  // 2.9, 380 3.7 and 3.1; up to 64 threads 68.8 and 10.0, but 456 4.8).
   const int rows = a.num_q_heads + a.num_kv_heads * (a.key_cache ? 2 : 1);
   const bool wide = a.num_tokens <= 2 * a.num_sms;
   const int widest = wide ? 512 : 128;
