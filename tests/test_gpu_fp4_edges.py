@@ -293,3 +293,90 @@ def test_many_sequences_leave_as_many_workers_as_fit(n, most):
     rows = pa.pa_decode_fp4_plan(n, heads, 1, d, most) // (heads * (d + 2) * 4)
     assert rows - n >= min(2 * 4 * sms - 1, n if most <= 256 else 1 << 30)
     decoded([most, 0, 1, most // 2] * (n // 4), heads, 1, d, 16, torch.float16, n)
+
+
+# --------------------------------------------------------- errors in builds --
+def test_gather_of_uneven_lengths_skips_what_is_wrong():
+    # as for even lengths: bad lengths, rows and blocks cost their own part only, whichever
+    # round of sequences they are in, and a bad scale leaves zeros
+    n, d, hkv, bs = 600, 64, 2, 8
+    lens = [20] * n
+    lens[300] = 5000
+    table, pools, scales = cache(lens, hkv, d, bs, 21)
+    starts = [0] * n
+    for b in range(1, n):
+        starts[b] = starts[b - 1] + lens[b - 1]
+    rows = starts[-1] + lens[-1]
+    bad_len, bad_rows, bad_block = {0: -3, 299: 5001, 520: 1 << 30}, {1: -1, 255: rows, 599: rows - 19}, \
+        {2: (1, 1 << 30), 300: (400, -1), 512: (0, pools[0].shape[0])}
+    out, err = torch.full((2, rows, hkv, d), 7.0, dtype=torch.float16, device=DEV), new_err()
+    ctx, at, ids = list(lens), list(starts), table.clone()
+    for b, v in bad_len.items():
+        ctx[b] = v
+    for b, v in bad_rows.items():
+        at[b] = v
+    for b, (block, v) in bad_block.items():
+        ids[b, block] = v
+    scales[1][1] = 0.0
+    pa.pa_gather_cache_fp4(out[0], out[1], *pools, ids, i32(ctx), i32(at), *scales,
+                           max_context_len=5000, d_error=err)
+    done(err, pa.DEVERR_CONTEXT | pa.DEVERR_CU_SEQLENS | pa.DEVERR_BLOCK_ID | pa.DEVERR_SCALE)
+    want = torch.full_like(out, 7.0)
+    for b in range(n):
+        if b in bad_len or b in bad_rows:
+            continue
+        slots, to = slots_of(table, b, lens[b], bs), torch.arange(lens[b], device=DEV)
+        if b in bad_block:
+            keep = to // bs != bad_block[b][0]
+            slots, to = slots[keep], to[keep]
+        for o, pool, S in zip(want, pools, scales):
+            o[starts[b] + to] = (F.values(*F.get(pool, slots, d)).float() * S[:, None]).half()
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("lens,hq,hkv,d", [
+    ([100] * 40 + [30000] + [100] * 30, 32, 32, 128), ([60] * 20 + [20000] + [200] * 20, 64, 8, 128),
+    ([20000] + [100] * 40, 16, 16, 128), ([50] * 30 + [40000, 9], 14, 7, 64),
+])
+def test_long_rows_keep_errors_and_nan_to_themselves(lens, hq, hkv, d, dtype):
+    # the long context's rows are joined by several warps; a NaN query, a bad block and a bad
+    # scale stay in their own rows
+    bs, long = 16, max(range(len(lens)), key=lambda b: lens[b])
+    table, pools, scales = cache(lens, hkv, d, bs, 31)
+    q = torch.randn(len(lens), hq, d, generator=gen(32), device=DEV).to(dtype)
+    args = dict(scale=d ** -0.5, max_context_len=max(lens))
+    clean = torch.empty_like(q)
+    pa.pa_decode_fp4(clean, q, *pools, table, i32(lens), *scales, **args)
+    slots = slots_of(table, long, lens[long], bs)
+    grp = hq // hkv
+    for h in (0, hkv - 1):
+        k, v = (rows64(pool, S, slots, d)[:, h] for pool, S in zip(pools, scales))
+        r = slice(h * grp, (h + 1) * grp)
+        F.check(clean[long, r], *F.attend(q[long, r], k, v, d ** -0.5), f"head {h}")
+    bits = clean.view(torch.int16)
+    # NaN in one query head of the long context
+    qn, out, err = q.clone(), torch.empty_like(q), new_err()
+    qn[long, hq - 1, 3] = float("nan")
+    pa.pa_decode_fp4(out, qn, *pools, table, i32(lens), *scales, d_error=err, **args)
+    done(err)
+    assert bool(out[long, hq - 1].isnan().all())
+    out[long, hq - 1] = clean[long, hq - 1]
+    assert torch.equal(out.view(torch.int16), bits)
+    # a block of the long context: finite, and the others as they were
+    ids = table.clone()
+    ids[long, 7] = pools[0].shape[0]
+    pa.pa_decode_fp4(out, q, *pools, ids, i32(lens), *scales, d_error=err, **args)
+    done(err, pa.DEVERR_BLOCK_ID)
+    assert bool(out[long].isfinite().all())
+    out[long] = clean[long]
+    assert torch.equal(out.view(torch.int16), bits)
+    # one head's scale
+    err.zero_()
+    bad = scales[0].clone()
+    bad[hkv - 1] = float("inf")
+    pa.pa_decode_fp4(out, q, *pools, table, i32(lens), bad, scales[1], d_error=err, **args)
+    done(err, pa.DEVERR_SCALE)
+    assert bool((out[:, hq - grp:] == 0).all())
+    out[:, hq - grp:] = clean[:, hq - grp:]
+    assert torch.equal(out.view(torch.int16), bits)
